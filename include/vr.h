@@ -334,6 +334,103 @@ VR_API vrResult_t vrRedOpCreatePreMulSum(vrRedOp_t* op, const void* scalar, vrDa
  * for anything else. Calls already enqueued keep the scalar they were given. */
 VR_API vrResult_t vrRedOpDestroy(vrRedOp_t op, vrComm_t comm);
 
+/* ---- The operators of a data-parallel training step around the AllReduce.
+ * Layer norm, whose backward pass sums the parameters' gradients over a
+ * rank's rows (what the rank hands to the AllReduce), and the norm of a list
+ * of gradients with clipping by it (what follows the AllReduce). They have no
+ * communicator and keep nothing between calls: calls on different streams,
+ * with workspaces of their own, may overlap. They are asynchronous on `stream`
+ * like vrAllReduce, allocate nothing, may be captured in a CUDA graph (the
+ * pointers and sizes are then those of the capture), and run on the device
+ * that is current. Sums are held in 32 bits or more and added up in a fixed
+ * order (no atomics), so equal calls give equal bits; each result is rounded
+ * once to its type. The pages have no counterpart of them.
+ * Common errors: vrInvalidArgument for a NULL or misaligned pointer (to the
+ * element size; workspaces to 16 bytes), a type, size or stride outside what
+ * is stated, a short workspace, or buffers that overlap where that is not
+ * allowed; vrCudaError if a launch fails. Nothing is enqueued then. */
+
+/* Layer norm over the last axis: for each row of `cols` elements
+ *   m = sum(x) / cols,  v = sum((x - m)^2) / cols,  r = 1 / sqrt(v + eps),
+ *   y = (x - m) r weight + bias.
+ *  x, y     [device] rows x cols of `dtype`; row i starts xStride (yStride)
+ *           elements after row i - 1, strides >= cols; y's elements between
+ *           cols and yStride are not written. y == x with equal strides is
+ *           allowed, other overlaps are not.
+ *  weight, bias  [device] cols elements of weightType each; NULL: ones, zeros.
+ *  mean, rstd    [device] m and r of each row, for the backward pass; NULL:
+ *           not written (inference).
+ *  rows     0 returns vrSuccess and launches nothing.  cols >= 1.
+ *  eps      >= 0, finite.
+ *  dtype    vrFloat16, vrBfloat16 or vrFloat32; weightType: dtype or
+ *           vrFloat32.
+ * A NaN or infinity makes its own row NaN and no other. Every alignment and
+ * stride works; rows that start on 16-byte boundaries are the fastest. */
+VR_API vrResult_t vrLayerNormForward(const void* x, const void* weight, const void* bias, void* y,
+                                     float* mean, float* rstd, size_t rows, size_t cols,
+                                     size_t xStride, size_t yStride, float eps,
+                                     vrDataType_t dtype, vrDataType_t weightType, void* stream);
+
+/* Workspace bytes of vrLayerNormBackward for these sizes, for any strides,
+ * alignments and weightType. Host only. */
+VR_API vrResult_t vrLayerNormBackwardWorkspace(size_t rows, size_t cols, vrDataType_t dtype,
+                                               size_t* bytes);
+
+/* The backward pass of vrLayerNormForward: with u = (x - m) r, g = dy weight,
+ *   dx = r (g - sum(g) / cols - u sum(g u) / cols)      for each row,
+ *   dweight = sum over the rows of dy u,  dbias = sum over the rows of dy.
+ *  dy, x, dx     [device] rows x cols of `dtype`, with row strides; dx may be
+ *           NULL (only the parameters' gradients) and overlaps neither dy nor x.
+ *  weight   as in the forward pass, NULL: ones.
+ *  mean, rstd    [device] as the forward pass wrote them.
+ *  dweight, dbias  [device] cols elements of weightType, overwritten; NULL:
+ *           not wanted. With rows == 0 they become zeros.
+ *  workspace     [device] 16-byte aligned, of at least
+ *           vrLayerNormBackwardWorkspace bytes, used until the work on
+ *           `stream` is done; may be NULL if dweight and dbias are. */
+VR_API vrResult_t vrLayerNormBackward(const void* dy, const void* x, const void* weight,
+                                      const float* mean, const float* rstd, void* dx,
+                                      void* dweight, void* dbias, size_t rows, size_t cols,
+                                      size_t dyStride, size_t xStride, size_t dxStride,
+                                      vrDataType_t dtype, vrDataType_t weightType,
+                                      void* workspace, size_t workspaceBytes, void* stream);
+
+/* Workspace bytes of vrGradNorm and vrClipGradNorm for nTensors tensors of
+ * any sizes. Host only. */
+VR_API vrResult_t vrGradNormWorkspace(int nTensors, size_t* bytes);
+
+/* The 2-norm of a list of gradients:
+ *   norm = |scale| sqrt(sum over tensors and elements of g^2).
+ *  grads    [host array of nTensors device pointers], counts [host] elements
+ *           of each (0 allowed, its pointer is then not examined), dtypes
+ *           [host] vrFloat16, vrBfloat16, vrFloat32 or vrFloat64 each; a list
+ *           may mix them. The arrays are read during the call only.
+ *  nTensors >= 1, any number.
+ *  scale    finite: what the gradients are to be multiplied by (1 / nRanks
+ *           after a vrSum AllReduce, or a loss scale's reciprocal).
+ *  norm     [device] one float, or NULL.  tensorNorms [device] nTensors
+ *           floats, each tensor's own norm, or NULL. Not both NULL.
+ * Squares of float32 and bfloat16 elements that leave the range of a float
+ * are summed in 64 bits; a float64 element's square has to fit a double. */
+VR_API vrResult_t vrGradNorm(const void* const* grads, const size_t* counts,
+                             const vrDataType_t* dtypes, int nTensors, float scale, float* norm,
+                             float* tensorNorms, void* workspace, size_t workspaceBytes,
+                             void* stream);
+
+/* Clipping by the norm of the list: with norm as above,
+ *   outs[t] = grads[t] * (scale * (norm > maxNorm ? maxNorm / norm : 1)),
+ * in the type of grads[t], each product rounded once. If the norm is infinite
+ * or NaN nothing is clipped (the factor is `scale`): read `norm` and drop the
+ * step.
+ *  outs     [host array of nTensors device pointers]; outs[t] == grads[t] is
+ *           allowed, other overlaps are not.
+ *  maxNorm  >= 0, may be infinite.   norm [device] one float, or NULL.
+ * Other arguments as for vrGradNorm. */
+VR_API vrResult_t vrClipGradNorm(const void* const* grads, void* const* outs,
+                                 const size_t* counts, const vrDataType_t* dtypes, int nTensors,
+                                 float scale, float maxNorm, float* norm, void* workspace,
+                                 size_t workspaceBytes, void* stream);
+
 /* Static description of a result code. Never NULL. */
 VR_API const char* vrGetErrorString(vrResult_t result);
 

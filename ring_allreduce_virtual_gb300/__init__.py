@@ -69,6 +69,19 @@ def lib():
         L.vrAllReduceNoAllocGetStatus.argtypes = [ctypes.POINTER(i32)]
         L.vrRedOpCreatePreMulSum.argtypes = [ctypes.POINTER(i32), ctypes.c_char_p, i32, vp]
         L.vrRedOpDestroy.argtypes = [i32, vp]
+        pp, psz, pi32, f32 = (ctypes.POINTER(vp), ctypes.POINTER(sz), ctypes.POINTER(i32),
+                              ctypes.c_float)
+        L.vrLayerNormForward.argtypes = [vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, f32, i32, i32,
+                                         vp]
+        L.vrLayerNormBackwardWorkspace.argtypes = [sz, sz, i32, psz]
+        L.vrLayerNormBackward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, sz, sz, sz, sz, i32,
+                                          i32, vp, sz, vp]
+        L.vrGradNormWorkspace.argtypes = [i32, psz]
+        L.vrGradNorm.argtypes = [pp, psz, pi32, i32, f32, vp, vp, vp, sz, vp]
+        L.vrClipGradNorm.argtypes = [pp, pp, psz, pi32, i32, f32, f32, vp, vp, sz, vp]
+        for name in ("vrLayerNormForward", "vrLayerNormBackwardWorkspace", "vrLayerNormBackward",
+                     "vrGradNormWorkspace", "vrGradNorm", "vrClipGradNorm"):
+            getattr(L, name).restype = i32
         for name in ("vrCommCreate", "vrAllReduce", "vrCommDestroy", "vrCommGetAsyncError",
                      "vrCommSetTimeout", "vrCommGetInfo", "vrAllReduceNoAlloc",
                      "vrAllReduceNoAllocGetStatus",
@@ -247,6 +260,73 @@ def vrAllReduceNoAllocGetStatus():
     e = ctypes.c_int()
     _check(lib().vrAllReduceNoAllocGetStatus(ctypes.byref(e)), "vrAllReduceNoAllocGetStatus")
     return e.value
+
+
+# The operators of a training step (addresses are ints, 0 or None: NULL; see
+# training.py for the same on torch tensors).
+def vrLayerNormForward(x, weight, bias, y, mean, rstd, rows, cols, xStride, yStride, eps, dtype,
+                       weightType, stream=0):
+    _check(lib().vrLayerNormForward(x or None, weight or None, bias or None, y or None,
+                                    mean or None, rstd or None, rows, cols, xStride, yStride, eps,
+                                    _code(DTYPES, dtype, "dtype"),
+                                    _code(DTYPES, weightType, "dtype"), stream or None),
+           "vrLayerNormForward")
+
+
+def vrLayerNormBackwardWorkspace(rows, cols, dtype):
+    """Workspace bytes of vrLayerNormBackward."""
+    b = ctypes.c_size_t()
+    _check(lib().vrLayerNormBackwardWorkspace(rows, cols, _code(DTYPES, dtype, "dtype"),
+                                              ctypes.byref(b)), "vrLayerNormBackwardWorkspace")
+    return b.value
+
+
+def vrLayerNormBackward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows, cols, dyStride,
+                        xStride, dxStride, dtype, weightType, workspace, workspaceBytes,
+                        stream=0):
+    _check(lib().vrLayerNormBackward(dy or None, x or None, weight or None, mean or None,
+                                     rstd or None, dx or None, dweight or None, dbias or None,
+                                     rows, cols, dyStride, xStride, dxStride,
+                                     _code(DTYPES, dtype, "dtype"),
+                                     _code(DTYPES, weightType, "dtype"), workspace or None,
+                                     workspaceBytes, stream or None), "vrLayerNormBackward")
+
+
+def vrGradNormWorkspace(nTensors):
+    """Workspace bytes of vrGradNorm and vrClipGradNorm."""
+    b = ctypes.c_size_t()
+    _check(lib().vrGradNormWorkspace(nTensors, ctypes.byref(b)), "vrGradNormWorkspace")
+    return b.value
+
+
+def tensor_arrays(ptrs, counts, dtypes):
+    """The host arrays that vrGradNorm and vrClipGradNorm read: device
+    addresses, element counts and element types (names or codes), as ctypes
+    arrays that a caller may keep and pass again."""
+    n = len(ptrs)
+    if len(counts) != n or len(dtypes) != n:
+        raise ValueError(f"{n} addresses, {len(counts)} counts and {len(dtypes)} types")
+    return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_size_t * n)(*counts),
+            (ctypes.c_int * n)(*[_code(DTYPES, d, "dtype") for d in dtypes]))
+
+
+def vrGradNorm(arrays, scale, norm, tensorNorms, workspace, workspaceBytes, stream=0):
+    """arrays: what tensor_arrays returned."""
+    ptrs, counts, types = arrays
+    _check(lib().vrGradNorm(ptrs, counts, types, len(ptrs), scale, norm or None,
+                            tensorNorms or None, workspace or None, workspaceBytes,
+                            stream or None), "vrGradNorm")
+
+
+def vrClipGradNorm(arrays, outs, scale, maxNorm, norm, workspace, workspaceBytes, stream=0):
+    """arrays: what tensor_arrays returned; outs: a ctypes array of as many
+    output addresses (arrays[0] itself: in place)."""
+    ptrs, counts, types = arrays
+    if len(outs) != len(ptrs):
+        raise ValueError(f"{len(ptrs)} gradients and {len(outs)} outputs")
+    _check(lib().vrClipGradNorm(ptrs, outs, counts, types, len(ptrs), scale, maxNorm,
+                                norm or None, workspace or None, workspaceBytes, stream or None),
+           "vrClipGradNorm")
 
 
 # ------------------------------------------------------------ torch helper

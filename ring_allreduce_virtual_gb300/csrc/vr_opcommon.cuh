@@ -1,0 +1,101 @@
+// vr_opcommon.cuh -- what the training-step operators (layer norm, gradient
+// norm, clipping) share: element conversions, block sums, launch and argument
+// helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+#include <stddef.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "vr.h"
+
+namespace vrop {
+
+// Grids are sized for the 152 SMs of the one GPU this library is written for,
+// so that the order of every sum is the same wherever it runs.
+constexpr int kSMs = 152;
+
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+};
+
+inline int elemSizeOf(vrDataType_t t) {
+  switch (t) {
+    case vrFloat16: case vrBfloat16: return 2;
+    case vrFloat32: return 4;
+    case vrFloat64: return 8;
+    default: return 0;  // not a type of these operators
+  }
+}
+
+inline bool misaligned(const void* p, size_t to) { return (uintptr_t)p % to != 0; }
+
+// [a, a + an) and [b, b + bn) share a byte.
+inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && an && bn && x < y + bn && y < x + an;
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ double to_f64(double x) { return x; }
+template <typename T>
+__device__ __forceinline__ double to_f64(T x) { return (double)to_f32(x); }
+// The one rounding of a result to its type, to nearest even.
+template <typename T>
+__device__ __forceinline__ T from_f32(float x) {
+  if constexpr (std::is_same_v<T, __half>) return __float2half_rn(x);
+  else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __float2bfloat16_rn(x);
+  else return x;
+}
+
+template <typename A>
+__device__ __forceinline__ A warp_sum(A v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over a block of NW warps, the same value in every thread, added up in an
+// order fixed by the lanes. `buf` holds NW values; the caller separates two
+// uses of it by a barrier (two buffers in turn do).
+template <int NW, typename A>
+__device__ __forceinline__ A block_sum(A v, A* buf) {
+  v = warp_sum(v);
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = buf[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) v += buf[i];
+  }
+  return v;
+}
+
+// Launch of `kernel` with one by-value argument struct.
+template <typename Args>
+inline vrResult_t launch(const void* kernel, dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t stream, Args& args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  void* a[] = {&args};
+  if (cudaLaunchKernelExC(&cfg, kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return vrCudaError;
+  }
+  return vrSuccess;
+}
+
+}  // namespace vrop
