@@ -10,11 +10,12 @@
 // variance is the mean of squared distances from the mean, never a difference
 // of two large sums. All of it is bound by memory traffic (8 to 14 flop for 4
 // to 12 bytes).
-#include "vr_opcommon.cuh"
+#include "vr_ln_rows.cuh"
 
 namespace {
 
 using namespace vrop;
+using namespace vrln;
 
 struct FwdArgs {
   const void* x;
@@ -25,6 +26,7 @@ struct FwdArgs {
   float* rstd;
   uint64_t rows, cols, xStride, yStride;
   float eps;
+  Layout l;
 };
 
 struct BwdArgs {
@@ -39,6 +41,7 @@ struct BwdArgs {
   uint64_t rows, cols, dyStride, xStride, dxStride;
   float* partials;  // [splits][2][cols]: sums of dy u and of dy over a split's rows
   int splits;
+  Layout l;
 };
 
 constexpr int kRowThreads = 256;
@@ -73,6 +76,152 @@ __global__ void __launch_bounds__(kRowThreads) vrLnForwardAny(const __grid_const
       if (a.mean) a.mean[row] = m;
       if (a.rstd) a.rstd[row] = r;
     }
+  }
+}
+
+// ROWS rows of a group in registers, E elements of each in a thread, and STAGES -
+// 1 times as many on their way: read once, written once.
+template <typename T, typename W, int E, int ROWS, int STAGES, int MODE, bool RAGGED, int REGS>
+__global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArgs a) {
+  constexpr int V = kV<T>, P = E / V;
+  extern __shared__ uint4 ring[];  // [warps][STAGES][ROWS][P][32]
+  __shared__ RowSum<MODE, ROWS> sum;
+  const int cols = (int)a.cols;
+  const Place<T, MODE, P> at(a.l, a.rows, cols);
+  int turn = 0;
+  if constexpr (MODE == IN_CLUSTER) cluster_sync();  // the others' buffers are there
+  const T* xp = static_cast<const T*>(a.x) + at.row * a.xStride;
+  T* yp = static_cast<T*>(a.y) + at.row * a.yStride;
+  const uint64_t xStep = a.l.step * a.xStride, yStep = a.l.step * a.yStride;
+  bool used[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) used[i] = at.used(i);
+  uint4* const mine = ring + (threadIdx.x >> 5) * (STAGES * ROWS * P * 32) + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (!used[i])
+      for (int k = 0; k < STAGES * ROWS; ++k) mine[(k * P + i) * 32] = make_uint4(0, 0, 0, 0);
+  T ahead[ROWS];  // the next rows' elements outside the packs
+  auto fetch = [&](int left, const T* p, uint4* to) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+      if (k < left) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (used[i])
+            copy16(&to[(k * P + i) * 32],
+                   p + k * xStep + i * (MODE == IN_WARP ? at.stripe : 32) * V);
+      }
+    copies_commit();
+  };
+  auto fetchEdge = [&](int left, const T* p) {
+    if constexpr (RAGGED) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k)
+        ahead[k] = at.edge >= 0 && k < left ? p[k * xStep + at.edge] : from_f32<T>(0.f);
+    }
+  };
+  const T* xf = xp + at.column(0);  // the rows to fetch next
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) {
+    fetch(at.n - i * ROWS, xf, mine + i * (ROWS * P * 32));
+    xf += ROWS * xStep;
+  }
+  fetchEdge(at.n, xp);
+  Params<T, W> w[P], b[P];
+  float we = 1.f, be = 0.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    w[i].load(static_cast<const W*>(a.w), at.column(i), used[i], 1.f);
+    b[i].load(static_cast<const W*>(a.b), at.column(i), used[i], 0.f);
+  }
+  if (RAGGED && at.edge >= 0) {
+    if (a.w) we = to_f32(static_cast<const W*>(a.w)[at.edge]);
+    if (a.b) be = to_f32(static_cast<const W*>(a.b)[at.edge]);
+  }
+  const float c = 1.f / (float)cols;
+  uint64_t row = at.row;
+  int left = at.n, stage = 0;
+  T* yo = yp + at.column(0);
+  for (int round = 0; round < at.rounds; round += ROWS) {
+    const int back = stage == 0 ? STAGES - 1 : stage - 1;
+    fetch(left - (STAGES - 1) * ROWS, xf, mine + back * (ROWS * P * 32));
+    xf += ROWS * xStep;
+    copies_wait<STAGES - 1>();
+    F2 x[ROWS][P][V / 2];
+    float e[ROWS], s[ROWS];
+    const uint4* from = mine + stage * (ROWS * P * 32);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      F2 s2 = f2(0.f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        unpack<T>(from[(k * P + i) * 32], x[k][i]);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) s2 = s2 + x[k][i][j];
+      }
+      s[k] = both(s2);
+      if constexpr (RAGGED) {
+        e[k] = to_f32(ahead[k]);
+        s[k] += e[k];
+      }
+    }
+    xp += ROWS * xStep;
+    fetchEdge(left - ROWS, xp);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    sum(s, a.l, at.group, turn);
+    float m[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      m[k] = s[k] * c;
+      const F2 minus = f2(-m[k]);
+      F2 q2 = f2(0.f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) x[k][i][j] = x[k][i][j] + minus;
+        if (used[i]) {
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) q2 = fma2(x[k][i][j], x[k][i][j], q2);
+        }
+      }
+      s[k] = both(q2);
+      if constexpr (RAGGED) {
+        e[k] -= m[k];
+        if (at.edge >= 0) s[k] = fmaf(e[k], e[k], s[k]);
+      }
+    }
+    sum(s, a.l, at.group, turn);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      s[k] = rsqrtf(s[k] * c + a.eps);
+      const F2 r2 = f2(s[k]);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        F2 g[V / 2], h[V / 2];
+        w[i].get(g);
+        b[i].get(h);
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) x[k][i][j] = fma2(x[k][i][j] * r2, g[j], h[j]);
+        if (used[i] && k < left)
+          *reinterpret_cast<uint4*>(yo + k * yStep + i * (MODE == IN_WARP ? at.stripe : 32) * V) =
+              pack<T>(x[k][i]);
+      }
+      if (RAGGED && at.edge >= 0 && k < left)
+        yp[k * yStep + at.edge] = from_f32<T>(fmaf(e[k] * s[k], we, be));
+    }
+    if (at.lane == 0) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k)
+        if (k < left) {
+          if (a.mean) a.mean[row + (uint64_t)k * a.l.step] = m[k];
+          if (a.rstd) a.rstd[row + (uint64_t)k * a.l.step] = s[k];
+        }
+    }
+    left -= ROWS;
+    row += (uint64_t)ROWS * a.l.step;
+    yp += ROWS * yStep;
+    yo += ROWS * yStep;
   }
 }
 
@@ -169,6 +318,72 @@ int splitsFor(uint64_t rows, uint64_t cols) {
   return s ? (int)s : 1;
 }
 
+// Two matrices whose rows lie alike modulo 16 bytes.
+bool alike(const void* p, uint64_t pStride, const void* q, uint64_t qStride, int es) {
+  return (((uintptr_t)p - (uintptr_t)q) & 15) == 0 && (((pStride - qStride) * es) & 15) == 0;
+}
+
+// One shape of the kernel for rows up to `maxThreads` threads wide (times 8 for a
+// cluster's blocks). False if a row does not fit.
+enum { NARROW = 1, BLOCK = 2, CLUSTER = 4, WHOLE = 8, CUT = 16 };  // what the shape is built for
+template <typename T, typename W, int E, int ROWS, int STAGES, int REGS, int FOR>
+bool forwardShape(FwdArgs& a, bool ragged, int blockThreads, int maxThreads, cudaStream_t st,
+                  vrResult_t* result) {
+  constexpr int V = kV<T>;
+  int mode;
+  if (!layoutFor(a.cols, V, E / V, blockThreads, maxThreads, ragged, &a.l, &mode)) return false;
+  const void* k = nullptr;
+  auto pick = [&](auto m, auto r) {
+    constexpr int MODE = decltype(m)::value;
+    constexpr bool RAGGED = decltype(r)::value;
+    if constexpr ((FOR & (1 << MODE)) != 0 && (FOR & (RAGGED ? CUT : WHOLE)) != 0)
+      if (mode == MODE && ragged == RAGGED)
+        k = (const void*)&vrLnForwardRows<T, W, E, ROWS, STAGES, MODE, RAGGED, REGS>;
+  };
+  const auto each = [&](auto m) {
+    pick(m, std::false_type{});
+    pick(m, std::true_type{});
+  };
+  each(std::integral_constant<int, IN_WARP>{});
+  each(std::integral_constant<int, IN_BLOCK>{});
+  each(std::integral_constant<int, IN_CLUSTER>{});
+  if (!k) return false;
+  const int threads = a.l.tpr * a.l.groups;
+  const size_t smem = (size_t)STAGES * ROWS * E * sizeof(T) * threads;
+  const unsigned grid = gridFor(a.rows, &a.l, V, residentWarps(REGS, smem, threads), ragged, ROWS);
+  *result = allowShared(k) ? launch(k, dim3(grid), dim3(threads), smem, st, a, a.l.ctas) : vrCudaError;
+  return true;
+}
+
+// Rows that are kept in registers: all but the widest. The shapes were chosen by
+// measuring on a GB300 (x read and y written once, of the measured copy peak).
+// 16 elements of 2 rows a thread carry the narrow rows (256 bf16 0.90, 1024 bf16
+// 0.90, 1280 float32 0.91) and ragged 16-bit rows up to 4096. Whole packs of
+// 16-bit rows over 1024 do better with 32 elements a thread, as fewer threads
+// share each sum (4096 bf16 0.91 against 0.88, 1600 0.87 against 0.77); ragged
+// 16-bit rows up to 2048 with 4 rows at a time, as the one-element loads of
+// their ends are latency (2051 bf16 0.77 against 0.68). Wider rows take 32
+// elements of one row a thread (4096 float32 0.93 against 0.85 with 16 of two,
+// 8192 bf16 0.91, 16384 0.77), beyond 512 threads a cluster, whose barrier is
+// paid twice a row (32768 bf16 0.46, 65536 0.26).
+template <typename T, typename W>
+bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
+  constexpr bool half = sizeof(T) == 2;
+  a.l.offset = (int)((uintptr_t)a.x & 15);
+  a.l.skew = (int)((a.xStride * sizeof(T)) & 15);
+  const bool ragged = a.l.offset || a.l.skew || a.cols % kV<T>;
+  if constexpr (half) {
+    if (!ragged && a.cols > 1024 &&
+        forwardShape<T, W, 32, 2, 2, 168, BLOCK | WHOLE>(a, ragged, 128, 128, st, r))
+      return true;
+    if (ragged && forwardShape<T, W, 16, 4, 2, 168, NARROW | BLOCK | CUT>(a, ragged, 128, 128, st, r))
+      return true;
+  }
+  constexpr int both = NARROW | BLOCK | WHOLE | CUT, wide = BLOCK | CLUSTER | WHOLE | CUT;
+  return forwardShape<T, W, 16, 2, 2, 128, both>(a, ragged, 256, half ? 256 : 128, st, r) ||
+         forwardShape<T, W, 32, 1, 3, 128, wide>(a, ragged, 256, 512, st, r);
+}
+
 // Bytes from a matrix's first element to the end of its last.
 size_t extent(uint64_t rows, uint64_t cols, uint64_t stride, int es) {
   return rows ? ((rows - 1) * stride + cols) * es : 0;
@@ -197,10 +412,14 @@ extern "C" VR_API vrResult_t vrLayerNormForward(const void* x, const void* weigh
   if (!(x == y && xStride == yStride) &&
       overlap(x, extent(rows, cols, xStride, es), y, extent(rows, cols, yStride, es)))
     return vrInvalidArgument;
-  FwdArgs a = {x, weight, bias, y, mean, rstd, rows, cols, xStride, yStride, eps};
+  FwdArgs a = {x, weight, bias, y, mean, rstd, rows, cols, xStride, yStride, eps, {}};
   return dispatch(dtype, weightType, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
+    vrResult_t r;
+    if (alike(x, xStride, y, yStride, es) && rows < kMostRows &&
+        forwardRows<T, W>(a, (cudaStream_t)stream, &r))
+      return r;
     const uint64_t most = (uint64_t)kSMs * 8;
     return launch((const void*)&vrLnForwardAny<T, W>, dim3((unsigned)(rows < most ? rows : most)),
                   dim3(kRowThreads), 0, (cudaStream_t)stream, a);

@@ -80,16 +80,24 @@ __device__ __forceinline__ A block_sum(A v, A* buf) {
   return v;
 }
 
-// Launch of `kernel` with one by-value argument struct.
+// Launch of `kernel` with one by-value argument struct, in clusters of `ctas`.
 template <typename Args>
 inline vrResult_t launch(const void* kernel, dim3 grid, dim3 block, size_t smem,
-                         cudaStream_t stream, Args& args) {
+                         cudaStream_t stream, Args& args, int ctas = 1) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (ctas > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
   void* a[] = {&args};
   if (cudaLaunchKernelExC(&cfg, kernel, a) != cudaSuccess) {
     cudaGetLastError();
