@@ -285,16 +285,231 @@ __global__ void __launch_bounds__(32 * kColWarps) vrLnColumns(const __grid_const
   }
 }
 
-// dw and db, second step: the splits' sums added up, split by split.
+// dw and db, second step: the splits' sums added up, split by split. A warp
+// takes every eighth split of 32 columns.
 template <typename W>
 __global__ void __launch_bounds__(256) vrLnJoin(const __grid_constant__ BwdArgs a) {
-  const uint64_t col = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  if (col >= a.cols) return;
+  __shared__ float buf[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t col = (uint64_t)blockIdx.x * 32 + lane;
   W* out = static_cast<W*>(blockIdx.y ? a.db : a.dw);
   if (!out) return;
   float s = 0.f;
-  for (int i = 0; i < a.splits; ++i) s += a.partials[((uint64_t)i * 2 + blockIdx.y) * a.cols + col];
-  out[col] = from_f32<W>(s);
+  if (col < a.cols) {
+    const float* p = a.partials + (uint64_t)blockIdx.y * a.cols + col;
+#pragma unroll 4
+    for (int i = warp; i < a.splits; i += 8) s += p[(uint64_t)i * 2 * a.cols];
+  }
+  buf[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && col < a.cols) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += buf[i][lane];
+    out[col] = from_f32<W>(s);
+  }
+}
+
+// The backward pass of rows that are kept on chip: dy and x are read once, dx is
+// written once, and the sums of dw and db over a group's rows stay in
+// registers until its last row. Each group's ROWS rows lie in shared memory
+// through both of their walks (s and p; then dx), STAGES - 1 times as many on
+// their way.
+template <typename T, typename W, int E, int ROWS, int STAGES, int MODE, bool RAGGED, int REGS>
+__global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdArgs a) {
+  constexpr int V = kV<T>, P = E / V;
+  extern __shared__ uint4 ring[];  // [warps][STAGES][ROWS][dy, x][P][32]
+  __shared__ RowSum<MODE, 2 * ROWS> sum;
+  const int cols = (int)a.cols;
+  const Place<T, MODE, P> at(a.l, a.rows, cols);
+  int turn = 0;
+  if constexpr (MODE == IN_CLUSTER) cluster_sync();  // the others' buffers are there
+  const T* gp = static_cast<const T*>(a.dy) + at.row * a.dyStride;
+  const T* xp = static_cast<const T*>(a.x) + at.row * a.xStride;
+  T* op = static_cast<T*>(a.dx) + at.row * a.dxStride;
+  const uint64_t gStep = a.l.step * a.dyStride, xStep = a.l.step * a.xStride,
+                 oStep = a.l.step * a.dxStride;
+  const int apart = (MODE == IN_WARP ? at.stripe : 32) * V;  // elements between a thread's packs
+  bool used[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) used[i] = at.used(i);
+  constexpr int kSet = ROWS * 2 * P * 32;
+  uint4* const mine = ring + (threadIdx.x >> 5) * (STAGES * kSet) + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (!used[i])
+      for (int k = 0; k < STAGES * ROWS * 2; ++k) mine[(k * P + i) * 32] = make_uint4(0, 0, 0, 0);
+  T aheadG[ROWS], aheadX[ROWS];    // the next rows' elements outside the packs
+  float nextM[ROWS], nextR[ROWS];  // and their statistics
+  auto fetch = [&](int left, const T* g, const T* x, uint4* to) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k)
+      if (k < left) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (used[i]) {
+            copy16(&to[(2 * k * P + i) * 32], g + k * gStep + i * apart);
+            copy16(&to[((2 * k + 1) * P + i) * 32], x + k * xStep + i * apart);
+          }
+      }
+    copies_commit();
+  };
+  auto fetchRest = [&](int left, uint64_t row, const T* g, const T* x) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      nextM[k] = nextR[k] = 0.f;
+      if (RAGGED) aheadG[k] = aheadX[k] = from_f32<T>(0.f);
+      if (k < left) {
+        nextM[k] = a.mean[row + (uint64_t)k * a.l.step];
+        nextR[k] = a.rstd[row + (uint64_t)k * a.l.step];
+        if (RAGGED && at.edge >= 0) {
+          aheadG[k] = g[k * gStep + at.edge];
+          aheadX[k] = x[k * xStep + at.edge];
+        }
+      }
+    }
+  };
+  const T *gf = gp + at.column(0), *xf = xp + at.column(0);  // the rows to fetch next
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) {
+    fetch(at.n - i * ROWS, gf, xf, mine + i * kSet);
+    gf += ROWS * gStep;
+    xf += ROWS * xStep;
+  }
+  fetchRest(at.n, at.row, gp, xp);
+  Params<T, W> w[P];
+  float we = 1.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    w[i].load(static_cast<const W*>(a.w), at.column(i), used[i], 1.f);
+  if (RAGGED && at.edge >= 0 && a.w) we = to_f32(static_cast<const W*>(a.w)[at.edge]);
+  F2 dw[P][V / 2], db[P][V / 2];
+  float dwe = 0.f, dbe = 0.f;
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) dw[i][j] = db[i][j] = f2(0.f);
+  const float c = 1.f / (float)cols;
+  uint64_t row = at.row;
+  int left = at.n, stage = 0;
+  T* oo = op + at.column(0);
+  for (int round = 0; round < at.rounds; round += ROWS) {
+    const int back = stage == 0 ? STAGES - 1 : stage - 1;
+    fetch(left - (STAGES - 1) * ROWS, gf, xf, mine + back * kSet);
+    gf += ROWS * gStep;
+    xf += ROWS * xStep;
+    float m[ROWS], r[ROWS], ge[ROWS], de[ROWS], s[2 * ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      m[k] = nextM[k];
+      r[k] = nextR[k];
+      if constexpr (RAGGED) {
+        ge[k] = to_f32(aheadG[k]);
+        de[k] = to_f32(aheadX[k]) - m[k];
+      }
+    }
+    gp += ROWS * gStep;
+    xp += ROWS * xStep;
+    row += (uint64_t)ROWS * a.l.step;
+    fetchRest(left - ROWS, row, gp, xp);
+    copies_wait<STAGES - 1>();
+    const uint4* from = mine + stage * kSet;
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      F2 s2 = f2(0.f), p2 = f2(0.f);
+      if (k < left) {
+        const F2 minus = f2(-m[k]), r2 = f2(r[k]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          F2 g[V / 2], x[V / 2], ww[V / 2];
+          unpack<T>(from[(2 * k * P + i) * 32], g);
+          unpack<T>(from[((2 * k + 1) * P + i) * 32], x);
+          w[i].get(ww);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            const F2 d = x[j] + minus;
+            db[i][j] = db[i][j] + g[j];
+            dw[i][j] = fma2(g[j] * r2, d, dw[i][j]);
+            const F2 gw = g[j] * ww[j];
+            s2 = s2 + gw;
+            p2 = fma2(gw, d, p2);
+          }
+        }
+        if constexpr (RAGGED) {
+          dbe += ge[k];
+          dwe = fmaf(ge[k] * r[k], de[k], dwe);
+        }
+      }
+      s[2 * k] = both(s2);
+      s[2 * k + 1] = both(p2);
+      if constexpr (RAGGED) {
+        ge[k] *= we;
+        s[2 * k] += ge[k];
+        s[2 * k + 1] = fmaf(ge[k], de[k], s[2 * k + 1]);
+      }
+    }
+    if (a.dx) {
+      sum(s, a.l, at.group, turn);
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        // dx = r g - r s - (x - m) r^2 p, s and p the means of g and of g (x - m)
+        const float c0 = -r[k] * (s[2 * k] * c), c1 = -r[k] * r[k] * (r[k] * (s[2 * k + 1] * c));
+        const F2 minus = f2(-m[k]), r2 = f2(r[k]), c02 = f2(c0), c12 = f2(c1);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          if (used[i] && k < left) {
+            F2 g[V / 2], x[V / 2], ww[V / 2];
+            unpack<T>(from[(2 * k * P + i) * 32], g);
+            unpack<T>(from[((2 * k + 1) * P + i) * 32], x);
+            w[i].get(ww);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+              x[j] = fma2(x[j] + minus, c12, fma2(g[j] * ww[j], r2, c02));
+            *reinterpret_cast<uint4*>(oo + k * oStep + i * apart) = pack<T>(x);
+          }
+        }
+        if (RAGGED && at.edge >= 0 && k < left)
+          op[k * oStep + at.edge] = from_f32<T>(fmaf(de[k], c1, fmaf(ge[k], r[k], c0)));
+      }
+    }
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    left -= ROWS;
+    op += ROWS * oStep;
+    oo += ROWS * oStep;
+  }
+  if (!a.dw && !a.db) return;
+  copies_wait<0>();
+  // The groups' sums are added up in shared memory, in the groups' order, so
+  // that a block leaves one; a cluster's blocks write their own columns.
+  float* part = a.partials + (uint64_t)(blockIdx.x / a.l.ctas) * 2 * a.cols;
+  if constexpr (MODE != IN_CLUSTER) {
+    __syncthreads();
+    float* all = reinterpret_cast<float*>(ring);
+    part = all + at.group * 2 * cols;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (used[i]) {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const int col = at.column(i) + 2 * j;
+        split(dw[i][j], part[col], part[col + 1]);
+        split(db[i][j], part[cols + col], part[cols + col + 1]);
+      }
+    }
+  if (RAGGED && at.edge >= 0) {
+    part[at.edge] = dwe;
+    part[cols + at.edge] = dbe;
+  }
+  if constexpr (MODE != IN_CLUSTER) {
+    __syncthreads();
+    const float* all = reinterpret_cast<const float*>(ring);
+    float* out = a.partials + (uint64_t)blockIdx.x * 2 * a.cols;
+    for (int i = threadIdx.x; i < 2 * cols; i += blockDim.x) {
+      float t = all[i];
+      for (int k = 1; k < a.l.groups; ++k) t += all[k * 2 * cols + i];
+      out[i] = t;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -310,6 +525,7 @@ vrResult_t dispatch(vrDataType_t t, vrDataType_t w, F f) {
   return w == t ? f(__nv_bfloat16{}, __nv_bfloat16{}) : f(__nv_bfloat16{}, float{});
 }
 
+// Splits of the rows where dw and db are summed in a kernel of their own.
 int splitsFor(uint64_t rows, uint64_t cols) {
   const uint64_t tiles = (cols + 31) / 32;
   uint64_t s = (uint64_t)kSMs * 8 / tiles + 1;
@@ -384,6 +600,86 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
          forwardShape<T, W, 32, 1, 3, 128, wide>(a, ragged, 256, 512, st, r);
 }
 
+// How a backward pass is laid out, and the sums of dw and db that it leaves.
+// The shape was chosen by measuring on a GB300 (dy and x read and dx written
+// once, of the measured copy peak): 16 elements of 2 rows a thread, the blocks
+// as large as one for each SM can be, which leaves the fewest sums to join (8192
+// bf16 0.94, 4096 bf16 0.88, 1024 bf16 0.88). float32 rows take 256 threads
+// of it (4096 0.91), as the ring of 512 would not fit, and from 4096 on one row at
+// a time (8192 0.90 against 0.84 as clusters of two); wider ones clusters (16384
+// bf16 0.65, 32768 0.44).
+struct BwdPlan {
+  Layout l;
+  int mode, threads;
+  unsigned grid;
+  size_t smem;
+};
+template <typename T, int E, int ROWS, int STAGES, int REGS>
+bool planShape(uint64_t rows, uint64_t cols, bool ragged, int blockThreads, int maxThreads,
+               BwdPlan* p) {
+  constexpr int V = kV<T>;
+  if (!layoutFor(cols, V, E / V, blockThreads, maxThreads, ragged, &p->l, &p->mode)) return false;
+  p->threads = p->l.tpr * p->l.groups;
+  const size_t ring = (size_t)STAGES * ROWS * E * sizeof(T) * 2 * p->threads;
+  // The groups' sums take the ring's place at the end, of every column.
+  const size_t join = p->mode == IN_CLUSTER ? 0 : (size_t)p->l.groups * 2 * cols * sizeof(float);
+  p->smem = ring > join ? ring : join;
+  p->grid = gridFor(rows, &p->l, V, residentWarps(REGS, p->smem, p->threads), ragged, ROWS);
+  return p->smem <= kMostShared;
+}
+enum { NO_PLAN = 0, TWO_ROWS = 1, ONE_ROW = 2 };
+template <typename T>
+int planBackward(uint64_t rows, uint64_t cols, bool ragged, BwdPlan* p) {
+  if (rows >= kMostRows) return NO_PLAN;
+  if constexpr (sizeof(T) == 2)
+    return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 512, 512, p) ? TWO_ROWS : NO_PLAN;
+  if (cols > 4096 && cols < 8192 + kV<T> &&
+      planShape<T, 16, 1, 3, 96>(rows, cols, ragged, 512, 512, p) && p->mode == IN_BLOCK)
+    return ONE_ROW;
+  return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 256, 256, p) ? TWO_ROWS : NO_PLAN;
+}
+
+template <typename T, typename W, int MODE>
+const void* backwardKernel(bool ragged) {
+  return ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 2, 2, MODE, true, 128>
+                : (const void*)&vrLnBackwardRows<T, W, 16, 2, 2, MODE, false, 128>;
+}
+// False if the rows do not fit.
+template <typename T, typename W>
+bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
+  const int offset = (int)((uintptr_t)a.x & 15), skew = (int)((a.xStride * sizeof(T)) & 15);
+  const bool ragged = offset || skew || a.cols % kV<T>;
+  BwdPlan p;
+  const int shape = planBackward<T>(a.rows, a.cols, ragged, &p);
+  if (shape == NO_PLAN) return false;
+  const void* k = p.mode == IN_WARP    ? backwardKernel<T, W, IN_WARP>(ragged)
+                  : p.mode == IN_BLOCK ? backwardKernel<T, W, IN_BLOCK>(ragged)
+                                       : backwardKernel<T, W, IN_CLUSTER>(ragged);
+  if constexpr (sizeof(T) == 4)
+    if (shape == ONE_ROW)
+      k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, true, 96>
+                 : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, false, 96>;
+  a.l = p.l;
+  a.l.offset = offset;
+  a.l.skew = skew;
+  a.splits = (int)(p.grid / p.l.ctas);
+  *r = allowShared(k) ? launch(k, dim3(p.grid), dim3(p.threads), p.smem, st, a, p.l.ctas)
+                      : vrCudaError;
+  return true;
+}
+
+// The most sums that any layout of these sizes leaves.
+template <typename T>
+uint64_t mostSplits(uint64_t rows, uint64_t cols) {
+  uint64_t most = splitsFor(rows, cols);
+  for (const bool ragged : {false, true}) {
+    BwdPlan p;
+    if (rows && planBackward<T>(rows, cols, ragged, &p) != NO_PLAN && p.grid / p.l.ctas > most)
+      most = p.grid / p.l.ctas;
+  }
+  return most;
+}
+
 // Bytes from a matrix's first element to the end of its last.
 size_t extent(uint64_t rows, uint64_t cols, uint64_t stride, int es) {
   return rows ? ((rows - 1) * stride + cols) * es : 0;
@@ -429,7 +725,9 @@ extern "C" VR_API vrResult_t vrLayerNormForward(const void* x, const void* weigh
 extern "C" VR_API vrResult_t vrLayerNormBackwardWorkspace(size_t rows, size_t cols,
                                                           vrDataType_t dtype, size_t* bytes) {
   if (!typesOk(dtype, dtype) || cols < 1 || !bytes) return vrInvalidArgument;
-  *bytes = (size_t)splitsFor(rows, cols) * 2 * cols * sizeof(float);
+  const uint64_t splits =
+      dtype == vrFloat32 ? mostSplits<float>(rows, cols) : mostSplits<__half>(rows, cols);
+  *bytes = (size_t)(splits * 2 * cols * sizeof(float));
   return vrSuccess;
 }
 
@@ -461,24 +759,27 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
     return vrInvalidArgument;
   const bool params = dweight || dbias;
   BwdArgs a = {dy, x, weight, mean, rstd, dx, dweight, dbias, rows, cols,
-               dyStride, xStride, dxStride, (float*)workspace, splitsFor(rows, cols)};
-  if (params && (!workspace || misaligned(workspace, 16) ||
-                 workspaceBytes < (size_t)a.splits * 2 * cols * sizeof(float)))
+               dyStride, xStride, dxStride, (float*)workspace, splitsFor(rows, cols), {}};
+  size_t need = 0;
+  if (params && (vrLayerNormBackwardWorkspace(rows, cols, dtype, &need) != vrSuccess ||
+                 !workspace || misaligned(workspace, 16) || workspaceBytes < need))
     return vrInvalidArgument;
   return dispatch(dtype, weightType, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
     vrResult_t r = vrSuccess;
-    const uint64_t most = (uint64_t)kSMs * 8;
-    if (dx)
-      r = launch((const void*)&vrLnBackwardAny<T, W>, dim3((unsigned)(rows < most ? rows : most)),
-                 dim3(kRowThreads), 0, st, a);
+    const bool same = alike(dy, dyStride, x, xStride, es) && (!dx || alike(dx, dxStride, x, xStride, es));
+    if (!same || !backwardRows<T, W>(a, st, &r)) {
+      const uint64_t most = (uint64_t)kSMs * 8;
+      if (dx)
+        r = launch((const void*)&vrLnBackwardAny<T, W>,
+                   dim3((unsigned)(rows < most ? rows : most)), dim3(kRowThreads), 0, st, a);
+      if (r == vrSuccess && params)
+        r = launch((const void*)&vrLnColumns<T>, dim3((unsigned)((cols + 31) / 32), a.splits),
+                   dim3(32 * kColWarps), 0, st, a);
+    }
     if (r == vrSuccess && params)
-      r = launch((const void*)&vrLnColumns<T>, dim3((unsigned)((cols + 31) / 32), a.splits),
-                 dim3(32 * kColWarps), 0, st, a);
-    if (r == vrSuccess && params)
-      r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 255) / 256), 2), dim3(256), 0,
-                 st, a);
+      r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 31) / 32), 2), dim3(256), 0, st, a);
     return r;
   });
 }

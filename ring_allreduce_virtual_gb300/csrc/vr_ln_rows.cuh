@@ -305,6 +305,9 @@ inline int residentWarps(int regs, size_t smem, int threads) {
   return byShared < byRegs ? byShared : byRegs;
 }
 
+// Dynamic shared memory of a block, at most.
+constexpr size_t kMostShared = 200 * 1024;
+
 // Raises a kernel's limit of dynamic shared memory, once on each device.
 inline bool allowShared(const void* kernel) {
   constexpr int kSeen = 256;
@@ -316,8 +319,8 @@ inline bool allowShared(const void* kernel) {
   std::lock_guard<std::mutex> g(m);
   for (int i = 0; i < n; ++i)
     if (seen[i] == kernel && device[i] == dev) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) !=
-      cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kMostShared) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
