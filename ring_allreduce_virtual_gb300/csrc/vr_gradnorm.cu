@@ -2,36 +2,60 @@
 //
 //   N = |s| sqrt(sum_t sum_i g_ti^2),  out = g s min(1, max / N)
 //
-// for tensors of any sizes, types and alignments. A list is cut into tiles of
-// kTileBytes; block b of B takes the tiles [nt b / B, nt (b + 1) / B), which
-// may lie in several tensors, and leaves one partial sum for each tensor it
-// meets, in slot b + t: along a block's walk t grows, from one block to the
-// next b does, so every slot has one writer and the sums have one order (no
-// atomics: equal inputs give equal bits). The second kernel adds the slots up.
+// for tensors of any sizes, types and alignments. A list is cut into tiles, and
+// the tiles into units of consecutive ones: unit u of U takes the tiles [nt u / U,
+// nt (u + 1) / U), which may lie in several tensors, and leaves one partial sum
+// for each tensor it meets, in slot u + t: along a unit t grows, from one unit
+// to the next u does, so every slot has one writer and the sums have one order
+// (no atomics: equal inputs give equal bits). A second kernel adds the slots up.
+// Lists of up to 2 MiB are one launch of one cluster, whose slots lie in
+// shared memory.
 //
-// Both kernels are bound by HBM: the norm reads every element once (2 flop
-// each), clipping reads it once more and writes it.
-#include "vr_opcommon.cuh"
+// All of it is bound by HBM (2 or 3 flop an element). The norm reads every
+// element once; clipping reads it again, from L2 for what the first kernel read
+// last, and writes it. Measured on a GB300: the norms of 0.94 GB of bf16 in 288
+// tensors 139 us (1.0 of the measured copy peak, reads alone being a little
+// faster than copies); clipping 1.06 GB of float32 490 us and 1.15 GB of mixed
+// odd-sized tensors 532 us, 0.96 of what two reads and a write take at that peak.
+#include "vr_ln_rows.cuh"
 
 namespace {
 
 using namespace vrop;
+using vrln::cluster_rank;
+using vrln::cluster_sync;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kPacks = 4;  // 16-byte packs of a thread in flight
-constexpr int kTileBytes = kThreads * kPacks * 16;
-constexpr int kBlocks = kSMs * 4;
+// A kernel's threads, and the tile that they read at a time: PACKS 16-byte packs
+// each.
+template <int THREADS, int PACKS>
+struct Shape {
+  static constexpr int threads = THREADS, warps = THREADS / 32, packs = PACKS;
+  static constexpr int tileBytes = THREADS * PACKS * 16;
+};
+// Long lists: 5 blocks an SM for the sums. Scaling takes 2: with more, reads and
+// writes of more places alternate in HBM (2 / 4 / 5 blocks: 490 / 518 / 522 us for
+// 1.06 GB).
+using Long = Shape<256, 8>;
+constexpr int kSumBlocks = 5, kScaleBlocks = 2;
+constexpr int kBlocks = kSMs * kSumBlocks;
+// A unit is at least 8 tiles where a block has more than one unit. Several
+// units a block keep what all blocks read at a time together in memory: 532
+// us against 543 for 1.15 GB in one unit a block.
+constexpr int kUnitTiles = 8, kMostWaves = 8;
+// Short lists: one cluster.
+using Short = Shape<512, 4>;
+constexpr int kShortBlocks = 16, kShortTiles = 64;
+
 // Tensors of one launch. Their table lies in the kernel's parameter space
 // (32,764 bytes at most): nothing is copied to the device beforehand and the
 // caller's arrays are free on return. Longer lists take several launches.
-constexpr int kSmallList = 64;
+constexpr int kShortList = 64;
 constexpr int kLongList = 960;
 
 template <int CAP>
 struct Table {
   int nTensors;
-  int nBlocks;
+  int nUnits;
   uint32_t nTiles;
   uint32_t nSlots;    // of all launches of the call
   uint32_t slotBase;  // of this launch
@@ -58,18 +82,18 @@ __host__ __device__ inline uint64_t headOf(const void* p, uint64_t count, int es
   return h < count ? h : count;
 }
 
-inline uint64_t tilesOf(const void* p, uint64_t count, int es) {
+inline uint64_t tilesOf(const void* p, uint64_t count, int es, int tileBytes) {
   if (!count) return 0;
   const uint64_t body = (count - headOf(p, count, es)) * es;
-  return body ? (body + kTileBytes - 1) / kTileBytes : 1;
+  return body ? (body + tileBytes - 1) / tileBytes : 1;
 }
 
-// The first tile of block b, and the block that holds tile k.
-__host__ __device__ inline uint32_t firstTile(uint32_t nTiles, int nBlocks, int b) {
-  return (uint32_t)((uint64_t)nTiles * b / nBlocks);
+// The first tile of unit u, and the unit that holds tile k.
+__host__ __device__ inline uint32_t firstTile(uint32_t nTiles, int nUnits, int u) {
+  return (uint32_t)((uint64_t)nTiles * u / nUnits);
 }
-__device__ inline uint32_t blockOf(uint32_t nTiles, int nBlocks, uint32_t k) {
-  return (uint32_t)((((uint64_t)k + 1) * nBlocks - 1) / nTiles);
+__device__ inline uint32_t unitOf(uint32_t nTiles, int nUnits, uint32_t k) {
+  return (uint32_t)((((uint64_t)k + 1) * nUnits - 1) / nTiles);
 }
 
 // The tensor that tile k lies in: the last t with tile[t] <= k.
@@ -92,8 +116,41 @@ struct Sum2 {
     lo += (hi - (s - z)) + (x - z);
     hi = s;
   }
+  __device__ void add(const Sum2& b) {
+    add(b.hi);
+    lo += b.lo;
+  }
   __device__ double value() const { return (double)hi + (double)lo; }
 };
+
+// The sum over a block, the same in every thread; `buf` holds WARPS + 1 values.
+// Float pairs up to the warps' sums and one warp after that: this GPU adds
+// 64-bit numbers at a sixty-fourth of its 32-bit rate (64-bit sums in all
+// threads: 152 us instead of 141 for the norms of 0.94 GB).
+template <int WARPS>
+__device__ __forceinline__ double block_sum2(double s, double* buf) {
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    s = threadIdx.x < WARPS ? buf[threadIdx.x] : 0.0;
+#pragma unroll
+    for (int o = WARPS / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    if (threadIdx.x == 0) buf[WARPS] = s;
+  }
+  __syncthreads();
+  return buf[WARPS];
+}
+template <int WARPS>
+__device__ __forceinline__ double block_sum2(Sum2 v, double* buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    Sum2 w;
+    w.hi = __shfl_xor_sync(~0u, v.hi, o);
+    w.lo = __shfl_xor_sync(~0u, v.lo, o);
+    v.add(w);
+  }
+  return block_sum2<WARPS>(v.value(), buf);
+}
 
 template <typename T>
 __device__ __forceinline__ void squares(const uint4& v, float* acc, uint32_t& bits) {
@@ -116,33 +173,33 @@ __device__ __forceinline__ void squares(const uint4& v, float* acc, uint32_t& bi
 }
 
 __device__ __forceinline__ uint4 load16(const void* p) {
-  return __ldg(reinterpret_cast<const uint4*>(p));
+  return *reinterpret_cast<const uint4*>(p);
 }
 
 // A block's sum of squares of the tiles [k0, k1) of one tensor, the same value in
 // every thread.
-template <typename T>
+template <typename S, typename T>
 __device__ double sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1, double* buf) {
   constexpr int V = 16 / (int)sizeof(T);
-  constexpr uint64_t E = kTileBytes / sizeof(T);
+  constexpr uint64_t E = S::tileBytes / sizeof(T);
   const uint64_t head = headOf(g, count, (int)sizeof(T)), body = count - head;
-  const T* p = g + head;
-  uint32_t bits = 0;
-  Sum2 sum;
   if constexpr (sizeof(T) < 8) {
+    const T* p = g + head;
+    uint32_t bits = 0;
+    Sum2 sum;
     for (uint32_t k = k0; k < k1; ++k) {
       const uint64_t left = body - k * E;
       const T* q = p + k * E;
       float acc[2] = {0.f, 0.f};
       if (left >= E) {
-        uint4 v[kPacks];
+        uint4 v[S::packs];
 #pragma unroll
-        for (int i = 0; i < kPacks; ++i) v[i] = load16(q + (threadIdx.x + i * kThreads) * V);
+        for (int i = 0; i < S::packs; ++i) v[i] = load16(q + (threadIdx.x + i * S::threads) * V);
 #pragma unroll
-        for (int i = 0; i < kPacks; ++i) squares<T>(v[i], acc, bits);
+        for (int i = 0; i < S::packs; ++i) squares<T>(v[i], acc, bits);
       } else {
         const int packs = (int)(left / V);
-        for (int i = threadIdx.x; i < packs; i += kThreads)
+        for (int i = threadIdx.x; i < packs; i += S::threads)
           squares<T>(load16(q + (uint64_t)i * V), acc, bits);
         const int at = packs * V + threadIdx.x;
         if (at < (int)left) {
@@ -158,7 +215,7 @@ __device__ double sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1,
       sum.add(x * x);
       bits |= x != 0.f;
     }
-    const double s = block_sum<kWarps>(sum.value(), buf);
+    const double s = block_sum2<S::warps>(sum, buf);
     // The squares of 32-bit floats and of bfloat16 leave the range of a float
     // long before their sum leaves that of a double. Where they did (the sum
     // is infinite, or so small that squares went below the smallest float),
@@ -166,87 +223,118 @@ __device__ double sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1,
     if (std::is_same_v<T, __half>) return s;
     const bool small = s < 0x1p-90;
     if (s < 0x1p120 && !(small && __syncthreads_or(bits != 0))) return s;
+    __syncthreads();  // before `buf` is used again
   }
-  __syncthreads();  // before `buf` is used again
   double d = 0;
   const uint64_t from = k0 ? head + k0 * E : 0, end = head + k1 * E, to = end < count ? end : count;
-  for (uint64_t i = from + threadIdx.x; i < to; i += kThreads) {
+  for (uint64_t i = from + threadIdx.x; i < to; i += S::threads) {
     const double x = to_f64(g[i]);
     d = fma(x, x, d);
   }
-  return block_sum<kWarps>(d, buf);
+  return block_sum2<S::warps>(warp_sum(d), buf);
 }
 
-template <int CAP>
+template <typename S, int CAP>
 __device__ double sumTensor(const Table<CAP>& a, int t, uint32_t k0, uint32_t k1, double* buf) {
   if (k0 >= k1) return 0.0;
+  const void* g = a.in[t];
+  const uint64_t n = a.count[t];
   switch (a.type[t]) {
-    case vrFloat16: return sumTiles((const __half*)a.in[t], a.count[t], k0, k1, buf);
-    case vrBfloat16: return sumTiles((const __nv_bfloat16*)a.in[t], a.count[t], k0, k1, buf);
-    case vrFloat32: return sumTiles((const float*)a.in[t], a.count[t], k0, k1, buf);
-    default: return sumTiles((const double*)a.in[t], a.count[t], k0, k1, buf);
+    case vrFloat16: return sumTiles<S>((const __half*)g, n, k0, k1, buf);
+    case vrBfloat16: return sumTiles<S>((const __nv_bfloat16*)g, n, k0, k1, buf);
+    case vrFloat32: return sumTiles<S>((const float*)g, n, k0, k1, buf);
+    default: return sumTiles<S>((const double*)g, n, k0, k1, buf);
   }
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) vrNormPartials(const __grid_constant__ Table<CAP> a) {
-  __shared__ double buf[2][kWarps];
-  const int b = blockIdx.x;
-  const uint32_t k0 = firstTile(a.nTiles, a.nBlocks, b), k1 = firstTile(a.nTiles, a.nBlocks, b + 1);
-  // This block owns the slots b + t from its first tensor to the next
-  // block's first; a tensor without a tile in here gets a zero.
-  const int t0 = b ? tensorOf(a, k0) : 0;
-  const int t1 = b + 1 < a.nBlocks ? tensorOf(a, k1) : a.nTensors - 1;
+// The partial sums of unit u: put(slot, sum) for each of its slots, u + t from
+// its first tensor to the next unit's first. A tensor without a tile in the
+// unit gets a zero.
+template <typename S, int CAP, typename Put>
+__device__ __forceinline__ void sumUnit(const Table<CAP>& a, int u, double (*buf)[S::warps + 1],
+                                        int& turn, Put put) {
+  const uint32_t k0 = firstTile(a.nTiles, a.nUnits, u), k1 = firstTile(a.nTiles, a.nUnits, u + 1);
+  const int t0 = u ? tensorOf(a, k0) : 0;
+  const int t1 = u + 1 < a.nUnits ? tensorOf(a, k1) : a.nTensors - 1;
   for (int t = t0; t <= t1; ++t) {
     const uint32_t first = a.tile[t], last = a.tile[t + 1];
     const uint32_t x = k0 > first ? k0 : first, y = k1 < last ? k1 : last;
-    const double s = sumTensor(a, t, x - first, y > x ? y - first : x - first, buf[t & 1]);
-    if (threadIdx.x == 0) a.slots[a.slotBase + b + t] = s;
-    __syncthreads();
+    const double s = sumTensor<S>(a, t, x - first, y > x ? y - first : x - first, buf[turn]);
+    turn ^= 1;
+    put(u + t, s);
   }
 }
 
-// The sum of all slots, the same in every thread.
 template <int CAP>
-__device__ double sumSlots(const Table<CAP>& a, double* buf) {
+__global__ void __launch_bounds__(Long::threads, kSumBlocks)
+    vrNormPartials(const __grid_constant__ Table<CAP> a) {
+  __shared__ double buf[2][Long::warps + 1];
+  launch_dependents();
+  int turn = 0;
+  for (int u = blockIdx.x; u < a.nUnits; u += gridDim.x)
+    sumUnit<Long>(a, u, buf, turn, [&](int slot, double s) {
+      if (threadIdx.x == 0) a.slots[a.slotBase + slot] = s;
+    });
+}
+
+// The sum of n slots, the same in every thread.
+template <typename S>
+__device__ double sumSlots(const double* slots, uint32_t n, double* buf) {
   double s = 0;
-  for (uint32_t i = threadIdx.x; i < a.nSlots; i += kThreads) s += a.slots[i];
-  return block_sum<kWarps>(s, buf);
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < n; i += S::threads) s += slots[i];
+  return block_sum2<S::warps>(warp_sum(s), buf);
 }
 
-// The norms: block 0 the whole list's (in the call's last launch), warp w of
-// all blocks those of the tensors w, w + warps, ...
+// Tensor t's sum of squares from the slots of one launch, in a warp.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) vrNormFinish(const __grid_constant__ Table<CAP> a) {
-  __shared__ double buf[kWarps];
+__device__ double tensorSum(const Table<CAP>& a, const double* slots, int t) {
+  double s = 0;
+  if (a.tile[t] < a.tile[t + 1]) {
+    const uint32_t u0 = unitOf(a.nTiles, a.nUnits, a.tile[t]);
+    const uint32_t u1 = unitOf(a.nTiles, a.nUnits, a.tile[t + 1] - 1);
+    for (uint32_t u = u0 + (threadIdx.x & 31); u <= u1; u += 32) s += slots[u + t];
+  }
+  return warp_sum(s);
+}
+
+// The norms: block 0 the whole list's (in the call's last launch), the other
+// blocks' warps one tensor's each.
+template <int CAP>
+__global__ void __launch_bounds__(Long::threads)
+    vrNormFinish(const __grid_constant__ Table<CAP> a) {
+  __shared__ double buf[Long::warps + 1];
+  wait_for_previous();
   const double scale = fabs((double)a.scale);
-  if (blockIdx.x == 0 && a.norm) {
-    const double s = sumSlots(a, buf);
+  if (blockIdx.x == 0) {
+    if (!a.norm) return;
+    const double s = sumSlots<Long>(a.slots, a.nSlots, buf);
     if (threadIdx.x == 0) *a.norm = (float)(scale * sqrt(s));
+    return;
   }
-  if (!a.tensorNorms) return;
-  const int lane = threadIdx.x & 31;
-  for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.nTensors; t += gridDim.x * kWarps) {
-    double s = 0;
-    if (a.tile[t] < a.tile[t + 1]) {
-      const uint32_t b0 = blockOf(a.nTiles, a.nBlocks, a.tile[t]);
-      const uint32_t b1 = blockOf(a.nTiles, a.nBlocks, a.tile[t + 1] - 1);
-      for (uint32_t b = b0 + lane; b <= b1; b += 32) s += a.slots[a.slotBase + b + t];
-    }
-    s = warp_sum(s);
-    if (lane == 0) a.tensorNorms[a.tensorBase + t] = (float)(scale * sqrt(s));
-  }
+  const int t = (blockIdx.x - 1) * Long::warps + (threadIdx.x >> 5);
+  if (t >= a.nTensors) return;
+  const double s = tensorSum(a, a.slots + a.slotBase, t);
+  if ((threadIdx.x & 31) == 0) a.tensorNorms[a.tensorBase + t] = (float)(scale * sqrt(s));
 }
 
 // One tile of out = g * factor: 16-byte packs where g and out lie alike modulo
 // 16 bytes, elements elsewhere. Each product is rounded once.
-template <typename T, typename F>
+template <typename S, typename T, typename F>
 __device__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F factor) {
   constexpr int V = 16 / (int)sizeof(T);
-  constexpr uint64_t E = kTileBytes / sizeof(T);
+  constexpr uint64_t E = S::tileBytes / sizeof(T);
   auto mul = [factor](T x) -> T {
     if constexpr (sizeof(T) == 8) return x * factor;
     else return from_f32<T>(to_f32(x) * factor);
+  };
+  auto mulPack = [&](uint4 v) {
+    T e[V];
+    memcpy(e, &v, 16);
+#pragma unroll
+    for (int c = 0; c < V; ++c) e[c] = mul(e[c]);
+    memcpy(&v, e, 16);
+    return v;
   };
   const uint64_t head = headOf(g, count, (int)sizeof(T)), body = count - head;
   if (k == 0 && threadIdx.x < head) out[threadIdx.x] = mul(g[threadIdx.x]);
@@ -255,65 +343,96 @@ __device__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F fact
   const T* p = g + head + k * E;
   T* q = out + head + k * E;
   const int packs = ((uintptr_t)q & 15) == 0 ? n / V : 0;
+  if (packs == S::tileBytes / 16) {
+    uint4 v[S::packs];
 #pragma unroll
-  for (int j = 0; j < kPacks; ++j) {
-    const int i = threadIdx.x + j * kThreads;
-    if (i < packs) {
-      uint4 v = *reinterpret_cast<const uint4*>(p + i * V);
-      T e[V];
-      memcpy(e, &v, 16);
+    for (int j = 0; j < S::packs; ++j) v[j] = load16(p + (threadIdx.x + j * S::threads) * V);
 #pragma unroll
-      for (int c = 0; c < V; ++c) e[c] = mul(e[c]);
-      memcpy(&v, e, 16);
-      *reinterpret_cast<uint4*>(q + i * V) = v;
-    }
+    for (int j = 0; j < S::packs; ++j)
+      *reinterpret_cast<uint4*>(q + (threadIdx.x + j * S::threads) * V) = mulPack(v[j]);
+    return;
   }
-  for (int i = packs * V + threadIdx.x; i < n; i += kThreads) q[i] = mul(p[i]);
+  for (int i = threadIdx.x; i < packs; i += S::threads)
+    *reinterpret_cast<uint4*>(q + i * V) = mulPack(load16(p + i * V));
+  for (int i = packs * V + threadIdx.x; i < n; i += S::threads) q[i] = mul(p[i]);
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) vrClip(const __grid_constant__ Table<CAP> a) {
-  __shared__ double buf[kWarps];
-  const double norm = fabs((double)a.scale) * sqrt(sumSlots(a, buf));
-  // A norm that is not finite clips nothing: the caller sees it and drops
-  // the step, and the gradients still show where it came from.
-  const bool clips = norm > (double)a.maxNorm && isfinite(norm);
-  const double factor = (double)a.scale * (clips ? (double)a.maxNorm / norm : 1.0);
-  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const int b = blockIdx.x;
-  const uint32_t k0 = firstTile(a.nTiles, a.nBlocks, b), k1 = firstTile(a.nTiles, a.nBlocks, b + 1);
-  if (k0 == k1) return;
-  int t = tensorOf(a, k0);
-  for (uint32_t k = k0; k < k1; ++k) {
-    while (k >= a.tile[t + 1]) ++t;
-    const uint32_t at = k - a.tile[t];
-    const void* g = a.in[t];
-    void* o = a.out[t];
-    switch (a.type[t]) {
-      case vrFloat16: scaleTile((const __half*)g, (__half*)o, a.count[t], at, (float)factor); break;
-      case vrBfloat16:
-        scaleTile((const __nv_bfloat16*)g, (__nv_bfloat16*)o, a.count[t], at, (float)factor);
-        break;
-      case vrFloat32: scaleTile((const float*)g, (float*)o, a.count[t], at, (float)factor); break;
-      default: scaleTile((const double*)g, (double*)o, a.count[t], at, factor); break;
-    }
+template <typename S, int CAP>
+__device__ __forceinline__ void scaleAt(const Table<CAP>& a, int t, uint32_t k, double factor) {
+  const void* g = a.in[t];
+  void* o = a.out[t];
+  const uint64_t n = a.count[t];
+  const float f = (float)factor;
+  k -= a.tile[t];
+  switch (a.type[t]) {
+    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, k, f);
+    case vrBfloat16: return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, k, f);
+    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, k, f);
+    default: return scaleTile<S>((const double*)g, (double*)o, n, k, factor);
   }
+}
+
+// What the gradients are multiplied by. A norm that is not finite clips nothing:
+// the caller sees it and drops the step, and the gradients still show where it
+// came from.
+template <int CAP>
+__device__ __forceinline__ double factorFor(const Table<CAP>& a, double norm) {
+  const bool clips = norm > (double)a.maxNorm && isfinite(norm);
+  return (double)a.scale * (clips ? (double)a.maxNorm / norm : 1.0);
+}
+
+// Every block adds the slots up for itself, then takes tiles in turn, from the
+// list's end to its start: what the first kernel read last is still in L2.
+template <int CAP>
+__global__ void __launch_bounds__(Long::threads, kScaleBlocks)
+    vrClip(const __grid_constant__ Table<CAP> a) {
+  __shared__ double buf[Long::warps + 1];
+  wait_for_previous();
+  const double norm = fabs((double)a.scale) * sqrt(sumSlots<Long>(a.slots, a.nSlots, buf));
+  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
+  const double factor = factorFor(a, norm);
+  for (uint32_t i = blockIdx.x; i < a.nTiles; i += gridDim.x) {
+    const uint32_t k = a.nTiles - 1 - i;
+    scaleAt<Long>(a, tensorOf(a, k), k, factor);
+  }
+}
+
+// A short list in one launch: a unit for each block of a cluster, the slots in
+// every block's shared memory. Where `out` is there, each block scales its unit.
+__global__ void __launch_bounds__(Short::threads)
+    vrShortList(const __grid_constant__ Table<kShortList> a) {
+  __shared__ double slots[kShortBlocks + kShortList];
+  __shared__ double buf[2][Short::warps + 1];
+  const int u = (int)cluster_rank();
+  int turn = 0;
+  cluster_sync();  // every block's slots are there
+  sumUnit<Short>(a, u, buf, turn, [&](int slot, double s) {
+    if (threadIdx.x < a.nUnits) {
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&slots[slot])), "r"(threadIdx.x));
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(s) : "memory");
+    }
+  });
+  cluster_sync();
+  const double scale = fabs((double)a.scale);
+  const double norm = scale * sqrt(sumSlots<Short>(slots, a.nUnits + a.nTensors - 1, buf[turn]));
+  if (u == 0) {
+    if (a.norm && threadIdx.x == 0) *a.norm = (float)norm;
+    if (a.tensorNorms)
+      for (int t = threadIdx.x >> 5; t < a.nTensors; t += Short::warps) {
+        const double s = tensorSum(a, slots, t);
+        if ((threadIdx.x & 31) == 0) a.tensorNorms[t] = (float)(scale * sqrt(s));
+      }
+  }
+  if (a.maxNorm < 0.f) return;  // the norm alone
+  const double factor = factorFor(a, norm);
+  const uint32_t k1 = firstTile(a.nTiles, a.nUnits, u + 1);
+  for (uint32_t k = firstTile(a.nTiles, a.nUnits, u); k < k1; ++k)
+    scaleAt<Short>(a, tensorOf(a, k), k, factor);
 }
 
 // ------------------------------------------------------------------ host
-int blocksFor(uint64_t tiles) { return tiles < (uint64_t)kBlocks ? (tiles ? (int)tiles : 1) : kBlocks; }
-
-// Slots of a launch of T tensors on B blocks: b + t runs from 0 to
-// (B - 1) + (T - 1).
-uint64_t slotsBound(int nTensors) {
-  uint64_t s = 0;
-  for (int at = 0; at < nTensors; at += kLongList) {
-    const int n = nTensors - at < kLongList ? nTensors - at : kLongList;
-    s += (uint64_t)kBlocks + n;
-  }
-  return s;
-}
-
 struct Call {
   const void* const* in;
   void* const* out;  // NULL: the norm alone
@@ -327,8 +446,14 @@ struct Call {
   cudaStream_t stream;
 };
 
+// Slots of a launch of T tensors in U units: u + t runs from 0 to (U - 1) + (T - 1).
+uint64_t slotsBound(int nTensors) {
+  const uint64_t launches = ((uint64_t)nTensors + kLongList - 1) / kLongList;
+  return launches * (uint64_t)(kBlocks * kMostWaves) + (uint64_t)nTensors;
+}
+
 template <int CAP>
-void fill(const Call& c, int at, int n, Table<CAP>* a) {
+void fill(const Call& c, int at, int n, int tileBytes, Table<CAP>* a) {
   uint64_t tiles = 0;
   for (int i = 0; i < n; ++i) {
     const int t = at + i;
@@ -337,22 +462,49 @@ void fill(const Call& c, int at, int n, Table<CAP>* a) {
     a->count[i] = c.counts[t];
     a->type[i] = (uint8_t)c.types[t];
     a->tile[i] = (uint32_t)tiles;
-    tiles += tilesOf(c.in[t], c.counts[t], sizeOfType(c.types[t]));
+    tiles += tilesOf(c.in[t], c.counts[t], sizeOfType(c.types[t]), tileBytes);
   }
   a->tile[n] = (uint32_t)tiles;
   a->nTensors = n;
   a->nTiles = (uint32_t)tiles;
-  a->nBlocks = blocksFor(tiles);
   a->tensorBase = at;
   a->scale = c.scale;
-  a->maxNorm = c.maxNorm;
+  a->maxNorm = c.out ? c.maxNorm : -1.f;
   a->slots = c.slots;
-  a->norm = nullptr;
+  a->norm = c.norm;
   a->tensorNorms = c.tensorNorms;
 }
 
+// Units of a long list's launch: one a block, or whole waves of them.
+int unitsFor(uint32_t tiles) {
+  if (tiles <= (uint32_t)kBlocks) return tiles ? (int)tiles : 1;
+  const uint32_t waves = tiles / (uint32_t)(kBlocks * kUnitTiles);
+  return kBlocks * (int)(waves < 1 ? 1 : waves > kMostWaves ? kMostWaves : waves);
+}
+
+// Every tile of a short list fits the cluster's blocks a few times over.
+bool isShort(const Call& c) {
+  if (c.nTensors > kShortList) return false;
+  uint64_t tiles = 0;
+  for (int t = 0; t < c.nTensors; ++t)
+    tiles += tilesOf(c.in[t], c.counts[t], sizeOfType(c.types[t]), Short::tileBytes);
+  return tiles <= kShortTiles;
+}
+
+vrResult_t runShort(const Call& c) {
+  Table<kShortList> a;
+  fill(c, 0, c.nTensors, Short::tileBytes, &a);
+  int blocks = 1;
+  while (blocks < kShortBlocks && (uint32_t)blocks < a.nTiles) blocks *= 2;
+  a.nUnits = blocks;
+  a.nSlots = a.slotBase = 0;
+  const void* k = (const void*)&vrShortList;
+  if (!vrln::allowLargeClusters(k)) return vrCudaError;
+  return launch(k, dim3(blocks), dim3(Short::threads), 0, c.stream, a, blocks);
+}
+
 template <int CAP>
-vrResult_t runCall(const Call& c) {
+vrResult_t runLong(const Call& c) {
   Table<CAP> a;
   const int launches = (c.nTensors + CAP - 1) / CAP;
   uint32_t slots = 0;
@@ -360,24 +512,32 @@ vrResult_t runCall(const Call& c) {
     uint32_t base = 0;
     for (int l = 0; l < launches; ++l) {
       const int at = l * CAP, n = c.nTensors - at < CAP ? c.nTensors - at : CAP;
-      if (pass == 0 || launches > 1) fill<CAP>(c, at, n, &a);
+      if (pass == 0 || launches > 1) {
+        fill(c, at, n, Long::tileBytes, &a);
+        a.nUnits = unitsFor(a.nTiles);
+      }
       a.slotBase = base;
       a.nSlots = slots;
-      base += (uint32_t)(a.nBlocks + n - 1);
+      base += (uint32_t)(a.nUnits + n - 1);
       const void* kernel;
-      int blocks = a.nBlocks;
+      int blocks;
       if (pass == 0) {
         kernel = (const void*)&vrNormPartials<CAP>;
+        blocks = a.nUnits < kBlocks ? a.nUnits : kBlocks;
       } else {
-        if (l == launches - 1) a.norm = c.norm;
+        if (l < launches - 1) a.norm = nullptr;
         if (c.out) {
           kernel = (const void*)&vrClip<CAP>;
+          blocks = a.nTiles < kSMs * kScaleBlocks ? (int)a.nTiles : kSMs * kScaleBlocks;
+          if (!blocks) blocks = 1;
         } else {
           kernel = (const void*)&vrNormFinish<CAP>;
-          blocks = c.tensorNorms ? (n + kWarps - 1) / kWarps : 1;
+          blocks = 1 + (c.tensorNorms ? (n + Long::warps - 1) / Long::warps : 0);
         }
       }
-      const vrResult_t r = launch(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, c.stream, a);
+      // The second pass's first kernel may start while the first pass ends.
+      const vrResult_t r = launch(kernel, dim3((unsigned)blocks), dim3(Long::threads), 0, c.stream,
+                                  a, 1, pass == 1 && l == 0);
       if (r != vrSuccess) return r;
     }
     slots = base;
@@ -392,8 +552,8 @@ vrResult_t checkList(const void* const* in, const size_t* counts, const vrDataTy
     const int es = elemSizeOf(types[t]);
     if (!es || (counts[t] && (!in[t] || misaligned(in[t], es)))) return vrInvalidArgument;
     if (counts[t] > ((size_t)1 << 48)) return vrInvalidArgument;
-    tiles += counts[t] ? tilesOf(in[t], counts[t], es) : 0;
-    if (tiles >= 0xffffffffull) return vrInvalidArgument;
+    tiles += tilesOf(in[t], counts[t], es, Long::tileBytes);
+    if (tiles >= 0x7fffffffull) return vrInvalidArgument;
   }
   return vrSuccess;
 }
@@ -402,7 +562,8 @@ vrResult_t runChecked(const Call& c, const void* workspace, size_t workspaceByte
   if (!workspace || misaligned(workspace, 16) ||
       workspaceBytes < slotsBound(c.nTensors) * sizeof(double))
     return vrInvalidArgument;
-  return c.nTensors <= kSmallList ? runCall<kSmallList>(c) : runCall<kLongList>(c);
+  if (isShort(c)) return runShort(c);
+  return c.nTensors <= kShortList ? runLong<kShortList>(c) : runLong<kLongList>(c);
 }
 
 }  // namespace

@@ -261,6 +261,7 @@ constexpr int kColWarps = 8;
 template <typename T>
 __global__ void __launch_bounds__(32 * kColWarps) vrLnColumns(const __grid_constant__ BwdArgs a) {
   __shared__ float buf[2][kColWarps][32];
+  launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint64_t col = (uint64_t)blockIdx.x * 32 + lane;
   const uint64_t r0 = a.rows * blockIdx.y / a.splits, r1 = a.rows * (blockIdx.y + 1) / a.splits;
@@ -293,6 +294,7 @@ __global__ void __launch_bounds__(256) vrLnJoin(const __grid_constant__ BwdArgs 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint64_t col = (uint64_t)blockIdx.x * 32 + lane;
   W* out = static_cast<W*>(blockIdx.y ? a.db : a.dw);
+  wait_for_previous();
   if (!out) return;
   float s = 0.f;
   if (col < a.cols) {
@@ -476,6 +478,7 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
     op += ROWS * oStep;
     oo += ROWS * oStep;
   }
+  launch_dependents();
   if (!a.dw && !a.db) return;
   copies_wait<0>();
   // The groups' sums are added up in shared memory, in the groups' order, so
@@ -779,7 +782,8 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
                    dim3(32 * kColWarps), 0, st, a);
     }
     if (r == vrSuccess && params)
-      r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 31) / 32), 2), dim3(256), 0, st, a);
+      r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 31) / 32), 2), dim3(256), 0, st, a,
+                 1, true);
     return r;
   });
 }

@@ -308,8 +308,8 @@ inline int residentWarps(int regs, size_t smem, int threads) {
 // Dynamic shared memory of a block, at most.
 constexpr size_t kMostShared = 200 * 1024;
 
-// Raises a kernel's limit of dynamic shared memory, once on each device.
-inline bool allowShared(const void* kernel) {
+// Sets an attribute of a kernel, once on each device.
+inline bool setOnce(const void* kernel, cudaFuncAttribute what, int value) {
   constexpr int kSeen = 256;
   static std::mutex m;
   static const void* seen[kSeen];
@@ -319,13 +319,18 @@ inline bool allowShared(const void* kernel) {
   std::lock_guard<std::mutex> g(m);
   for (int i = 0; i < n; ++i)
     if (seen[i] == kernel && device[i] == dev) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)kMostShared) != cudaSuccess) {
+  if (cudaFuncSetAttribute(kernel, what, value) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
   if (n < kSeen) seen[n] = kernel, device[n++] = dev;
   return true;
+}
+inline bool allowShared(const void* kernel) {
+  return setOnce(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostShared);
+}
+inline bool allowLargeClusters(const void* kernel) {
+  return setOnce(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 // How rows of `cols` elements are laid over threads: PACKS packs for each

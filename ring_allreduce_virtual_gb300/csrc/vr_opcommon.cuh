@@ -80,23 +80,38 @@ __device__ __forceinline__ A block_sum(A v, A* buf) {
   return v;
 }
 
+// A kernel may let the next one on its stream start (all of its blocks being
+// resident or done); the next one, launched `early`, waits for its end, and for
+// all it wrote, before it reads any of it.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Launch of `kernel` with one by-value argument struct, in clusters of `ctas`.
 template <typename Args>
 inline vrResult_t launch(const void* kernel, dim3 grid, dim3 block, size_t smem,
-                         cudaStream_t stream, Args& args, int ctas = 1) {
+                         cudaStream_t stream, Args& args, int ctas = 1, bool early = false) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
   if (ctas > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)ctas;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (early) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
   }
   void* a[] = {&args};
   if (cudaLaunchKernelExC(&cfg, kernel, a) != cudaSuccess) {
