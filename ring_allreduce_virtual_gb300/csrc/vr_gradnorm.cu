@@ -8,7 +8,7 @@
 // for each tensor it meets, in slot u + t: along a unit t grows, from one unit
 // to the next u does, so every slot has one writer and the sums have one order
 // (no atomics: equal inputs give equal bits). A second kernel adds the slots up.
-// Lists of up to 2 MiB are one launch of one cluster, whose slots lie in
+// Lists of up to 1 MiB are one launch of one cluster, whose slots lie in
 // shared memory.
 //
 // All of it is bound by HBM (2 or 3 flop an element). The norm reads every
@@ -24,27 +24,31 @@ namespace {
 using namespace vrop;
 using vrln::cluster_rank;
 using vrln::cluster_sync;
+using vrop::warp_sum;
 
-// A kernel's threads, and the tile that they read at a time: PACKS 16-byte packs
-// each.
+// Who works on a unit (a block, or a warp), and the tile that it reads at a time:
+// PACKS 16-byte packs a thread.
 template <int THREADS, int PACKS>
-struct Shape {
-  static constexpr int threads = THREADS, warps = THREADS / 32, packs = PACKS;
-  static constexpr int tileBytes = THREADS * PACKS * 16;
+struct Team {
+  enum { threads = THREADS, warps = THREADS / 32, packs = PACKS, tileBytes = THREADS * PACKS * 16 };
+  static __device__ __forceinline__ int id() {
+    return THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+  }
 };
 // Long lists: 5 blocks an SM for the sums. Scaling takes 2: with more, reads and
 // writes of more places alternate in HBM (2 / 4 / 5 blocks: 490 / 518 / 522 us for
 // 1.06 GB).
-using Long = Shape<256, 8>;
+using Block = Team<256, 8>;
 constexpr int kSumBlocks = 5, kScaleBlocks = 2;
 constexpr int kBlocks = kSMs * kSumBlocks;
 // A unit is at least 8 tiles where a block has more than one unit. Several
 // units a block keep what all blocks read at a time together in memory: 532
 // us against 543 for 1.15 GB in one unit a block.
 constexpr int kUnitTiles = 8, kMostWaves = 8;
-// Short lists: one cluster.
-using Short = Shape<512, 4>;
-constexpr int kShortBlocks = 16, kShortTiles = 64;
+// Short lists: the warps of one cluster.
+using Warp = Team<32, 8>;
+constexpr int kShortBlocks = 16, kShortWarps = 16, kShortUnits = kShortBlocks * kShortWarps;
+constexpr int kShortTiles = kShortUnits;
 
 // Tensors of one launch. Their table lies in the kernel's parameter space
 // (32,764 bytes at most): nothing is copied to the device beforehand and the
@@ -53,7 +57,7 @@ constexpr int kShortList = 64;
 constexpr int kLongList = 960;
 
 template <int CAP>
-struct Table {
+struct alignas(8) Table {
   int nTensors;
   int nUnits;
   uint32_t nTiles;
@@ -62,7 +66,7 @@ struct Table {
   int tensorBase;
   float scale;
   float maxNorm;
-  double* slots;
+  uint64_t* slots;
   float* norm;
   float* tensorNorms;
   const void* in[CAP];
@@ -89,16 +93,19 @@ inline uint64_t tilesOf(const void* p, uint64_t count, int es, int tileBytes) {
 }
 
 // The first tile of unit u, and the unit that holds tile k.
+__host__ __device__ inline uint32_t divide(uint64_t a, uint32_t b) {
+  return a >> 32 ? (uint32_t)(a / b) : (uint32_t)a / b;  // 64-bit division is slow
+}
 __host__ __device__ inline uint32_t firstTile(uint32_t nTiles, int nUnits, int u) {
-  return (uint32_t)((uint64_t)nTiles * u / nUnits);
+  return divide((uint64_t)nTiles * u, nUnits);
 }
 __device__ inline uint32_t unitOf(uint32_t nTiles, int nUnits, uint32_t k) {
-  return (uint32_t)((((uint64_t)k + 1) * nUnits - 1) / nTiles);
+  return divide(((uint64_t)k + 1) * nUnits - 1, nTiles);
 }
 
 // The tensor that tile k lies in: the last t with tile[t] <= k.
-template <int CAP>
-__device__ inline int tensorOf(const Table<CAP>& a, uint32_t k) {
+template <typename A>
+__device__ inline int tensorOf(const A& a, uint32_t k) {
   int lo = 0, hi = a.nTensors;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -108,40 +115,25 @@ __device__ inline int tensorOf(const Table<CAP>& a, uint32_t k) {
 }
 
 // A sum in two floats: hi + lo, the rounding errors of hi caught exactly
-// (Knuth's two-sum), so that a thread's long run costs no precision.
+// (Knuth's two-sum), so that a long run costs no precision. This GPU works on
+// 64-bit numbers at a sixty-fourth of its 32-bit rate: with them, a square root,
+// a division and the sums over a block were 5 of the 10 us of a small call.
 struct Sum2 {
   float hi = 0.f, lo = 0.f;
-  __device__ void add(float x) {
+  __device__ __forceinline__ void add(float x) {
     const float s = hi + x, z = s - hi;
     lo += (hi - (s - z)) + (x - z);
     hi = s;
   }
-  __device__ void add(const Sum2& b) {
+  __device__ __forceinline__ void add(const Sum2& b) {
     add(b.hi);
     lo += b.lo;
   }
-  __device__ double value() const { return (double)hi + (double)lo; }
+  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
 
-// The sum over a block, the same in every thread; `buf` holds WARPS + 1 values.
-// Float pairs up to the warps' sums and one warp after that: this GPU adds
-// 64-bit numbers at a sixty-fourth of its 32-bit rate (64-bit sums in all
-// threads: 152 us instead of 141 for the norms of 0.94 GB).
-template <int WARPS>
-__device__ __forceinline__ double block_sum2(double s, double* buf) {
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    s = threadIdx.x < WARPS ? buf[threadIdx.x] : 0.0;
-#pragma unroll
-    for (int o = WARPS / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    if (threadIdx.x == 0) buf[WARPS] = s;
-  }
-  __syncthreads();
-  return buf[WARPS];
-}
-template <int WARPS>
-__device__ __forceinline__ double block_sum2(Sum2 v, double* buf) {
+// The sum over a warp, the same bits in every lane.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     Sum2 w;
@@ -149,7 +141,98 @@ __device__ __forceinline__ double block_sum2(Sum2 v, double* buf) {
     w.lo = __shfl_xor_sync(~0u, v.lo, o);
     v.add(w);
   }
-  return block_sum2<WARPS>(v.value(), buf);
+  // hi + lo are the same in all lanes, but lo's roundings go by the order
+  v.hi = __shfl_sync(~0u, v.hi, 0);
+  v.lo = __shfl_sync(~0u, v.lo, 0);
+  return v;
+}
+
+// A sum of squares as a slot holds it: two floats, hi in the upper word, where it
+// is zero or within [2^-90, 2^100] (the sum of all slots then fits a float), else
+// a double with the sign bit set.
+constexpr float kLeast = 0x1p-90f, kMost = 0x1p100f;
+__device__ __forceinline__ uint64_t slotOf(const Sum2& v) {
+  return (uint64_t)__float_as_uint(v.hi) << 32 | __float_as_uint(v.lo);
+}
+__device__ __forceinline__ uint64_t slotOf(double d) {
+  return (uint64_t)__double_as_longlong(d) | 1ull << 63;
+}
+
+// Slots added up: the pairs, and the doubles apart.
+struct Total {
+  Sum2 pair;
+  double rest = 0;
+  bool wide = false;
+  __device__ __forceinline__ void add(uint64_t slot) {
+    if (slot >> 63) {
+      wide = true;
+      rest += __longlong_as_double((long long)(slot & ~(1ull << 63)));
+    } else {
+      Sum2 v;
+      v.hi = __uint_as_float((uint32_t)(slot >> 32));
+      v.lo = __uint_as_float((uint32_t)slot);
+      pair.add(v);
+    }
+  }
+  __device__ __forceinline__ double value() const { return pair.value() + rest; }
+  // |scale| sqrt(sum)
+  __device__ __forceinline__ float norm(float scale) const {
+    if (!wide) {
+      const float h = pair.hi + pair.lo, l = (pair.hi - h) + pair.lo;
+      float r = sqrtf(h);
+      if (r > 0.f) r += (fmaf(-r, r, h) + l) / (2.f * r);
+      r *= fabsf(scale);
+      if (r == 0.f ? h == 0.f || scale == 0.f : r >= 0x1p-100f && r <= 0x1p120f) return r;
+    }
+    return (float)wideNorm(scale);
+  }
+  __device__ double wideNorm(float scale) const { return fabs((double)scale) * sqrt(value()); }
+};
+
+// Sums over a team, the same in every thread. `buf` holds a block's warps + 1
+// values; it may be used again after a barrier.
+template <typename S>
+__device__ __forceinline__ Sum2 team_sum(Sum2 v, uint64_t* buf) {
+  v = warp_sum(v);
+  if constexpr (S::warps > 1) {
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = slotOf(v);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      Total t;
+      if (threadIdx.x < S::warps) t.pair = {__uint_as_float(buf[threadIdx.x] >> 32),
+                                            __uint_as_float((uint32_t)buf[threadIdx.x])};
+      const Sum2 all = warp_sum(t.pair);
+      if (threadIdx.x == 0) buf[S::warps] = slotOf(all);
+    }
+    __syncthreads();
+    v.hi = __uint_as_float((uint32_t)(buf[S::warps] >> 32));
+    v.lo = __uint_as_float((uint32_t)buf[S::warps]);
+  }
+  return v;
+}
+template <typename S>
+__device__ double team_sum(double s, uint64_t* buf) {
+  s = vrop::warp_sum(s);
+  if constexpr (S::warps > 1) {
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = (uint64_t)__double_as_longlong(s);
+    __syncthreads();
+    s = 0;
+    for (int i = 0; i < S::warps; ++i) s += __longlong_as_double((long long)buf[i]);
+    __syncthreads();
+  }
+  return s;
+}
+template <typename S>
+__device__ __forceinline__ bool team_any(bool b) {
+  if constexpr (S::warps == 1) return __any_sync(~0u, b);
+  else return __syncthreads_or(b);
+}
+template <typename S>
+__device__ __forceinline__ Total team_sum(Total t, uint64_t* buf) {
+  t.wide = team_any<S>(t.wide);
+  t.pair = team_sum<S>(t.pair, buf);
+  if (t.wide) t.rest = team_sum<S>(t.rest, buf);
+  return t;
 }
 
 template <typename T>
@@ -176,10 +259,10 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return *reinterpret_cast<const uint4*>(p);
 }
 
-// A block's sum of squares of the tiles [k0, k1) of one tensor, the same value in
-// every thread.
+// A team's sum of squares of the tiles [k0, k1) of one tensor, as a slot, the same
+// in every thread.
 template <typename S, typename T>
-__device__ double sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1, double* buf) {
+__device__ uint64_t sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1, uint64_t* buf) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr uint64_t E = S::tileBytes / sizeof(T);
   const uint64_t head = headOf(g, count, (int)sizeof(T)), body = count - head;
@@ -194,14 +277,14 @@ __device__ double sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1,
       if (left >= E) {
         uint4 v[S::packs];
 #pragma unroll
-        for (int i = 0; i < S::packs; ++i) v[i] = load16(q + (threadIdx.x + i * S::threads) * V);
+        for (int i = 0; i < S::packs; ++i) v[i] = load16(q + (S::id() + i * S::threads) * V);
 #pragma unroll
         for (int i = 0; i < S::packs; ++i) squares<T>(v[i], acc, bits);
       } else {
         const int packs = (int)(left / V);
-        for (int i = threadIdx.x; i < packs; i += S::threads)
+        for (int i = S::id(); i < packs; i += S::threads)
           squares<T>(load16(q + (uint64_t)i * V), acc, bits);
-        const int at = packs * V + threadIdx.x;
+        const int at = packs * V + S::id();
         if (at < (int)left) {
           const float x = to_f32(q[at]);
           acc[0] = fmaf(x, x, acc[0]);
@@ -210,33 +293,35 @@ __device__ double sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k1,
       }
       sum.add(acc[0] + acc[1]);
     }
-    if (k0 == 0 && threadIdx.x < head) {
-      const float x = to_f32(g[threadIdx.x]);
+    if (k0 == 0 && S::id() < head) {
+      const float x = to_f32(g[S::id()]);
       sum.add(x * x);
       bits |= x != 0.f;
     }
-    const double s = block_sum2<S::warps>(sum, buf);
+    sum = team_sum<S>(sum, buf);
     // The squares of 32-bit floats and of bfloat16 leave the range of a float
     // long before their sum leaves that of a double. Where they did (the sum
     // is infinite, or so small that squares went below the smallest float),
     // the tiles are summed again in 64 bits. float16's squares always fit.
-    if (std::is_same_v<T, __half>) return s;
-    const bool small = s < 0x1p-90;
-    if (s < 0x1p120 && !(small && __syncthreads_or(bits != 0))) return s;
-    __syncthreads();  // before `buf` is used again
+    const bool fits = sum.hi >= kLeast && sum.hi <= kMost;
+    if (std::is_same_v<T, __half> || fits || (sum.hi < kLeast && !team_any<S>(bits != 0))) {
+      const bool bad = !(sum.hi <= kMost) || !(fabsf(sum.lo) <= kMost);  // float16 inf, NaN
+      return bad ? slotOf((double)sum.hi + (double)sum.lo) : slotOf(sum);
+    }
+    if (S::warps > 1) __syncthreads();  // before `buf` is used again
   }
   double d = 0;
   const uint64_t from = k0 ? head + k0 * E : 0, end = head + k1 * E, to = end < count ? end : count;
-  for (uint64_t i = from + threadIdx.x; i < to; i += S::threads) {
+  for (uint64_t i = from + S::id(); i < to; i += S::threads) {
     const double x = to_f64(g[i]);
     d = fma(x, x, d);
   }
-  return block_sum2<S::warps>(warp_sum(d), buf);
+  return slotOf(team_sum<S>(d, buf));
 }
 
-template <typename S, int CAP>
-__device__ double sumTensor(const Table<CAP>& a, int t, uint32_t k0, uint32_t k1, double* buf) {
-  if (k0 >= k1) return 0.0;
+template <typename S, typename A>
+__device__ uint64_t sumTensor(const A& a, int t, uint32_t k0, uint32_t k1, uint64_t* buf) {
+  if (k0 >= k1) return 0;
   const void* g = a.in[t];
   const uint64_t n = a.count[t];
   switch (a.type[t]) {
@@ -250,73 +335,96 @@ __device__ double sumTensor(const Table<CAP>& a, int t, uint32_t k0, uint32_t k1
 // The partial sums of unit u: put(slot, sum) for each of its slots, u + t from
 // its first tensor to the next unit's first. A tensor without a tile in the
 // unit gets a zero.
-template <typename S, int CAP, typename Put>
-__device__ __forceinline__ void sumUnit(const Table<CAP>& a, int u, double (*buf)[S::warps + 1],
-                                        int& turn, Put put) {
+template <typename S, typename A, typename Put>
+__device__ __forceinline__ void sumUnit(const A& a, int u, uint64_t (*buf)[S::warps + 1], int& turn,
+                                        Put put) {
   const uint32_t k0 = firstTile(a.nTiles, a.nUnits, u), k1 = firstTile(a.nTiles, a.nUnits, u + 1);
   const int t0 = u ? tensorOf(a, k0) : 0;
   const int t1 = u + 1 < a.nUnits ? tensorOf(a, k1) : a.nTensors - 1;
   for (int t = t0; t <= t1; ++t) {
     const uint32_t first = a.tile[t], last = a.tile[t + 1];
     const uint32_t x = k0 > first ? k0 : first, y = k1 < last ? k1 : last;
-    const double s = sumTensor<S>(a, t, x - first, y > x ? y - first : x - first, buf[turn]);
+    const uint64_t s = sumTensor<S>(a, t, x - first, y > x ? y - first : x - first, buf[turn]);
     turn ^= 1;
     put(u + t, s);
   }
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(Long::threads, kSumBlocks)
+__global__ void __launch_bounds__(Block::threads, kSumBlocks)
     vrNormPartials(const __grid_constant__ Table<CAP> a) {
-  __shared__ double buf[2][Long::warps + 1];
+  __shared__ uint64_t buf[2][Block::warps + 1];
   launch_dependents();
   int turn = 0;
   for (int u = blockIdx.x; u < a.nUnits; u += gridDim.x)
-    sumUnit<Long>(a, u, buf, turn, [&](int slot, double s) {
+    sumUnit<Block>(a, u, buf, turn, [&](int slot, uint64_t s) {
       if (threadIdx.x == 0) a.slots[a.slotBase + slot] = s;
     });
 }
 
 // The sum of n slots, the same in every thread.
 template <typename S>
-__device__ double sumSlots(const double* slots, uint32_t n, double* buf) {
-  double s = 0;
+__device__ Total sumSlots(const uint64_t* slots, uint32_t n, uint64_t* buf) {
+  Total t;
 #pragma unroll 4
-  for (uint32_t i = threadIdx.x; i < n; i += S::threads) s += slots[i];
-  return block_sum2<S::warps>(warp_sum(s), buf);
+  for (uint32_t i = S::id(); i < n; i += S::threads) t.add(slots[i]);
+  return team_sum<S>(t, buf);
 }
 
 // Tensor t's sum of squares from the slots of one launch, in a warp.
-template <int CAP>
-__device__ double tensorSum(const Table<CAP>& a, const double* slots, int t) {
-  double s = 0;
+template <typename A>
+__device__ Total tensorSum(const A& a, const uint64_t* slots, int t) {
+  Total s;
   if (a.tile[t] < a.tile[t + 1]) {
     const uint32_t u0 = unitOf(a.nTiles, a.nUnits, a.tile[t]);
     const uint32_t u1 = unitOf(a.nTiles, a.nUnits, a.tile[t + 1] - 1);
-    for (uint32_t u = u0 + (threadIdx.x & 31); u <= u1; u += 32) s += slots[u + t];
+    for (uint32_t u = u0 + (threadIdx.x & 31); u <= u1; u += 32) s.add(slots[u + t]);
   }
-  return warp_sum(s);
+  return team_sum<Warp>(s, nullptr);
 }
 
 // The norms: block 0 the whole list's (in the call's last launch), the other
 // blocks' warps one tensor's each.
 template <int CAP>
-__global__ void __launch_bounds__(Long::threads)
+__global__ void __launch_bounds__(Block::threads)
     vrNormFinish(const __grid_constant__ Table<CAP> a) {
-  __shared__ double buf[Long::warps + 1];
+  __shared__ uint64_t buf[Block::warps + 1];
   wait_for_previous();
-  const double scale = fabs((double)a.scale);
   if (blockIdx.x == 0) {
     if (!a.norm) return;
-    const double s = sumSlots<Long>(a.slots, a.nSlots, buf);
-    if (threadIdx.x == 0) *a.norm = (float)(scale * sqrt(s));
+    const Total s = sumSlots<Block>(a.slots, a.nSlots, buf);
+    if (threadIdx.x == 0) *a.norm = s.norm(a.scale);
     return;
   }
-  const int t = (blockIdx.x - 1) * Long::warps + (threadIdx.x >> 5);
+  const int t = (blockIdx.x - 1) * Block::warps + (threadIdx.x >> 5);
   if (t >= a.nTensors) return;
-  const double s = tensorSum(a, a.slots + a.slotBase, t);
-  if ((threadIdx.x & 31) == 0) a.tensorNorms[a.tensorBase + t] = (float)(scale * sqrt(s));
+  const Total s = tensorSum(a, a.slots + a.slotBase, t);
+  if ((threadIdx.x & 31) == 0) a.tensorNorms[a.tensorBase + t] = s.norm(a.scale);
 }
+
+// What the gradients are multiplied by. A norm that is not finite clips nothing:
+// the caller sees it and drops the step, and the gradients still show where it
+// came from.
+struct Factor {
+  float norm, f;
+  bool clips;
+  __device__ Factor(const Total& s, float scale, float maxNorm) {
+    norm = s.norm(scale);
+    clips = norm > maxNorm;
+    f = scale;
+    if (norm >= 0x1p-100f && norm <= 0x1p120f) {
+      if (clips) f *= maxNorm / norm;
+    } else {  // rare: in 64 bits
+      const double n = s.wideNorm(scale);
+      clips = n > (double)maxNorm && isfinite(n);
+      if (clips) f = (float)((double)scale * ((double)maxNorm / n));
+    }
+  }
+  // For elements of 64 bits.
+  __device__ static double of(const Total& s, float scale, float maxNorm, bool clips) {
+    return clips ? (double)scale * ((double)maxNorm / s.wideNorm(scale)) : (double)scale;
+  }
+};
 
 // One tile of out = g * factor: 16-byte packs where g and out lie alike modulo
 // 16 bytes, elements elsewhere. Each product is rounded once.
@@ -337,7 +445,7 @@ __device__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F fact
     return v;
   };
   const uint64_t head = headOf(g, count, (int)sizeof(T)), body = count - head;
-  if (k == 0 && threadIdx.x < head) out[threadIdx.x] = mul(g[threadIdx.x]);
+  if (k == 0 && S::id() < head) out[S::id()] = mul(g[S::id()]);
   const uint64_t left = body - k * E;
   const int n = (int)(left < E ? left : E);
   const T* p = g + head + k * E;
@@ -346,90 +454,90 @@ __device__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F fact
   if (packs == S::tileBytes / 16) {
     uint4 v[S::packs];
 #pragma unroll
-    for (int j = 0; j < S::packs; ++j) v[j] = load16(p + (threadIdx.x + j * S::threads) * V);
+    for (int j = 0; j < S::packs; ++j) v[j] = load16(p + (S::id() + j * S::threads) * V);
 #pragma unroll
     for (int j = 0; j < S::packs; ++j)
-      *reinterpret_cast<uint4*>(q + (threadIdx.x + j * S::threads) * V) = mulPack(v[j]);
+      *reinterpret_cast<uint4*>(q + (S::id() + j * S::threads) * V) = mulPack(v[j]);
     return;
   }
-  for (int i = threadIdx.x; i < packs; i += S::threads)
+  for (int i = S::id(); i < packs; i += S::threads)
     *reinterpret_cast<uint4*>(q + i * V) = mulPack(load16(p + i * V));
-  for (int i = packs * V + threadIdx.x; i < n; i += S::threads) q[i] = mul(p[i]);
+  for (int i = packs * V + S::id(); i < n; i += S::threads) q[i] = mul(p[i]);
 }
 
-template <typename S, int CAP>
-__device__ __forceinline__ void scaleAt(const Table<CAP>& a, int t, uint32_t k, double factor) {
+template <typename S, typename A>
+__device__ __forceinline__ void scaleAt(const A& a, int t, uint32_t k, const Factor& by,
+                                        const Total& s) {
   const void* g = a.in[t];
   void* o = a.out[t];
   const uint64_t n = a.count[t];
-  const float f = (float)factor;
   k -= a.tile[t];
   switch (a.type[t]) {
-    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, k, f);
-    case vrBfloat16: return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, k, f);
-    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, k, f);
-    default: return scaleTile<S>((const double*)g, (double*)o, n, k, factor);
+    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, k, by.f);
+    case vrBfloat16: return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, k, by.f);
+    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, k, by.f);
+    default:
+      return scaleTile<S>((const double*)g, (double*)o, n, k,
+                          Factor::of(s, a.scale, a.maxNorm, by.clips));
   }
-}
-
-// What the gradients are multiplied by. A norm that is not finite clips nothing:
-// the caller sees it and drops the step, and the gradients still show where it
-// came from.
-template <int CAP>
-__device__ __forceinline__ double factorFor(const Table<CAP>& a, double norm) {
-  const bool clips = norm > (double)a.maxNorm && isfinite(norm);
-  return (double)a.scale * (clips ? (double)a.maxNorm / norm : 1.0);
 }
 
 // Every block adds the slots up for itself, then takes tiles in turn, from the
 // list's end to its start: what the first kernel read last is still in L2.
 template <int CAP>
-__global__ void __launch_bounds__(Long::threads, kScaleBlocks)
+__global__ void __launch_bounds__(Block::threads, kScaleBlocks)
     vrClip(const __grid_constant__ Table<CAP> a) {
-  __shared__ double buf[Long::warps + 1];
+  __shared__ uint64_t buf[Block::warps + 1];
   wait_for_previous();
-  const double norm = fabs((double)a.scale) * sqrt(sumSlots<Long>(a.slots, a.nSlots, buf));
-  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const double factor = factorFor(a, norm);
+  const Total s = sumSlots<Block>(a.slots, a.nSlots, buf);
+  const Factor by(s, a.scale, a.maxNorm);
+  if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = by.norm;
   for (uint32_t i = blockIdx.x; i < a.nTiles; i += gridDim.x) {
     const uint32_t k = a.nTiles - 1 - i;
-    scaleAt<Long>(a, tensorOf(a, k), k, factor);
+    scaleAt<Block>(a, tensorOf(a, k), k, by, s);
   }
 }
 
-// A short list in one launch: a unit for each block of a cluster, the slots in
-// every block's shared memory. Where `out` is there, each block scales its unit.
-__global__ void __launch_bounds__(Short::threads)
-    vrShortList(const __grid_constant__ Table<kShortList> a) {
-  __shared__ double slots[kShortBlocks + kShortList];
-  __shared__ double buf[2][Short::warps + 1];
-  const int u = (int)cluster_rank();
+// A short list in one launch: a unit for each warp of a cluster, the slots in every
+// block's shared memory. Where `out` is there, each warp scales its unit. The
+// table is copied to shared memory first, as lookups of single parameters would
+// each wait for the constant cache.
+__global__ void __launch_bounds__(32 * kShortWarps)
+    vrShortList(const __grid_constant__ Table<kShortList> p) {
+  __shared__ Table<kShortList> a;
+  __shared__ uint64_t slots[kShortUnits + kShortList];
+  __shared__ uint64_t total[kShortWarps + 1];
+  uint64_t none[2][2];
+  const int threads = 32 * kShortWarps;
+  for (int i = threadIdx.x; i < (int)(sizeof(p) / 8); i += threads)
+    reinterpret_cast<uint64_t*>(&a)[i] = reinterpret_cast<const uint64_t*>(&p)[i];
+  cluster_sync();  // the table, and every block's slots, are there
+  const int u = (int)cluster_rank() * kShortWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   int turn = 0;
-  cluster_sync();  // every block's slots are there
-  sumUnit<Short>(a, u, buf, turn, [&](int slot, double s) {
-    if (threadIdx.x < a.nUnits) {
+  sumUnit<Warp>(a, u, none, turn, [&](int slot, uint64_t s) {
+    if (lane * kShortWarps < a.nUnits) {
       uint32_t at;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                   : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&slots[slot])), "r"(threadIdx.x));
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(s) : "memory");
+                   : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&slots[slot])), "r"(lane));
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(s) : "memory");
     }
   });
   cluster_sync();
-  const double scale = fabs((double)a.scale);
-  const double norm = scale * sqrt(sumSlots<Short>(slots, a.nUnits + a.nTensors - 1, buf[turn]));
-  if (u == 0) {
-    if (a.norm && threadIdx.x == 0) *a.norm = (float)norm;
+  const Total s =
+      sumSlots<Team<32 * kShortWarps, 1>>(slots, a.nUnits + a.nTensors - 1, total);
+  const Factor by(s, a.scale, a.maxNorm);
+  if (cluster_rank() == 0) {
+    if (a.norm && threadIdx.x == 0) *a.norm = by.norm;
     if (a.tensorNorms)
-      for (int t = threadIdx.x >> 5; t < a.nTensors; t += Short::warps) {
-        const double s = tensorSum(a, slots, t);
-        if ((threadIdx.x & 31) == 0) a.tensorNorms[t] = (float)(scale * sqrt(s));
+      for (int t = threadIdx.x >> 5; t < a.nTensors; t += kShortWarps) {
+        const Total one = tensorSum(a, slots, t);
+        if (lane == 0) a.tensorNorms[t] = one.norm(a.scale);
       }
   }
   if (a.maxNorm < 0.f) return;  // the norm alone
-  const double factor = factorFor(a, norm);
   const uint32_t k1 = firstTile(a.nTiles, a.nUnits, u + 1);
   for (uint32_t k = firstTile(a.nTiles, a.nUnits, u); k < k1; ++k)
-    scaleAt<Short>(a, tensorOf(a, k), k, factor);
+    scaleAt<Warp>(a, tensorOf(a, k), k, by, s);
 }
 
 // ------------------------------------------------------------------ host
@@ -442,7 +550,7 @@ struct Call {
   float scale, maxNorm;
   float* norm;
   float* tensorNorms;
-  double* slots;
+  uint64_t* slots;
   cudaStream_t stream;
 };
 
@@ -482,25 +590,27 @@ int unitsFor(uint32_t tiles) {
   return kBlocks * (int)(waves < 1 ? 1 : waves > kMostWaves ? kMostWaves : waves);
 }
 
-// Every tile of a short list fits the cluster's blocks a few times over.
+// At most a tile for each warp of the cluster: a launch costs the host 3 us, the
+// cluster's two barriers the GPU 2 (1 MiB of gradients clipped in 10.6 us, by the
+// long path in 6.7).
 bool isShort(const Call& c) {
   if (c.nTensors > kShortList) return false;
   uint64_t tiles = 0;
   for (int t = 0; t < c.nTensors; ++t)
-    tiles += tilesOf(c.in[t], c.counts[t], sizeOfType(c.types[t]), Short::tileBytes);
+    tiles += tilesOf(c.in[t], c.counts[t], sizeOfType(c.types[t]), Warp::tileBytes);
   return tiles <= kShortTiles;
 }
 
 vrResult_t runShort(const Call& c) {
   Table<kShortList> a;
-  fill(c, 0, c.nTensors, Short::tileBytes, &a);
+  memset(&a, 0, sizeof(a));
+  fill(c, 0, c.nTensors, Warp::tileBytes, &a);
   int blocks = 1;
-  while (blocks < kShortBlocks && (uint32_t)blocks < a.nTiles) blocks *= 2;
-  a.nUnits = blocks;
-  a.nSlots = a.slotBase = 0;
+  while (blocks < kShortBlocks && (uint32_t)(blocks * kShortWarps) < a.nTiles) blocks *= 2;
+  a.nUnits = blocks * kShortWarps;
   const void* k = (const void*)&vrShortList;
   if (!vrln::allowLargeClusters(k)) return vrCudaError;
-  return launch(k, dim3(blocks), dim3(Short::threads), 0, c.stream, a, blocks);
+  return launch(k, dim3(blocks), dim3(32 * kShortWarps), 0, c.stream, a, blocks);
 }
 
 template <int CAP>
@@ -513,7 +623,7 @@ vrResult_t runLong(const Call& c) {
     for (int l = 0; l < launches; ++l) {
       const int at = l * CAP, n = c.nTensors - at < CAP ? c.nTensors - at : CAP;
       if (pass == 0 || launches > 1) {
-        fill(c, at, n, Long::tileBytes, &a);
+        fill(c, at, n, Block::tileBytes, &a);
         a.nUnits = unitsFor(a.nTiles);
       }
       a.slotBase = base;
@@ -532,11 +642,11 @@ vrResult_t runLong(const Call& c) {
           if (!blocks) blocks = 1;
         } else {
           kernel = (const void*)&vrNormFinish<CAP>;
-          blocks = 1 + (c.tensorNorms ? (n + Long::warps - 1) / Long::warps : 0);
+          blocks = 1 + (c.tensorNorms ? (n + Block::warps - 1) / Block::warps : 0);
         }
       }
       // The second pass's first kernel may start while the first pass ends.
-      const vrResult_t r = launch(kernel, dim3((unsigned)blocks), dim3(Long::threads), 0, c.stream,
+      const vrResult_t r = launch(kernel, dim3((unsigned)blocks), dim3(Block::threads), 0, c.stream,
                                   a, 1, pass == 1 && l == 0);
       if (r != vrSuccess) return r;
     }
@@ -552,7 +662,7 @@ vrResult_t checkList(const void* const* in, const size_t* counts, const vrDataTy
     const int es = elemSizeOf(types[t]);
     if (!es || (counts[t] && (!in[t] || misaligned(in[t], es)))) return vrInvalidArgument;
     if (counts[t] > ((size_t)1 << 48)) return vrInvalidArgument;
-    tiles += tilesOf(in[t], counts[t], es, Long::tileBytes);
+    tiles += tilesOf(in[t], counts[t], es, Block::tileBytes);
     if (tiles >= 0x7fffffffull) return vrInvalidArgument;
   }
   return vrSuccess;
@@ -560,7 +670,7 @@ vrResult_t checkList(const void* const* in, const size_t* counts, const vrDataTy
 
 vrResult_t runChecked(const Call& c, const void* workspace, size_t workspaceBytes) {
   if (!workspace || misaligned(workspace, 16) ||
-      workspaceBytes < slotsBound(c.nTensors) * sizeof(double))
+      workspaceBytes < slotsBound(c.nTensors) * sizeof(uint64_t))
     return vrInvalidArgument;
   if (isShort(c)) return runShort(c);
   return c.nTensors <= kShortList ? runLong<kShortList>(c) : runLong<kLongList>(c);
@@ -570,7 +680,7 @@ vrResult_t runChecked(const Call& c, const void* workspace, size_t workspaceByte
 
 extern "C" VR_API vrResult_t vrGradNormWorkspace(int nTensors, size_t* bytes) {
   if (nTensors < 1 || !bytes) return vrInvalidArgument;
-  *bytes = (size_t)(slotsBound(nTensors) * sizeof(double));
+  *bytes = (size_t)(slotsBound(nTensors) * sizeof(uint64_t));
   return vrSuccess;
 }
 
@@ -585,7 +695,7 @@ extern "C" VR_API vrResult_t vrGradNorm(const void* const* grads, const size_t* 
       !(scale - scale == 0.f))
     return vrInvalidArgument;
   const Call c = {grads, nullptr, counts, dtypes, nTensors, scale, 0.f, norm, tensorNorms,
-                  (double*)workspace, (cudaStream_t)stream};
+                  (uint64_t*)workspace, (cudaStream_t)stream};
   return runChecked(c, workspace, workspaceBytes);
 }
 
@@ -605,6 +715,6 @@ extern "C" VR_API vrResult_t vrClipGradNorm(const void* const* grads, void* cons
       return vrInvalidArgument;
   }
   const Call c = {grads, outs, counts, dtypes, nTensors, scale, maxNorm, norm, nullptr,
-                  (double*)workspace, (cudaStream_t)stream};
+                  (uint64_t*)workspace, (cudaStream_t)stream};
   return runChecked(c, workspace, workspaceBytes);
 }
