@@ -354,7 +354,7 @@ template <int CAP>
 __global__ void __launch_bounds__(Block::threads, kSumBlocks)
     vrNormPartials(const __grid_constant__ Table<CAP> a) {
   __shared__ uint64_t buf[2][Block::warps + 1];
-  launch_dependents();
+  begin_kernel();
   int turn = 0;
   for (int u = blockIdx.x; u < a.nUnits; u += gridDim.x)
     sumUnit<Block>(a, u, buf, turn, [&](int slot, uint64_t s) {
@@ -389,7 +389,7 @@ template <int CAP>
 __global__ void __launch_bounds__(Block::threads)
     vrNormFinish(const __grid_constant__ Table<CAP> a) {
   __shared__ uint64_t buf[Block::warps + 1];
-  wait_for_previous();
+  begin_kernel();
   if (blockIdx.x == 0) {
     if (!a.norm) return;
     const Total s = sumSlots<Block>(a.slots, a.nSlots, buf);
@@ -488,7 +488,7 @@ template <int CAP>
 __global__ void __launch_bounds__(Block::threads, kScaleBlocks)
     vrClip(const __grid_constant__ Table<CAP> a) {
   __shared__ uint64_t buf[Block::warps + 1];
-  wait_for_previous();
+  begin_kernel();
   const Total s = sumSlots<Block>(a.slots, a.nSlots, buf);
   const Factor by(s, a.scale, a.maxNorm);
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = by.norm;
@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(32 * kShortWarps)
   __shared__ uint64_t slots[kShortUnits + kShortList];
   __shared__ uint64_t total[kShortWarps + 1];
   uint64_t none[2][2];
+  begin_kernel();
   const int threads = 32 * kShortWarps;
   for (int i = threadIdx.x; i < (int)(sizeof(p) / 8); i += threads)
     reinterpret_cast<uint64_t*>(&a)[i] = reinterpret_cast<const uint64_t*>(&p)[i];
@@ -645,9 +646,8 @@ vrResult_t runLong(const Call& c) {
           blocks = 1 + (c.tensorNorms ? (n + Block::warps - 1) / Block::warps : 0);
         }
       }
-      // The second pass's first kernel may start while the first pass ends.
-      const vrResult_t r = launch(kernel, dim3((unsigned)blocks), dim3(Block::threads), 0, c.stream,
-                                  a, 1, pass == 1 && l == 0);
+      const vrResult_t r =
+          launch(kernel, dim3((unsigned)blocks), dim3(Block::threads), 0, c.stream, a);
       if (r != vrSuccess) return r;
     }
     slots = base;

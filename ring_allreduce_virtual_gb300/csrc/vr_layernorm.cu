@@ -52,6 +52,7 @@ constexpr int kRowWarps = kRowThreads / 32;
 template <typename T, typename W>
 __global__ void __launch_bounds__(kRowThreads) vrLnForwardAny(const __grid_constant__ FwdArgs a) {
   __shared__ float buf[2][kRowWarps];
+  begin_kernel();
   const W* w = static_cast<const W*>(a.w);
   const W* b = static_cast<const W*>(a.b);
   const float c = 1.f / (float)a.cols;
@@ -86,6 +87,7 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
   constexpr int V = kV<T>, P = E / V;
   extern __shared__ uint4 ring[];  // [warps][STAGES][ROWS][P][32]
   __shared__ RowSum<MODE, ROWS> sum;
+  begin_kernel();
   const int cols = (int)a.cols;
   const Place<T, MODE, P> at(a.l, a.rows, cols);
   int turn = 0;
@@ -102,20 +104,27 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
     if (!used[i])
       for (int k = 0; k < STAGES * ROWS; ++k) mine[(k * P + i) * 32] = make_uint4(0, 0, 0, 0);
   T ahead[ROWS];  // the next rows' elements outside the packs
-  auto fetch = [&](int left, const T* p, uint4* to) {
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k)
+  const uint32_t ringAt = (uint32_t)__cvta_generic_to_shared(mine);
+  auto fetch = [&](int left, const T* p, int stage) {
+    const uint32_t to = ringAt + stage * (ROWS * P * 512);
+    each<ROWS>([&](auto kk) {
+      constexpr int k = decltype(kk)::value;
       if (k < left) {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (used[i])
-            copy16(&to[(k * P + i) * 32],
-                   p + k * xStep + i * (MODE == IN_WARP ? at.stripe : 32) * V);
+        const T* q = p + k * xStep;
+        each<P>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          if (!used[i]) return;
+          if constexpr (MODE == IN_WARP) copy16<(k * P + i) * 512, 0>(to, q + i * at.stripe * V);
+          else copy16<(k * P + i) * 512, i * 512>(to, q);
+        });
       }
+    });
     copies_commit();
   };
+  // Only the first warps of a row hold elements outside the packs.
+  const bool edges = RAGGED && __any_sync(~0u, at.edge >= 0);
   auto fetchEdge = [&](int left, const T* p) {
-    if constexpr (RAGGED) {
+    if (edges) {
 #pragma unroll
       for (int k = 0; k < ROWS; ++k)
         ahead[k] = at.edge >= 0 && k < left ? p[k * xStep + at.edge] : from_f32<T>(0.f);
@@ -124,7 +133,7 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
   const T* xf = xp + at.column(0);  // the rows to fetch next
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
-    fetch(at.n - i * ROWS, xf, mine + i * (ROWS * P * 32));
+    fetch(at.n - i * ROWS, xf, i);
     xf += ROWS * xStep;
   }
   fetchEdge(at.n, xp);
@@ -145,7 +154,7 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
   T* yo = yp + at.column(0);
   for (int round = 0; round < at.rounds; round += ROWS) {
     const int back = stage == 0 ? STAGES - 1 : stage - 1;
-    fetch(left - (STAGES - 1) * ROWS, xf, mine + back * (ROWS * P * 32));
+    fetch(left - (STAGES - 1) * ROWS, xf, back);
     xf += ROWS * xStep;
     copies_wait<STAGES - 1>();
     F2 x[ROWS][P][V / 2];
@@ -161,7 +170,10 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
         for (int j = 0; j < V / 2; ++j) s2 = s2 + x[k][i][j];
       }
       s[k] = both(s2);
-      if constexpr (RAGGED) {
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
         e[k] = to_f32(ahead[k]);
         s[k] += e[k];
       }
@@ -186,7 +198,10 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
         }
       }
       s[k] = both(q2);
-      if constexpr (RAGGED) {
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
         e[k] -= m[k];
         if (at.edge >= 0) s[k] = fmaf(e[k], e[k], s[k]);
       }
@@ -207,8 +222,12 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
           *reinterpret_cast<uint4*>(yo + k * yStep + i * (MODE == IN_WARP ? at.stripe : 32) * V) =
               pack<T>(x[k][i]);
       }
-      if (RAGGED && at.edge >= 0 && k < left)
-        yp[k * yStep + at.edge] = from_f32<T>(fmaf(e[k] * s[k], we, be));
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k)
+        if (at.edge >= 0 && k < left)
+          yp[k * yStep + at.edge] = from_f32<T>(fmaf(e[k] * s[k], we, be));
     }
     if (at.lane == 0) {
 #pragma unroll
@@ -229,6 +248,7 @@ __global__ void __maxnreg__(REGS) vrLnForwardRows(const __grid_constant__ FwdArg
 template <typename T, typename W>
 __global__ void __launch_bounds__(kRowThreads) vrLnBackwardAny(const __grid_constant__ BwdArgs a) {
   __shared__ float buf[4][kRowWarps];
+  begin_kernel();
   const W* w = static_cast<const W*>(a.w);
   const float c = 1.f / (float)a.cols;
   int turn = 0;
@@ -261,7 +281,7 @@ constexpr int kColWarps = 8;
 template <typename T>
 __global__ void __launch_bounds__(32 * kColWarps) vrLnColumns(const __grid_constant__ BwdArgs a) {
   __shared__ float buf[2][kColWarps][32];
-  launch_dependents();
+  begin_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint64_t col = (uint64_t)blockIdx.x * 32 + lane;
   const uint64_t r0 = a.rows * blockIdx.y / a.splits, r1 = a.rows * (blockIdx.y + 1) / a.splits;
@@ -286,29 +306,28 @@ __global__ void __launch_bounds__(32 * kColWarps) vrLnColumns(const __grid_const
   }
 }
 
-// dw and db, second step: the splits' sums added up, split by split. A warp
-// takes every eighth split of 32 columns.
+// dw and db, second step: the splits' sums added up in a fixed order. A block
+// takes 32 columns, a warp of it every 32nd split, so that few loads follow one
+// another: the kernel is all latency.
+constexpr int kJoinWarps = 32;
 template <typename W>
-__global__ void __launch_bounds__(256) vrLnJoin(const __grid_constant__ BwdArgs a) {
-  __shared__ float buf[8][32];
+__global__ void __launch_bounds__(32 * kJoinWarps) vrLnJoin(const __grid_constant__ BwdArgs a) {
+  __shared__ float buf[kJoinWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint64_t col = (uint64_t)blockIdx.x * 32 + lane;
+  const uint64_t first = (uint64_t)blockIdx.x * 32;
   W* out = static_cast<W*>(blockIdx.y ? a.db : a.dw);
-  wait_for_previous();
+  begin_kernel();
   if (!out) return;
   float s = 0.f;
-  if (col < a.cols) {
-    const float* p = a.partials + (uint64_t)blockIdx.y * a.cols + col;
-#pragma unroll 4
-    for (int i = warp; i < a.splits; i += 8) s += p[(uint64_t)i * 2 * a.cols];
+  if (first + lane < a.cols) {
+    const float* p = a.partials + (uint64_t)blockIdx.y * a.cols + first + lane;
+#pragma unroll 8
+    for (int i = warp; i < a.splits; i += kJoinWarps) s += p[(uint64_t)i * 2 * a.cols];
   }
   buf[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < a.cols) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s += buf[i][lane];
-    out[col] = from_f32<W>(s);
-  }
+  s = warp_sum(buf[lane][warp]);  // column `warp`
+  if (lane == 0 && first + warp < a.cols) out[first + warp] = from_f32<W>(s);
 }
 
 // The backward pass of rows that are kept on chip: dy and x are read once, dx is
@@ -321,6 +340,7 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
   constexpr int V = kV<T>, P = E / V;
   extern __shared__ uint4 ring[];  // [warps][STAGES][ROWS][dy, x][P][32]
   __shared__ RowSum<MODE, 2 * ROWS> sum;
+  begin_kernel();
   const int cols = (int)a.cols;
   const Place<T, MODE, P> at(a.l, a.rows, cols);
   int turn = 0;
@@ -342,28 +362,48 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
       for (int k = 0; k < STAGES * ROWS * 2; ++k) mine[(k * P + i) * 32] = make_uint4(0, 0, 0, 0);
   T aheadG[ROWS], aheadX[ROWS];    // the next rows' elements outside the packs
   float nextM[ROWS], nextR[ROWS];  // and their statistics
-  auto fetch = [&](int left, const T* g, const T* x, uint4* to) {
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k)
+  const uint32_t ringAt = (uint32_t)__cvta_generic_to_shared(mine);
+  auto fetch = [&](int left, const T* g, const T* x, int stage) {
+    const uint32_t to = ringAt + stage * (kSet * 16);
+    each<ROWS>([&](auto kk) {
+      constexpr int k = decltype(kk)::value;
       if (k < left) {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-          if (used[i]) {
-            copy16(&to[(2 * k * P + i) * 32], g + k * gStep + i * apart);
-            copy16(&to[((2 * k + 1) * P + i) * 32], x + k * xStep + i * apart);
+        const T *gk = g + k * gStep, *xk = x + k * xStep;
+        each<P>([&](auto ii) {
+          constexpr int i = decltype(ii)::value;
+          if (!used[i]) return;
+          constexpr int at0 = (2 * k * P + i) * 512, at1 = at0 + P * 512;
+          if constexpr (MODE == IN_WARP) {
+            copy16<at0, 0>(to, gk + i * apart);
+            copy16<at1, 0>(to, xk + i * apart);
+          } else {
+            copy16<at0, i * 512>(to, gk);
+            copy16<at1, i * 512>(to, xk);
           }
+        });
       }
+    });
     copies_commit();
   };
-  auto fetchRest = [&](int left, uint64_t row, const T* g, const T* x) {
+  // Only the first warps of a row hold elements outside the packs.
+  const bool edges = RAGGED && __any_sync(~0u, at.edge >= 0);
+  const float *mp = a.mean + at.row, *rp = a.rstd + at.row;
+  auto fetchRest = [&](int left, const T* g, const T* x) {
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       nextM[k] = nextR[k] = 0.f;
-      if (RAGGED) aheadG[k] = aheadX[k] = from_f32<T>(0.f);
       if (k < left) {
-        nextM[k] = a.mean[row + (uint64_t)k * a.l.step];
-        nextR[k] = a.rstd[row + (uint64_t)k * a.l.step];
-        if (RAGGED && at.edge >= 0) {
+        nextM[k] = mp[(uint64_t)k * a.l.step];
+        nextR[k] = rp[(uint64_t)k * a.l.step];
+      }
+    }
+    mp += (uint64_t)ROWS * a.l.step;
+    rp += (uint64_t)ROWS * a.l.step;
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        aheadG[k] = aheadX[k] = from_f32<T>(0.f);
+        if (at.edge >= 0 && k < left) {
           aheadG[k] = g[k * gStep + at.edge];
           aheadX[k] = x[k * xStep + at.edge];
         }
@@ -373,11 +413,11 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
   const T *gf = gp + at.column(0), *xf = xp + at.column(0);  // the rows to fetch next
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
-    fetch(at.n - i * ROWS, gf, xf, mine + i * kSet);
+    fetch(at.n - i * ROWS, gf, xf, i);
     gf += ROWS * gStep;
     xf += ROWS * xStep;
   }
-  fetchRest(at.n, at.row, gp, xp);
+  fetchRest(at.n, gp, xp);
   Params<T, W> w[P];
   float we = 1.f;
 #pragma unroll
@@ -391,12 +431,11 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) dw[i][j] = db[i][j] = f2(0.f);
   const float c = 1.f / (float)cols;
-  uint64_t row = at.row;
   int left = at.n, stage = 0;
   T* oo = op + at.column(0);
   for (int round = 0; round < at.rounds; round += ROWS) {
     const int back = stage == 0 ? STAGES - 1 : stage - 1;
-    fetch(left - (STAGES - 1) * ROWS, gf, xf, mine + back * kSet);
+    fetch(left - (STAGES - 1) * ROWS, gf, xf, back);
     gf += ROWS * gStep;
     xf += ROWS * xStep;
     float m[ROWS], r[ROWS], ge[ROWS], de[ROWS], s[2 * ROWS];
@@ -404,15 +443,17 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
     for (int k = 0; k < ROWS; ++k) {
       m[k] = nextM[k];
       r[k] = nextR[k];
-      if constexpr (RAGGED) {
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
         ge[k] = to_f32(aheadG[k]);
         de[k] = to_f32(aheadX[k]) - m[k];
       }
     }
     gp += ROWS * gStep;
     xp += ROWS * xStep;
-    row += (uint64_t)ROWS * a.l.step;
-    fetchRest(left - ROWS, row, gp, xp);
+    fetchRest(left - ROWS, gp, xp);
     copies_wait<STAGES - 1>();
     const uint4* from = mine + stage * kSet;
 #pragma unroll
@@ -436,18 +477,20 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
             p2 = fma2(gw, d, p2);
           }
         }
-        if constexpr (RAGGED) {
-          dbe += ge[k];
-          dwe = fmaf(ge[k] * r[k], de[k], dwe);
-        }
       }
       s[2 * k] = both(s2);
       s[2 * k + 1] = both(p2);
-      if constexpr (RAGGED) {
-        ge[k] *= we;
-        s[2 * k] += ge[k];
-        s[2 * k + 1] = fmaf(ge[k], de[k], s[2 * k + 1]);
-      }
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k)
+        if (k < left) {
+          dbe += ge[k];
+          dwe = fmaf(ge[k] * r[k], de[k], dwe);
+          ge[k] *= we;
+          s[2 * k] += ge[k];
+          s[2 * k + 1] = fmaf(ge[k], de[k], s[2 * k + 1]);
+        }
     }
     if (a.dx) {
       sum(s, a.l, at.group, turn);
@@ -469,7 +512,7 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
             *reinterpret_cast<uint4*>(oo + k * oStep + i * apart) = pack<T>(x);
           }
         }
-        if (RAGGED && at.edge >= 0 && k < left)
+        if (edges && at.edge >= 0 && k < left)
           op[k * oStep + at.edge] = from_f32<T>(fmaf(de[k], c1, fmaf(ge[k], r[k], c0)));
       }
     }
@@ -478,38 +521,42 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
     op += ROWS * oStep;
     oo += ROWS * oStep;
   }
-  launch_dependents();
   if (!a.dw && !a.db) return;
   copies_wait<0>();
   // The groups' sums are added up in shared memory, in the groups' order, so
-  // that a block leaves one; a cluster's blocks write their own columns.
+  // that a block leaves one; a cluster's blocks write their own columns. In
+  // shared memory every eighth word is left out: a thread's columns lie
+  // together, and the same one of all lanes would lie in four banks.
+  auto slot = [](int col) { return MODE == IN_CLUSTER ? col : col + (col >> 3); };
   float* part = a.partials + (uint64_t)(blockIdx.x / a.l.ctas) * 2 * a.cols;
+  const int half = slot(cols + 7);  // dw, then db
   if constexpr (MODE != IN_CLUSTER) {
     __syncthreads();
-    float* all = reinterpret_cast<float*>(ring);
-    part = all + at.group * 2 * cols;
+    part = reinterpret_cast<float*>(ring) + at.group * 2 * half;
   }
+  float* const partB = part + (MODE == IN_CLUSTER ? cols : half);
 #pragma unroll
   for (int i = 0; i < P; ++i)
     if (used[i]) {
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         const int col = at.column(i) + 2 * j;
-        split(dw[i][j], part[col], part[col + 1]);
-        split(db[i][j], part[cols + col], part[cols + col + 1]);
+        split(dw[i][j], part[slot(col)], part[slot(col + 1)]);
+        split(db[i][j], partB[slot(col)], partB[slot(col + 1)]);
       }
     }
   if (RAGGED && at.edge >= 0) {
-    part[at.edge] = dwe;
-    part[cols + at.edge] = dbe;
+    part[slot(at.edge)] = dwe;
+    partB[slot(at.edge)] = dbe;
   }
   if constexpr (MODE != IN_CLUSTER) {
     __syncthreads();
     const float* all = reinterpret_cast<const float*>(ring);
     float* out = a.partials + (uint64_t)blockIdx.x * 2 * a.cols;
     for (int i = threadIdx.x; i < 2 * cols; i += blockDim.x) {
-      float t = all[i];
-      for (int k = 1; k < a.l.groups; ++k) t += all[k * 2 * cols + i];
+      const int at0 = i < cols ? slot(i) : half + slot(i - cols);
+      float t = all[at0];
+      for (int k = 1; k < a.l.groups; ++k) t += all[k * 2 * half + at0];
       out[i] = t;
     }
   }
@@ -607,10 +654,11 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
 // The shape was chosen by measuring on a GB300 (dy and x read and dx written
 // once, of the measured copy peak): 16 elements of 2 rows a thread, the blocks
 // as large as one for each SM can be, which leaves the fewest sums to join (8192
-// bf16 0.94, 4096 bf16 0.88, 1024 bf16 0.88). float32 rows take 256 threads
-// of it (4096 0.91), as the ring of 512 would not fit, and from 4096 on one row at
-// a time (8192 0.90 against 0.84 as clusters of two); wider ones clusters (16384
-// bf16 0.65, 32768 0.44).
+// bf16 0.95, 4096 bf16 0.91, 1024 bf16 0.90). float32 rows take 256 threads
+// of it (4096 0.94), as the ring of 512 would not fit, and beyond 4096 one row at
+// a time (8192 0.92 against 0.84 with two in clusters). Rows wider than 512
+// threads are a cluster's, which waits for its slowest block at every row (16384
+// bf16 0.65, float32 0.73; 32768 bf16 0.37).
 struct BwdPlan {
   Layout l;
   int mode, threads;
@@ -625,7 +673,9 @@ bool planShape(uint64_t rows, uint64_t cols, bool ragged, int blockThreads, int 
   p->threads = p->l.tpr * p->l.groups;
   const size_t ring = (size_t)STAGES * ROWS * E * sizeof(T) * 2 * p->threads;
   // The groups' sums take the ring's place at the end, of every column.
-  const size_t join = p->mode == IN_CLUSTER ? 0 : (size_t)p->l.groups * 2 * cols * sizeof(float);
+  const size_t join = p->mode == IN_CLUSTER
+                          ? 0
+                          : (size_t)p->l.groups * 2 * ((cols + 7) * 9 / 8 + 1) * sizeof(float);
   p->smem = ring > join ? ring : join;
   p->grid = gridFor(rows, &p->l, V, residentWarps(REGS, p->smem, p->threads), ragged, ROWS);
   return p->smem <= kMostShared;
@@ -636,9 +686,7 @@ int planBackward(uint64_t rows, uint64_t cols, bool ragged, BwdPlan* p) {
   if (rows >= kMostRows) return NO_PLAN;
   if constexpr (sizeof(T) == 2)
     return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 512, 512, p) ? TWO_ROWS : NO_PLAN;
-  if (cols > 4096 && cols < 8192 + kV<T> &&
-      planShape<T, 16, 1, 3, 96>(rows, cols, ragged, 512, 512, p) && p->mode == IN_BLOCK)
-    return ONE_ROW;
+  if (cols > 4096 && planShape<T, 16, 1, 3, 96>(rows, cols, ragged, 512, 512, p)) return ONE_ROW;
   return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 256, 256, p) ? TWO_ROWS : NO_PLAN;
 }
 
@@ -655,17 +703,25 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
   BwdPlan p;
   const int shape = planBackward<T>(a.rows, a.cols, ragged, &p);
   if (shape == NO_PLAN) return false;
-  const void* k = p.mode == IN_WARP    ? backwardKernel<T, W, IN_WARP>(ragged)
-                  : p.mode == IN_BLOCK ? backwardKernel<T, W, IN_BLOCK>(ragged)
-                                       : backwardKernel<T, W, IN_CLUSTER>(ragged);
+  const void* k = nullptr;
+  if (p.mode == IN_WARP) k = backwardKernel<T, W, IN_WARP>(ragged);
+  if (p.mode == IN_BLOCK) k = backwardKernel<T, W, IN_BLOCK>(ragged);
+  if constexpr (sizeof(T) == 2)
+    if (p.mode == IN_CLUSTER) k = backwardKernel<T, W, IN_CLUSTER>(ragged);
   if constexpr (sizeof(T) == 4)
-    if (shape == ONE_ROW)
-      k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, true, 96>
-                 : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, false, 96>;
+    if (shape == ONE_ROW) {
+      if (p.mode == IN_BLOCK)
+        k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, true, 96>
+                   : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, false, 96>;
+      else
+        k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, true, 96>
+                   : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, false, 96>;
+    }
   a.l = p.l;
   a.l.offset = offset;
   a.l.skew = skew;
   a.splits = (int)(p.grid / p.l.ctas);
+  if (!k) return false;
   *r = allowShared(k) ? launch(k, dim3(p.grid), dim3(p.threads), p.smem, st, a, p.l.ctas)
                       : vrCudaError;
   return true;
@@ -782,8 +838,8 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
                    dim3(32 * kColWarps), 0, st, a);
     }
     if (r == vrSuccess && params)
-      r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 31) / 32), 2), dim3(256), 0, st, a,
-                 1, true);
+      r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 31) / 32), 2),
+                 dim3(32 * kJoinWarps), 0, st, a);
     return r;
   });
 }

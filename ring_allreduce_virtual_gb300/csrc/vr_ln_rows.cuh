@@ -129,15 +129,20 @@ __device__ __forceinline__ uint4 pack(const F2* f) {
 // Rows on their way into shared memory. Each thread copies the packs that it
 // will read itself, some rows ahead, so no barrier separates the copy from the
 // read, and the bytes in flight (what HBM's latency asks for) take no registers.
-__device__ __forceinline__ void copy16(void* smem, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(smem)),
-               "l"(g) : "memory");
+template <int S, int G>  // constant offsets of both addresses
+__device__ __forceinline__ void copy16(uint32_t smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;" ::"r"(smem), "l"(g), "n"(S), "n"(G)
+               : "memory");
+}
+// f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ uint4 load_shared(const void* p, int offset) {
-  return *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + offset);
-}
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -384,7 +389,7 @@ inline unsigned gridFor(uint64_t rows, Layout* l, int V, int residentWarps, bool
   while (ragged && lot * unit % V) ++lot;
   most = most / lot * lot ? most / lot * lot : lot;
   uint64_t rounds = (rows + most * unit - 1) / (most * unit);
-  rounds = (rounds + rowsAtOnce - 1) / rowsAtOnce * rowsAtOnce;
+  if (rounds < (uint64_t)rowsAtOnce) rounds = rowsAtOnce;
   uint64_t blocks = ((rows + rounds - 1) / rounds + unit - 1) / unit;
   if (rounds > 1) blocks = (blocks + lot - 1) / lot * lot;
   l->step = (uint32_t)(blocks * unit);
