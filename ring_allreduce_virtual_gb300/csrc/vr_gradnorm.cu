@@ -35,11 +35,11 @@ struct Team {
     return THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
   }
 };
-// Long lists: 5 blocks an SM for the sums. Scaling takes 2: with more, reads and
-// writes of more places alternate in HBM (2 / 4 / 5 blocks: 490 / 518 / 522 us for
-// 1.06 GB).
+// Long lists: 5 blocks an SM for the sums, 3 for scaling, with the registers that
+// 8 loads in flight take (2 / 3 / 4 / 5 blocks: 1.06 GB 511 / 498 / 504 / 510 us,
+// 25 MB 20.7 / 19.3 / 20.1 / 20.1 us; 3 in the registers of 4: 526 and 20.2).
 using Block = Team<256, 8>;
-constexpr int kSumBlocks = 5, kScaleBlocks = 2;
+constexpr int kSumBlocks = 5, kScaleBlocks = 3;
 constexpr int kBlocks = kSMs * kSumBlocks;
 // A unit is at least 8 tiles where a block has more than one unit. Several
 // units a block keep what all blocks read at a time together in memory: 532
@@ -54,7 +54,7 @@ constexpr int kShortTiles = kShortUnits;
 // (32,764 bytes at most): nothing is copied to the device beforehand and the
 // caller's arrays are free on return. Longer lists take several launches.
 constexpr int kShortList = 64;
-constexpr int kLongList = 960;
+constexpr int kLongList = 960;  // and LongTable's table of units
 
 template <int CAP>
 struct alignas(8) Table {
@@ -74,6 +74,13 @@ struct alignas(8) Table {
   uint64_t count[CAP];
   uint32_t tile[CAP + 1];  // tiles before tensor t
   uint8_t type[CAP];
+};
+// With one unit a block the host looks up the units' first tensors: a search in
+// parameter space is a chain of misses in the constant cache, 4 of the 11 us of
+// 25 MB (lists with more units are long enough not to notice).
+template <int CAP>
+struct LongTable : Table<CAP> {
+  uint16_t first[kBlocks];
 };
 
 __host__ __device__ inline int sizeOfType(int t) {
@@ -112,6 +119,16 @@ __device__ inline int tensorOf(const A& a, uint32_t k) {
     if (a.tile[mid] <= k) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// The same for a launch of single units: the first tensor of unit u, and from
+// there on.
+template <int CAP>
+__device__ inline int tensorOf(const LongTable<CAP>& a, uint32_t k) {
+  if (a.nUnits > kBlocks) return tensorOf(static_cast<const Table<CAP>&>(a), k);
+  int t = a.first[unitOf(a.nTiles, a.nUnits, k)];
+  while (a.tile[t + 1] <= k) ++t;
+  return t;
 }
 
 // A sum in two floats: hi + lo, the rounding errors of hi caught exactly
@@ -352,7 +369,7 @@ __device__ __forceinline__ void sumUnit(const A& a, int u, uint64_t (*buf)[S::wa
 
 template <int CAP>
 __global__ void __launch_bounds__(Block::threads, kSumBlocks)
-    vrNormPartials(const __grid_constant__ Table<CAP> a) {
+    vrNormPartials(const __grid_constant__ LongTable<CAP> a) {
   __shared__ uint64_t buf[2][Block::warps + 1];
   begin_kernel();
   int turn = 0;
@@ -387,7 +404,7 @@ __device__ Total tensorSum(const A& a, const uint64_t* slots, int t) {
 // blocks' warps one tensor's each.
 template <int CAP>
 __global__ void __launch_bounds__(Block::threads)
-    vrNormFinish(const __grid_constant__ Table<CAP> a) {
+    vrNormFinish(const __grid_constant__ LongTable<CAP> a) {
   __shared__ uint64_t buf[Block::warps + 1];
   begin_kernel();
   if (blockIdx.x == 0) {
@@ -486,7 +503,7 @@ __device__ __forceinline__ void scaleAt(const A& a, int t, uint32_t k, const Fac
 // list's end to its start: what the first kernel read last is still in L2.
 template <int CAP>
 __global__ void __launch_bounds__(Block::threads, kScaleBlocks)
-    vrClip(const __grid_constant__ Table<CAP> a) {
+    vrClip(const __grid_constant__ LongTable<CAP> a) {
   __shared__ uint64_t buf[Block::warps + 1];
   begin_kernel();
   const Total s = sumSlots<Block>(a.slots, a.nSlots, buf);
@@ -614,9 +631,21 @@ vrResult_t runShort(const Call& c) {
   return launch(k, dim3(blocks), dim3(32 * kShortWarps), 0, c.stream, a, blocks);
 }
 
+// The first tensor of each unit, where a block has one unit.
+template <int CAP>
+void findFirst(LongTable<CAP>* a) {
+  if (a->nUnits > kBlocks) return;
+  int t = 0;
+  for (int u = 0; u < a->nUnits; ++u) {
+    const uint32_t k = firstTile(a->nTiles, a->nUnits, u);
+    while (t + 1 < a->nTensors && a->tile[t + 1] <= k) ++t;
+    a->first[u] = (uint16_t)t;
+  }
+}
+
 template <int CAP>
 vrResult_t runLong(const Call& c) {
-  Table<CAP> a;
+  LongTable<CAP> a;
   const int launches = (c.nTensors + CAP - 1) / CAP;
   uint32_t slots = 0;
   for (int pass = 0; pass < 2; ++pass) {
@@ -624,8 +653,9 @@ vrResult_t runLong(const Call& c) {
     for (int l = 0; l < launches; ++l) {
       const int at = l * CAP, n = c.nTensors - at < CAP ? c.nTensors - at : CAP;
       if (pass == 0 || launches > 1) {
-        fill(c, at, n, Block::tileBytes, &a);
+        fill(c, at, n, Block::tileBytes, static_cast<Table<CAP>*>(&a));
         a.nUnits = unitsFor(a.nTiles);
+        findFirst(&a);
       }
       a.slotBase = base;
       a.nSlots = slots;
