@@ -41,6 +41,7 @@ struct BwdArgs {
   uint64_t rows, cols, dyStride, xStride, dxStride;
   float* partials;  // [splits][2][cols]: sums of dy u and of dy over a split's rows
   int splits;
+  bool together;  // the grid is one cluster, which joins its sums itself
   Layout l;
 };
 
@@ -551,14 +552,27 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
   }
   if constexpr (MODE != IN_CLUSTER) {
     __syncthreads();
-    const float* all = reinterpret_cast<const float*>(ring);
+    float* all = reinterpret_cast<float*>(ring);
     float* out = a.partials + (uint64_t)blockIdx.x * 2 * a.cols;
     for (int i = threadIdx.x; i < 2 * cols; i += blockDim.x) {
       const int at0 = i < cols ? slot(i) : half + slot(i - cols);
       float t = all[at0];
       for (int k = 1; k < a.l.groups; ++k) t += all[k * 2 * half + at0];
-      out[i] = t;
+      if (a.together) all[at0] = t;
+      else out[i] = t;
     }
+    if (!a.together) return;
+    cluster_sync();
+    const int blocks = gridDim.x;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < 2 * cols; i += blocks * blockDim.x) {
+      const int at0 = i < cols ? slot(i) : half + slot(i - cols);
+      float t = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < blocks; ++k) t += load_remote(&all[at0], k);
+      W* to = static_cast<W*>(i < cols ? a.dw : a.db);
+      if (to) to[i < cols ? i : i - cols] = from_f32<W>(t);
+    }
+    cluster_sync();  // the others may still be reading this block's sums
   }
 }
 
@@ -680,6 +694,7 @@ bool planShape(uint64_t rows, uint64_t cols, bool ragged, int blockThreads, int 
   p->grid = gridFor(rows, &p->l, V, residentWarps(REGS, p->smem, p->threads), ragged, ROWS);
   return p->smem <= kMostShared;
 }
+constexpr unsigned kTogether = 16;
 enum { NO_PLAN = 0, TWO_ROWS = 1, ONE_ROW = 2 };
 template <typename T>
 int planBackward(uint64_t rows, uint64_t cols, bool ragged, BwdPlan* p) {
@@ -722,7 +737,26 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
   a.l.skew = skew;
   a.splits = (int)(p.grid / p.l.ctas);
   if (!k) return false;
-  *r = allowShared(k) ? launch(k, dim3(p.grid), dim3(p.threads), p.smem, st, a, p.l.ctas)
+  // Small calls: one cluster, each group of it up to 8 rows, and nothing left to
+  // join. The launch that it saves is 3 us of the host's time, against up to 2
+  // on the GPU (64 x 64 float32 3.7 us against 4.5, 256 x 1024 bf16 6.6 against
+  // 6.4, 200 x 1280 float32 9.5 against 7.4; 1000 x 1024 bf16 12.2 against 6.9).
+  const uint64_t groups = (uint64_t)p.l.groups;
+  if ((a.dw || a.db) && p.mode != IN_CLUSTER && a.rows <= groups * kTogether * 8 &&
+      a.rows * a.cols <= 1u << 18) {
+    unsigned blocks = 1;
+    while (blocks < kTogether && blocks * groups * 2 < a.rows) blocks *= 2;
+    if (ragged && blocks * groups % kV<T>) blocks = kTogether;
+    a.together = true;
+    p.grid = blocks;
+    a.l.step = (uint32_t)(blocks * groups);
+    if (!allowLargeClusters(k)) {
+      *r = vrCudaError;
+      return true;
+    }
+  }
+  *r = allowShared(k) ? launch(k, dim3(p.grid), dim3(p.threads), p.smem, st, a,
+                               a.together ? (int)p.grid : p.l.ctas)
                       : vrCudaError;
   return true;
 }
@@ -818,7 +852,7 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
     return vrInvalidArgument;
   const bool params = dweight || dbias;
   BwdArgs a = {dy, x, weight, mean, rstd, dx, dweight, dbias, rows, cols,
-               dyStride, xStride, dxStride, (float*)workspace, splitsFor(rows, cols), {}};
+               dyStride, xStride, dxStride, (float*)workspace, splitsFor(rows, cols), false, {}};
   size_t need = 0;
   if (params && (vrLayerNormBackwardWorkspace(rows, cols, dtype, &need) != vrSuccess ||
                  !workspace || misaligned(workspace, 16) || workspaceBytes < need))
@@ -837,7 +871,7 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
         r = launch((const void*)&vrLnColumns<T>, dim3((unsigned)((cols + 31) / 32), a.splits),
                    dim3(32 * kColWarps), 0, st, a);
     }
-    if (r == vrSuccess && params)
+    if (r == vrSuccess && params && !a.together)
       r = launch((const void*)&vrLnJoin<W>, dim3((unsigned)((cols + 31) / 32), 2),
                  dim3(32 * kJoinWarps), 0, st, a);
     return r;

@@ -197,6 +197,14 @@ __device__ __forceinline__ void store_remote(float* p, uint32_t cta, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ float load_remote(const float* p, uint32_t cta) {
+  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(cta));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
+
 // Sums of N values (N rows') over the threads of a row, the same in each of
 // them. In a warp the N values share the steps: after log2(N) of them a lane
 // holds one value, that of row (lane & (N - 1)). Between warps two halves of the
@@ -318,17 +326,17 @@ inline bool setOnce(const void* kernel, cudaFuncAttribute what, int value) {
   constexpr int kSeen = 256;
   static std::mutex m;
   static const void* seen[kSeen];
-  static int device[kSeen], n = 0;
+  static int device[kSeen], attribute[kSeen], n = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   std::lock_guard<std::mutex> g(m);
   for (int i = 0; i < n; ++i)
-    if (seen[i] == kernel && device[i] == dev) return true;
+    if (seen[i] == kernel && device[i] == dev && attribute[i] == (int)what) return true;
   if (cudaFuncSetAttribute(kernel, what, value) != cudaSuccess) {
     cudaGetLastError();
     return false;
   }
-  if (n < kSeen) seen[n] = kernel, device[n++] = dev;
+  if (n < kSeen) seen[n] = kernel, attribute[n] = (int)what, device[n++] = dev;
   return true;
 }
 inline bool allowShared(const void* kernel) {

@@ -87,9 +87,14 @@ def _check_param(p, x, cols, device, other=None):
         raise ValueError("weight and bias must have one type: x's or float32")
 
 
-def _check_like(t, x, what):
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+def _check_like(t, x, device, what):
+    if t.get_device() != device or t.dtype != x.dtype or t.shape != x.shape:
         raise ValueError(f"{what} must have x's shape, type and device")
+
+
+def _dense_like(x):
+    return torch.empty_like(x) if x.is_contiguous() else \
+        torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _ptr(t):
@@ -112,9 +117,9 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, stats=True, out=None
         wcode = _NORM_CODE[bias.dtype]
     rows, xs = _rows(x, "x")
     if out is None:
-        y, ys = torch.empty_like(x, memory_format=torch.contiguous_format), cols
+        y, ys = _dense_like(x), cols
     else:
-        _check_like(out, x, "out")
+        _check_like(out, x, device, "out")
         y, ys = out, _rows(out, "out")[1]
     mean = rstd = None
     if stats:
@@ -144,7 +149,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
         return _on(stream, layer_norm_backward, dy, x, mean, rstd, weight, dx, dweight, dbias)
     cols, code, device = _check_x(x)
     rows, xs = _rows(x, "x")
-    _check_like(dy, x, "dy")
+    _check_like(dy, x, device, "dy")
     dys = _rows(dy, "dy")[1]
     for t in (mean, rstd):
         if t.dtype != _F32 or t.get_device() != device or t.numel() != rows or \
@@ -163,9 +168,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
     wt = x.dtype if wt is None else wt.dtype
     dxs = cols
     if dx is True:
-        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        dx = _dense_like(x)
     elif isinstance(dx, torch.Tensor):
-        _check_like(dx, x, "dx")
+        _check_like(dx, x, device, "dx")
         dxs = _rows(dx, "dx")[1]
     else:
         dx = None
@@ -175,7 +180,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
         ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
         for i in (0, 1):
             if grads[i] is True:
-                grads[i] = torch.empty(cols, dtype=wt, device=x.device)
+                grads[i] = torch.empty_like(weight) if weight is not None else \
+                    torch.empty(cols, dtype=wt, device=x.device)
     elif dx is None:
         return None, None, None
     dw, db = grads
