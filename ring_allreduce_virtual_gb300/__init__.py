@@ -9,6 +9,9 @@ CPU fallback: if libvr.so has not been built, every call raises ImportError.
                            chunk_bytes=512 << 10)
     comm.all_reduce(send_tensors, recv_tensors, op="sum")   # on the current stream
 
+The operators of a training step around it (layer norm forward and backward,
+the norm of a list of gradients, clipping by it) are the module `training`.
+
 Build the library with `python -m ring_allreduce_virtual_gb300.build`.
 """
 import ctypes
