@@ -12,11 +12,12 @@
 // shared memory.
 //
 // All of it is bound by HBM (2 or 3 flop an element). The norm reads every
-// element once; clipping reads it again, from L2 for what the first kernel read
-// last, and writes it. Measured on a GB300: the norms of 0.94 GB of bf16 in 288
-// tensors 139 us (1.0 of the measured copy peak, reads alone being a little
-// faster than copies); clipping 1.06 GB of float32 490 us and 1.15 GB of mixed
-// odd-sized tensors 532 us, 0.96 of what two reads and a write take at that peak.
+// element once. Clipping reads it again, as the factor needs all of them, and
+// writes it; lists of some 25 MB are still in L2 then, of 197 MB nothing is.
+// Measured on a GB300: the norms of 0.94 GB of bf16 in 288 tensors 138 us (1.01
+// of the measured copy peak: reads alone are a little faster than copies);
+// clipping 1.06 GB of float32 498 us and 1.15 GB of mixed odd-sized tensors 544
+// us, 0.94 of what two reads and a write take at that peak.
 #include "vr_ln_rows.cuh"
 
 namespace {
@@ -500,7 +501,7 @@ __device__ __forceinline__ void scaleAt(const A& a, int t, uint32_t k, const Fac
 }
 
 // Every block adds the slots up for itself, then takes tiles in turn, from the
-// list's end to its start: what the first kernel read last is still in L2.
+// list's end to its start, so that a list that fits L2 is found there.
 template <int CAP>
 __global__ void __launch_bounds__(Block::threads, kScaleBlocks)
     vrClip(const __grid_constant__ LongTable<CAP> a) {

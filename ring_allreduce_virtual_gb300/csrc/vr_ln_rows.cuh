@@ -287,8 +287,9 @@ struct Place {
       row = (uint64_t)blockIdx.x * l.groups + group;
       first = MODE == IN_WARP ? (uint64_t)blockIdx.x * l.groups + (threadIdx.x & ~31) / l.tpr : row;
     }
-    n = row < rows ? (int)((rows - row + l.step - 1) / l.step) : 0;
-    rounds = first < rows ? (int)((rows - first + l.step - 1) / l.step) : 0;
+    // fewer than kMostRows rows: 32-bit divisions
+    n = row < rows ? (int)(((uint32_t)(rows - row) + l.step - 1) / l.step) : 0;
+    rounds = first < rows ? (int)(((uint32_t)(rows - first) + l.step - 1) / l.step) : 0;
     stripe = MODE == IN_WARP ? l.tpr : 32;
     const int shift = (int)((l.offset + (uint32_t)row * (uint32_t)l.skew) & 15) / (int)sizeof(T);
     head = (V - shift) & (V - 1);
