@@ -383,9 +383,15 @@ __global__ void __launch_bounds__(Block::threads, kSumBlocks)
 // The sum of n slots, the same in every thread.
 template <typename S>
 __device__ Total sumSlots(const uint64_t* slots, uint32_t n, uint64_t* buf) {
+  constexpr int kAtOnce = 4;  // loads in flight
   Total t;
-#pragma unroll 4
-  for (uint32_t i = S::id(); i < n; i += S::threads) t.add(slots[i]);
+  for (uint32_t i = S::id(); i < n; i += kAtOnce * S::threads) {
+    uint64_t v[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) v[j] = i + j * S::threads < n ? slots[i + j * S::threads] : 0;
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) t.add(v[j]);
+  }
   return team_sum<S>(t, buf);
 }
 
@@ -445,9 +451,11 @@ struct Factor {
 };
 
 // One tile of out = g * factor: 16-byte packs where g and out lie alike modulo
-// 16 bytes, elements elsewhere. Each product is rounded once.
+// 16 bytes, elements elsewhere. Each product is rounded once. `loaded`: `v` holds
+// the packs of a whole tile.
 template <typename S, typename T, typename F>
-__device__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F factor) {
+__device__ __forceinline__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F factor,
+                                          bool loaded, const uint4 (&v)[S::packs]) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr uint64_t E = S::tileBytes / sizeof(T);
   auto mul = [factor](T x) -> T {
@@ -468,51 +476,75 @@ __device__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F fact
   const int n = (int)(left < E ? left : E);
   const T* p = g + head + k * E;
   T* q = out + head + k * E;
-  const int packs = ((uintptr_t)q & 15) == 0 ? n / V : 0;
-  if (packs == S::tileBytes / 16) {
-    uint4 v[S::packs];
-#pragma unroll
-    for (int j = 0; j < S::packs; ++j) v[j] = load16(p + (S::id() + j * S::threads) * V);
+  if (loaded) {
 #pragma unroll
     for (int j = 0; j < S::packs; ++j)
       *reinterpret_cast<uint4*>(q + (S::id() + j * S::threads) * V) = mulPack(v[j]);
     return;
   }
+  const int packs = ((uintptr_t)q & 15) == 0 ? n / V : 0;
   for (int i = S::id(); i < packs; i += S::threads)
     *reinterpret_cast<uint4*>(q + i * V) = mulPack(load16(p + i * V));
   for (int i = packs * V + S::id(); i < n; i += S::threads) q[i] = mul(p[i]);
 }
 
+// Tile k of the list, and its packs loaded if it is a whole one and its output
+// lies like it: what can be done before the factor is known.
+template <typename S>
+struct Tile {
+  int t;
+  uint32_t k;  // in tensor t
+  bool whole;
+  uint4 v[S::packs];
+  template <typename A>
+  __device__ __forceinline__ void load(const A& a, uint32_t at) {
+    t = tensorOf(a, at);
+    k = at - a.tile[t];
+    const char* g = static_cast<const char*>(a.in[t]);
+    const int es = sizeOfType(a.type[t]);
+    const uint64_t head = headOf(g, a.count[t], es) * es, bytes = a.count[t] * es;
+    const uint64_t from = head + (uint64_t)k * S::tileBytes;
+    whole = from + S::tileBytes <= bytes && (((uintptr_t)g - (uintptr_t)a.out[t]) & 15) == 0;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < S::packs; ++j) v[j] = load16(g + from + (S::id() + j * S::threads) * 16);
+    }
+  }
+};
+
 template <typename S, typename A>
-__device__ __forceinline__ void scaleAt(const A& a, int t, uint32_t k, const Factor& by,
-                                        const Total& s) {
-  const void* g = a.in[t];
-  void* o = a.out[t];
-  const uint64_t n = a.count[t];
-  k -= a.tile[t];
-  switch (a.type[t]) {
-    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, k, by.f);
-    case vrBfloat16: return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, k, by.f);
-    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, k, by.f);
+__device__ __forceinline__ void scale(const A& a, const Tile<S>& at, const Factor& by,
+                                      const Total& s) {
+  const void* g = a.in[at.t];
+  void* o = a.out[at.t];
+  const uint64_t n = a.count[at.t];
+  switch (a.type[at.t]) {
+    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, at.k, by.f, at.whole, at.v);
+    case vrBfloat16:
+      return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, at.k, by.f, at.whole, at.v);
+    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, at.k, by.f, at.whole, at.v);
     default:
-      return scaleTile<S>((const double*)g, (double*)o, n, k,
-                          Factor::of(s, a.scale, a.maxNorm, by.clips));
+      return scaleTile<S>((const double*)g, (double*)o, n, at.k,
+                          Factor::of(s, a.scale, a.maxNorm, by.clips), at.whole, at.v);
   }
 }
 
-// Every block adds the slots up for itself, then takes tiles in turn, from the
-// list's end to its start, so that a list that fits L2 is found there.
+// Every block adds the slots up for itself, while its first tile is on its way,
+// then takes tiles in turn, from the list's end to its start, so that a list
+// that fits L2 is found there.
 template <int CAP>
 __global__ void __launch_bounds__(Block::threads, kScaleBlocks)
     vrClip(const __grid_constant__ LongTable<CAP> a) {
   __shared__ uint64_t buf[Block::warps + 1];
   begin_kernel();
+  Tile<Block> tile;
+  if (blockIdx.x < a.nTiles) tile.load(a, a.nTiles - 1 - blockIdx.x);
   const Total s = sumSlots<Block>(a.slots, a.nSlots, buf);
   const Factor by(s, a.scale, a.maxNorm);
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = by.norm;
   for (uint32_t i = blockIdx.x; i < a.nTiles; i += gridDim.x) {
-    const uint32_t k = a.nTiles - 1 - i;
-    scaleAt<Block>(a, tensorOf(a, k), k, by, s);
+    if (i != blockIdx.x) tile.load(a, a.nTiles - 1 - i);
+    scale(a, tile, by, s);
   }
 }
 
@@ -520,7 +552,7 @@ __global__ void __launch_bounds__(Block::threads, kScaleBlocks)
 // block's shared memory. Where `out` is there, each warp scales its unit. The
 // table is copied to shared memory first, as lookups of single parameters would
 // each wait for the constant cache.
-__global__ void __launch_bounds__(32 * kShortWarps)
+__global__ void __launch_bounds__(32 * kShortWarps, 1)
     vrShortList(const __grid_constant__ Table<kShortList> p) {
   __shared__ Table<kShortList> a;
   __shared__ uint64_t slots[kShortUnits + kShortList];
@@ -555,8 +587,11 @@ __global__ void __launch_bounds__(32 * kShortWarps)
   }
   if (a.maxNorm < 0.f) return;  // the norm alone
   const uint32_t k1 = firstTile(a.nTiles, a.nUnits, u + 1);
-  for (uint32_t k = firstTile(a.nTiles, a.nUnits, u); k < k1; ++k)
-    scaleAt<Warp>(a, tensorOf(a, k), k, by, s);
+  for (uint32_t k = firstTile(a.nTiles, a.nUnits, u); k < k1; ++k) {
+    Tile<Warp> tile;
+    tile.load(a, k);
+    scale(a, tile, by, s);
+  }
 }
 
 // ------------------------------------------------------------------ host
