@@ -636,43 +636,64 @@ bool forwardShape(FwdArgs& a, bool ragged, int blockThreads, int maxThreads, cud
 }
 
 // Rows that are kept in registers: all but the widest. The shapes were chosen by
-// measuring on a GB300 (x read and y written once, of the measured copy peak).
-// 16 elements of 2 rows a thread carry the narrow rows (256 bf16 0.90, 1024 bf16
-// 0.90, 1280 float32 0.91) and ragged 16-bit rows up to 4096. Whole packs of
-// 16-bit rows over 1024 do better with 32 elements a thread, as fewer threads
-// share each sum (4096 bf16 0.91 against 0.88, 1600 0.87 against 0.77); ragged
-// 16-bit rows up to 2048 with 4 rows at a time, as the one-element loads of
-// their ends are latency (2051 bf16 0.77 against 0.68). Wider rows take 32
-// elements of one row a thread (4096 float32 0.93 against 0.85 with 16 of two,
-// 8192 bf16 0.91, 16384 0.77), beyond 512 threads a cluster, whose barrier is
-// paid twice a row (32768 bf16 0.46, 65536 0.26).
+// measuring on a GB300 (x read and y written once, of the measured copy peak);
+// what decides is how many warps an SM holds, how many share a row's sums, and
+// that no register is spilled (the ends of ragged rows take a few more).
+//  16 elements of 2 rows a thread: narrow rows (256 bf16 0.90, 1024 bf16 0.90),
+//    float32 up to 4096 (3000 0.96; with 32 of one row 0.69), and ragged rows up
+//    to 8192 (8191 bf16 0.69, 3001 float32 0.84; 0.55 and 0.52).
+//  32 elements of 2 rows: whole packs of 16-bit rows over 1024 (4096 bf16 0.92
+//    against 0.88, 6000 0.84 against 0.66 with one row), and all rows up to 12288
+//    beyond the above (12288 bf16 0.86 against 0.69, 10240 float32 0.90 against
+//    0.66) -- but for 7 or 8 warps a row, of which an SM holds one row only.
+//  16 elements of 4 rows: ragged 16-bit rows up to 2048, whose one-element loads
+//    are latency (2051 bf16 0.77 against 0.68).
+//  32 elements of one row: the rest (8192 bf16 0.91 against 0.80, 16384 0.77);
+//    beyond 512 threads clusters, whose barrier is paid twice a row (32768 bf16
+//    0.46, 65536 0.26); of ragged float32 rows clusters of the first shape.
 template <typename T, typename W>
 bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
   constexpr bool half = sizeof(T) == 2;
   a.l.offset = (int)((uintptr_t)a.x & 15);
   a.l.skew = (int)((a.xStride * sizeof(T)) & 15);
   const bool ragged = a.l.offset || a.l.skew || a.cols % kV<T>;
+  const uint64_t warps = (a.cols / 32 + 31) / 32;  // of a row, 32 elements a thread
+  const bool oneRow = warps == 7 || warps == 8;
   if constexpr (half) {
-    if (!ragged && a.cols > 1024 &&
-        forwardShape<T, W, 32, 2, 2, 168, BLOCK | WHOLE>(a, ragged, 128, 128, st, r))
+    if (!ragged && a.cols > 1024 && !oneRow &&
+        forwardShape<T, W, 32, 2, 2, 168, BLOCK | WHOLE>(a, ragged, 128, 384, st, r))
       return true;
     if (ragged && forwardShape<T, W, 16, 4, 2, 168, NARROW | BLOCK | CUT>(a, ragged, 128, 128, st, r))
       return true;
+    return forwardShape<T, W, 16, 2, 2, 128, NARROW | BLOCK | WHOLE | CUT>(
+               a, ragged, 256, ragged ? 512 : 64, st, r) ||
+           (ragged && forwardShape<T, W, 32, 2, 2, 168, BLOCK | CUT>(a, ragged, 128, 384, st, r)) ||
+           forwardShape<T, W, 32, 1, 3, 128, BLOCK | CLUSTER | WHOLE | CUT>(a, ragged, 256, 512, st, r);
+  } else {
+    // Just under 128 threads of 32 elements (4096 0.92 against 0.86 with 16 of two
+    // rows; 3500 0.80 against 0.89).
+    const bool full = !ragged && a.cols > 3840 && a.cols <= 4096;
+    return (!full && forwardShape<T, W, 16, 2, 2, 128, NARROW | BLOCK | WHOLE | CUT>(
+                         a, ragged, 256, ragged ? 512 : 256, st, r)) ||
+           (!full && forwardShape<T, W, 32, 2, 2, 168, BLOCK | WHOLE | CUT>(a, ragged, 128, 384, st,
+                                                                           r)) ||
+           (ragged ? forwardShape<T, W, 16, 2, 2, 128, CLUSTER | CUT>(a, ragged, 256, 512, st, r)
+                   : forwardShape<T, W, 32, 1, 3, 128, BLOCK | CLUSTER | WHOLE>(a, ragged, 256, 512,
+                                                                               st, r));
   }
-  constexpr int both = NARROW | BLOCK | WHOLE | CUT, wide = BLOCK | CLUSTER | WHOLE | CUT;
-  return forwardShape<T, W, 16, 2, 2, 128, both>(a, ragged, 256, half ? 256 : 128, st, r) ||
-         forwardShape<T, W, 32, 1, 3, 128, wide>(a, ragged, 256, 512, st, r);
 }
 
 // How a backward pass is laid out, and the sums of dw and db that it leaves.
-// The shape was chosen by measuring on a GB300 (dy and x read and dx written
-// once, of the measured copy peak): 16 elements of 2 rows a thread, the blocks
-// as large as one for each SM can be, which leaves the fewest sums to join (8192
-// bf16 0.95, 4096 bf16 0.91, 1024 bf16 0.90). float32 rows take 256 threads
-// of it (4096 0.94), as the ring of 512 would not fit, and beyond 4096 one row at
-// a time (8192 0.92 against 0.84 with two in clusters). Rows wider than 512
-// threads are a cluster's, which waits for its slowest block at every row (16384
-// bf16 0.65, float32 0.73; 32768 bf16 0.37).
+// The shapes were chosen by measuring on a GB300 (dy and x read and dx written
+// once, of the measured copy peak). 16 elements of 2 rows a thread, the blocks
+// as large as one for each SM can be, leave the fewest sums to join (8192 bf16
+// 0.95, 4096 bf16 0.91, 1024 bf16 0.90). float32 rows take 256 threads of it
+// (4096 0.94), as the ring of 512 would not fit, and beyond 4096 one row at a
+// time (8192 0.92 against 0.84 with two in clusters). Rows too wide for that are
+// 384 threads' with 32 elements of each row, up to 12288 (12288 bf16 0.77
+// against 0.55 in clusters, 10240 float32 0.82 against 0.60), and then clusters',
+// which wait for their slowest block at every row (16384 bf16 0.65, float32
+// 0.77; 32768 bf16 0.37).
 struct BwdPlan {
   Layout l;
   int mode, threads;
@@ -695,13 +716,18 @@ bool planShape(uint64_t rows, uint64_t cols, bool ragged, int blockThreads, int 
   return p->smem <= kMostShared;
 }
 constexpr unsigned kTogether = 16;
-enum { NO_PLAN = 0, TWO_ROWS = 1, ONE_ROW = 2 };
+enum { NO_PLAN = 0, TWO_ROWS = 1, ONE_ROW = 2, WIDE = 3 };
+template <typename T>
+constexpr int kWideRows = sizeof(T) == 2 ? 2 : 1;
 template <typename T>
 int planBackward(uint64_t rows, uint64_t cols, bool ragged, BwdPlan* p) {
   if (rows >= kMostRows) return NO_PLAN;
+  if (cols > 8192 + 8 &&
+      planShape<T, 32, kWideRows<T>, 2, 168>(rows, cols, ragged, 384, 384, p) && p->mode == IN_BLOCK)
+    return WIDE;
   if constexpr (sizeof(T) == 2)
     return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 512, 512, p) ? TWO_ROWS : NO_PLAN;
-  if (cols > 4096 && planShape<T, 16, 1, 3, 96>(rows, cols, ragged, 512, 512, p)) return ONE_ROW;
+  if (cols > 4096 && planShape<T, 16, 1, 3, 128>(rows, cols, ragged, 512, 512, p)) return ONE_ROW;
   return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 256, 256, p) ? TWO_ROWS : NO_PLAN;
 }
 
@@ -726,12 +752,15 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
   if constexpr (sizeof(T) == 4)
     if (shape == ONE_ROW) {
       if (p.mode == IN_BLOCK)
-        k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, true, 96>
-                   : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, false, 96>;
+        k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, true, 128>
+                   : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_BLOCK, false, 128>;
       else
-        k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, true, 96>
-                   : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, false, 96>;
+        k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, true, 128>
+                   : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, false, 128>;
     }
+  if (shape == WIDE)
+    k = ragged ? (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, true, 168>
+               : (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, false, 168>;
   a.l = p.l;
   a.l.offset = offset;
   a.l.skew = skew;

@@ -348,8 +348,10 @@ inline bool allowLargeClusters(const void* kernel) {
 }
 
 // How rows of `cols` elements are laid over threads: PACKS packs for each
-// thread, in a warp, a block, or a cluster of up to 8 blocks. False if the
-// row is too wide for it.
+// thread, in a warp, a block, or a cluster of up to 8 blocks; blocks of as many
+// rows as blockThreads hold (smaller blocks that fill an SM better are slower:
+// 1280 float32 forward 0.71 with 15 warps in 5 blocks, 0.91 with 12 in 2). False if
+// the row is too wide for it.
 inline bool layoutFor(uint64_t cols, int V, int packs, int blockThreads, int maxThreads,
                       bool ragged, Layout* l, int* mode) {
   const uint64_t n = cols / V;  // whole packs of a row, at most
