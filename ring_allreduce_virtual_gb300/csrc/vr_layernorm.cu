@@ -639,13 +639,15 @@ bool forwardShape(FwdArgs& a, bool ragged, int blockThreads, int maxThreads, cud
 // measuring on a GB300 (x read and y written once, of the measured copy peak);
 // what decides is how many warps an SM holds, how many share a row's sums, and
 // that no register is spilled (the ends of ragged rows take a few more).
-//  16 elements of 2 rows a thread: narrow rows (256 bf16 0.90, 1024 bf16 0.90),
+//  16 elements of 2 rows a thread: narrow rows (256 bf16 0.90, 1024 bf16 0.88),
 //    float32 up to 4096 (3000 0.96; with 32 of one row 0.69), and ragged rows up
 //    to 8192 (8191 bf16 0.69, 3001 float32 0.84; 0.55 and 0.52).
-//  32 elements of 2 rows: whole packs of 16-bit rows over 1024 (4096 bf16 0.92
-//    against 0.88, 6000 0.84 against 0.66 with one row), and all rows up to 12288
-//    beyond the above (12288 bf16 0.86 against 0.69, 10240 float32 0.90 against
-//    0.66) -- but for 7 or 8 warps a row, of which an SM holds one row only.
+//  32 elements of 2 rows: whole packs of 16-bit rows over 256 (4096 bf16 0.92
+//    against 0.88, 640 0.77 against 0.61, 6000 0.84 against 0.66 with one row),
+//    and all rows up to 12288 beyond the above (12288 bf16 0.86 against 0.69,
+//    10240 float32 0.90 against 0.66) -- but for 7 or 8 warps a row, of which an
+//    SM holds one row only, and 64 whole threads of the first shape (1024 bf16
+//    0.88 against 0.86).
 //  16 elements of 4 rows: ragged 16-bit rows up to 2048, whose one-element loads
 //    are latency (2051 bf16 0.77 against 0.68).
 //  32 elements of one row: the rest (8192 bf16 0.91 against 0.80, 16384 0.77);
@@ -660,14 +662,16 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
   const uint64_t warps = (a.cols / 32 + 31) / 32;  // of a row, 32 elements a thread
   const bool oneRow = warps == 7 || warps == 8;
   if constexpr (half) {
-    if (!ragged && a.cols > 1024 && !oneRow &&
-        forwardShape<T, W, 32, 2, 2, 168, BLOCK | WHOLE>(a, ragged, 128, 384, st, r))
+    const bool full = a.cols > 960 && a.cols <= 1024;  // 64 threads of 16 elements
+    if (!ragged && a.cols > 256 && !full && !oneRow &&
+        forwardShape<T, W, 32, 2, 2, 168, NARROW | BLOCK | WHOLE>(a, ragged, 128, 384, st, r))
       return true;
     if (ragged && forwardShape<T, W, 16, 4, 2, 168, NARROW | BLOCK | CUT>(a, ragged, 128, 128, st, r))
       return true;
-    return forwardShape<T, W, 16, 2, 2, 128, NARROW | BLOCK | WHOLE | CUT>(
-               a, ragged, 256, ragged ? 512 : 64, st, r) ||
-           (ragged && forwardShape<T, W, 32, 2, 2, 168, BLOCK | CUT>(a, ragged, 128, 384, st, r)) ||
+    return (ragged ? forwardShape<T, W, 16, 2, 2, 128, BLOCK | CUT>(a, ragged, 256, 512, st, r) ||
+                         forwardShape<T, W, 32, 2, 2, 168, BLOCK | CUT>(a, ragged, 128, 384, st, r)
+                   : forwardShape<T, W, 16, 2, 2, 128, NARROW | BLOCK | WHOLE>(a, ragged, 256, 64,
+                                                                               st, r)) ||
            forwardShape<T, W, 32, 1, 3, 128, BLOCK | CLUSTER | WHOLE | CUT>(a, ragged, 256, 512, st, r);
   } else {
     // Just under 128 threads of 32 elements (4096 0.92 against 0.86 with 16 of two
@@ -687,7 +691,9 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
 // The shapes were chosen by measuring on a GB300 (dy and x read and dx written
 // once, of the measured copy peak). 16 elements of 2 rows a thread, the blocks
 // as large as one for each SM can be, leave the fewest sums to join (8192 bf16
-// 0.95, 4096 bf16 0.91, 1024 bf16 0.90). float32 rows take 256 threads of it
+// 0.95, 4096 bf16 0.91, 1024 bf16 0.90). Whole packs of 257 to 768 16-bit
+// elements are one warp's at 32 elements a lane, which saves the barriers (768
+// 0.84 against 0.78, 640 0.71 against 0.65; 896 0.84 against 0.87). float32 rows take 256 threads of it
 // (4096 0.94), as the ring of 512 would not fit, and beyond 4096 one row at a
 // time (8192 0.92 against 0.84 with two in clusters). Rows too wide for that are
 // 384 threads' with 32 elements of each row, up to 12288 (12288 bf16 0.77
@@ -716,7 +722,7 @@ bool planShape(uint64_t rows, uint64_t cols, bool ragged, int blockThreads, int 
   return p->smem <= kMostShared;
 }
 constexpr unsigned kTogether = 16;
-enum { NO_PLAN = 0, TWO_ROWS = 1, ONE_ROW = 2, WIDE = 3 };
+enum { NO_PLAN = 0, TWO_ROWS = 1, ONE_ROW = 2, WIDE = 3, ONE_WARP = 4 };
 template <typename T>
 constexpr int kWideRows = sizeof(T) == 2 ? 2 : 1;
 template <typename T>
@@ -725,8 +731,12 @@ int planBackward(uint64_t rows, uint64_t cols, bool ragged, BwdPlan* p) {
   if (cols > 8192 + 8 &&
       planShape<T, 32, kWideRows<T>, 2, 168>(rows, cols, ragged, 384, 384, p) && p->mode == IN_BLOCK)
     return WIDE;
-  if constexpr (sizeof(T) == 2)
+  if constexpr (sizeof(T) == 2) {
+    if (!ragged && cols > 256 && cols <= 768 &&
+        planShape<T, 32, 2, 2, 168>(rows, cols, ragged, 384, 32, p))
+      return ONE_WARP;
     return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 512, 512, p) ? TWO_ROWS : NO_PLAN;
+  }
   if (cols > 4096 && planShape<T, 16, 1, 3, 128>(rows, cols, ragged, 512, 512, p)) return ONE_ROW;
   return planShape<T, 16, 2, 2, 128>(rows, cols, ragged, 256, 256, p) ? TWO_ROWS : NO_PLAN;
 }
@@ -758,6 +768,9 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
         k = ragged ? (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, true, 128>
                    : (const void*)&vrLnBackwardRows<T, W, 16, 1, 3, IN_CLUSTER, false, 128>;
     }
+  if constexpr (sizeof(T) == 2)
+    if (shape == ONE_WARP)
+      k = (const void*)&vrLnBackwardRows<T, W, 32, 2, 2, IN_WARP, false, 168>;
   if (shape == WIDE)
     k = ragged ? (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, true, 168>
                : (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, false, 168>;

@@ -25,6 +25,17 @@ def test_layout_borders(rows, cols, dtype):
     check_backward(dy, x, mean, rstd, w, dx, dw, db)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("cols", [256, 264, 320, 640, 760, 768, 776, 960, 968, 1024])
+@pytest.mark.parametrize("rows", [1, 47, 400, 3000])
+def test_rows_of_one_warp(rows, cols, dtype):
+    x, w, b, dy = inputs(rows + cols, rows, cols, dtype, dtype)
+    y, mean, rstd = training.layer_norm_forward(x, w, b, EPS)
+    check_forward(x, w, b, y, mean, rstd)
+    dx, dw, db = training.layer_norm_backward(dy, x, mean, rstd, w)
+    check_backward(dy, x, mean, rstd, w, dx, dw, db)
+
+
 @pytest.mark.parametrize("rows,cols", [(2, 40), (250, 64), (256, 1024), (257, 1024), (64, 4096), (65, 4096),
                                        (31, 8192), (33, 7000), (200, 1280), (205, 1281), (4096, 64), (4097, 64)])
 def test_small_calls_write_nothing_but_their_outputs(rows, cols):
