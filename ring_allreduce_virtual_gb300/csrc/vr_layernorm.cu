@@ -630,8 +630,14 @@ bool forwardShape(FwdArgs& a, bool ragged, int blockThreads, int maxThreads, cud
   if (!k) return false;
   const int threads = a.l.tpr * a.l.groups;
   const size_t smem = (size_t)STAGES * ROWS * E * sizeof(T) * threads;
-  const unsigned grid = gridFor(a.rows, &a.l, V, residentWarps(REGS, smem, threads), ragged, ROWS);
-  *result = allowShared(k) ? launch(k, dim3(grid), dim3(threads), smem, st, a, a.l.ctas) : vrCudaError;
+  if (!allowShared(k)) {
+    *result = vrCudaError;
+    return true;
+  }
+  uint64_t most = mostAtOnce(a.l, residentWarps(REGS, smem, threads));
+  if (mode == IN_CLUSTER) most = clustersAtOnce(k, a.l, smem, most);
+  const unsigned grid = gridFor(a.rows, &a.l, V, most, ragged, ROWS);
+  *result = launch(k, dim3(grid), dim3(threads), smem, st, a, a.l.ctas);
   return true;
 }
 
@@ -650,9 +656,12 @@ bool forwardShape(FwdArgs& a, bool ragged, int blockThreads, int maxThreads, cud
 //    0.88 against 0.86).
 //  16 elements of 4 rows: ragged 16-bit rows up to 2048, whose one-element loads
 //    are latency (2051 bf16 0.77 against 0.68).
-//  32 elements of one row: the rest (8192 bf16 0.91 against 0.80, 16384 0.77);
-//    beyond 512 threads clusters, whose barrier is paid twice a row (32768 bf16
-//    0.46, 65536 0.26); of ragged float32 rows clusters of the first shape.
+//  32 elements of one row: the rest (8192 bf16 0.91 against 0.80, 16384 0.81).
+//  Clusters, whose barrier is paid twice for each set of rows: of 32 elements of
+//    2 rows in blocks of 384 threads where these are as few as of 512 (24576 bf16
+//    0.56 against 0.40, 49152 0.53 against 0.36, 24576 float32 0.70 against 0.48),
+//    else of one row (32768 bf16 0.46 against 0.44, 65536 0.43 against 0.37), of
+//    float32 the first shape (32768 0.63 against 0.57) up to 65536.
 template <typename T, typename W>
 bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
   constexpr bool half = sizeof(T) == 2;
@@ -661,15 +670,23 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
   const bool ragged = a.l.offset || a.l.skew || a.cols % kV<T>;
   const uint64_t warps = (a.cols / 32 + 31) / 32;  // of a row, 32 elements a thread
   const bool oneRow = warps == 7 || warps == 8;
+  const auto blocks = [&](uint64_t threads) {  // of a row, 32 elements a thread
+    uint64_t n = 1;
+    while (n <= 8 && n * threads * 32 < a.cols / kV<T> * kV<T>) n *= 2;
+    return n;
+  };
+  const bool asFew = blocks(384) == blocks(512);
   if constexpr (half) {
     const bool full = a.cols > 960 && a.cols <= 1024;  // 64 threads of 16 elements
-    if (!ragged && a.cols > 256 && !full && !oneRow &&
-        forwardShape<T, W, 32, 2, 2, 168, NARROW | BLOCK | WHOLE>(a, ragged, 128, 384, st, r))
+    if (!ragged && a.cols > 256 && !full && !oneRow && asFew &&
+        forwardShape<T, W, 32, 2, 2, 168, NARROW | BLOCK | CLUSTER | WHOLE>(a, ragged, 128, 384, st,
+                                                                            r))
       return true;
     if (ragged && forwardShape<T, W, 16, 4, 2, 168, NARROW | BLOCK | CUT>(a, ragged, 128, 128, st, r))
       return true;
     return (ragged ? forwardShape<T, W, 16, 2, 2, 128, BLOCK | CUT>(a, ragged, 256, 512, st, r) ||
-                         forwardShape<T, W, 32, 2, 2, 168, BLOCK | CUT>(a, ragged, 128, 384, st, r)
+                         (asFew && forwardShape<T, W, 32, 2, 2, 168, BLOCK | CLUSTER | CUT>(
+                                       a, ragged, 128, 384, st, r))
                    : forwardShape<T, W, 16, 2, 2, 128, NARROW | BLOCK | WHOLE>(a, ragged, 256, 64,
                                                                                st, r)) ||
            forwardShape<T, W, 32, 1, 3, 128, BLOCK | CLUSTER | WHOLE | CUT>(a, ragged, 256, 512, st, r);
@@ -679,11 +696,12 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
     const bool full = !ragged && a.cols > 3840 && a.cols <= 4096;
     return (!full && forwardShape<T, W, 16, 2, 2, 128, NARROW | BLOCK | WHOLE | CUT>(
                          a, ragged, 256, ragged ? 512 : 256, st, r)) ||
-           (!full && forwardShape<T, W, 32, 2, 2, 168, BLOCK | WHOLE | CUT>(a, ragged, 128, 384, st,
-                                                                           r)) ||
-           (ragged ? forwardShape<T, W, 16, 2, 2, 128, CLUSTER | CUT>(a, ragged, 256, 512, st, r)
-                   : forwardShape<T, W, 32, 1, 3, 128, BLOCK | CLUSTER | WHOLE>(a, ragged, 256, 512,
-                                                                               st, r));
+           (!full && asFew && forwardShape<T, W, 32, 2, 2, 168, BLOCK | CLUSTER | WHOLE | CUT>(
+                                  a, ragged, 128, 384, st, r)) ||
+           ((ragged || a.cols > 16384) &&
+            forwardShape<T, W, 16, 2, 2, 128, CLUSTER | WHOLE | CUT>(a, ragged, 256, 512, st, r)) ||
+           (!ragged &&
+            forwardShape<T, W, 32, 1, 3, 128, BLOCK | CLUSTER | WHOLE>(a, ragged, 256, 512, st, r));
   }
 }
 
@@ -691,18 +709,19 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
 // The shapes were chosen by measuring on a GB300 (dy and x read and dx written
 // once, of the measured copy peak). 16 elements of 2 rows a thread, the blocks
 // as large as one for each SM can be, leave the fewest sums to join (8192 bf16
-// 0.95, 4096 bf16 0.91, 1024 bf16 0.90). Whole packs of 257 to 768 16-bit
+// 0.95, 4096 bf16 0.93, 1024 bf16 0.90). Whole packs of 257 to 768 16-bit
 // elements are one warp's at 32 elements a lane, which saves the barriers (768
-// 0.84 against 0.78, 640 0.71 against 0.65; 896 0.84 against 0.87). float32 rows take 256 threads of it
-// (4096 0.94), as the ring of 512 would not fit, and beyond 4096 one row at a
-// time (8192 0.92 against 0.84 with two in clusters). Rows too wide for that are
-// 384 threads' with 32 elements of each row, up to 12288 (12288 bf16 0.77
-// against 0.55 in clusters, 10240 float32 0.82 against 0.60), and then clusters',
-// which wait for their slowest block at every row (16384 bf16 0.65, float32
-// 0.77; 32768 bf16 0.37).
+// 0.84 against 0.78, 640 0.71 against 0.65; 896 0.84 against 0.87). float32 rows
+// take 256 threads of the first (4096 0.95), as the ring of 512 would not fit, and
+// beyond 4096 one row at a time (8192 0.92 against 0.84 with two in clusters). Rows
+// too wide for that are 384 threads' with 32 elements of each row, up to 12288
+// (12288 bf16 0.87 against 0.55 in clusters, 10240 float32 0.87 against 0.60), and
+// then clusters', which wait for their slowest block at every row (16384 bf16
+// 0.72, float32 0.80; 32768 bf16 0.65, 65536 0.53).
 struct BwdPlan {
   Layout l;
-  int mode, threads;
+  int mode, threads, rowsAtOnce;
+  uint64_t most;
   unsigned grid;
   size_t smem;
 };
@@ -718,7 +737,9 @@ bool planShape(uint64_t rows, uint64_t cols, bool ragged, int blockThreads, int 
                           ? 0
                           : (size_t)p->l.groups * 2 * ((cols + 7) * 9 / 8 + 1) * sizeof(float);
   p->smem = ring > join ? ring : join;
-  p->grid = gridFor(rows, &p->l, V, residentWarps(REGS, p->smem, p->threads), ragged, ROWS);
+  p->rowsAtOnce = ROWS;
+  p->most = mostAtOnce(p->l, residentWarps(REGS, p->smem, p->threads));
+  p->grid = gridFor(rows, &p->l, V, p->most, ragged, ROWS);
   return p->smem <= kMostShared;
 }
 constexpr unsigned kTogether = 16;
@@ -774,11 +795,17 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
   if (shape == WIDE)
     k = ragged ? (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, true, 168>
                : (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, false, 168>;
+  if (!k) return false;
+  if (!allowShared(k)) {
+    *r = vrCudaError;
+    return true;
+  }
+  if (p.mode == IN_CLUSTER)
+    p.grid = gridFor(a.rows, &p.l, kV<T>, clustersAtOnce(k, p.l, p.smem, p.most), ragged, p.rowsAtOnce);
   a.l = p.l;
   a.l.offset = offset;
   a.l.skew = skew;
   a.splits = (int)(p.grid / p.l.ctas);
-  if (!k) return false;
   // Small calls: one cluster, each group of it up to 8 rows, and nothing left to
   // join. The launch that it saves is 3 us of the host's time, against up to 2
   // on the GPU (64 x 64 float32 3.7 us against 4.5, 256 x 1024 bf16 6.6 against
@@ -797,9 +824,7 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
       return true;
     }
   }
-  *r = allowShared(k) ? launch(k, dim3(p.grid), dim3(p.threads), p.smem, st, a,
-                               a.together ? (int)p.grid : p.l.ctas)
-                      : vrCudaError;
+  *r = launch(k, dim3(p.grid), dim3(p.threads), p.smem, st, a, a.together ? (int)p.grid : p.l.ctas);
   return true;
 }
 

@@ -36,6 +36,18 @@ def test_rows_of_one_warp(rows, cols, dtype):
     check_backward(dy, x, mean, rstd, w, dx, dw, db)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("rows,cols", [(1, 16385), (75, 20000), (90, 20001), (77, 24576), (40, 24584), (3, 32768),
+                                       (39, 32769), (100, 49152), (37, 49160), (81, 65536), (20, 65537), (17, 90000),
+                                       (40, 98304), (16, 98312), (31, 131072), (9, 131080)])
+def test_rows_of_clusters(rows, cols, dtype):
+    x, w, b, dy = inputs(rows + cols, rows, cols, dtype, torch.float32)
+    y, mean, rstd = training.layer_norm_forward(x, w, b, EPS)
+    check_forward(x, w, b, y, mean, rstd)
+    dx, dw, db = training.layer_norm_backward(dy, x, mean, rstd, w)
+    check_backward(dy, x, mean, rstd, w, dx, dw, db)
+
+
 @pytest.mark.parametrize("rows,cols", [(2, 40), (250, 64), (256, 1024), (257, 1024), (64, 4096), (65, 4096),
                                        (31, 8192), (33, 7000), (200, 1280), (205, 1281), (4096, 64), (4097, 64)])
 def test_small_calls_write_nothing_but_their_outputs(rows, cols):
