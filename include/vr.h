@@ -343,8 +343,8 @@ VR_API vrResult_t vrRedOpDestroy(vrRedOp_t op, vrComm_t comm);
  * like vrAllReduce, allocate nothing, may be captured in a CUDA graph (the
  * pointers and sizes are then those of the capture), and run on the device
  * that is current. Sums are held in 32 bits or more and added up in a fixed
- * order (no atomics), so equal calls give equal bits; each result is rounded
- * once to its type. Outputs and workspaces overlap no other argument, except
+ * order (no atomics), so equal calls on one GPU give equal bits; each result is
+ * rounded once to its type. Outputs and workspaces overlap no other argument, except
  * where a call says so. The pages have no counterpart of them.
  * Common errors: vrInvalidArgument for a NULL or misaligned pointer (to the
  * element size; workspaces to 16 bytes), a type, size or stride outside what

@@ -715,9 +715,11 @@ bool forwardRows(FwdArgs& a, cudaStream_t st, vrResult_t* r) {
 // take 256 threads of the first (4096 0.95), as the ring of 512 would not fit, and
 // beyond 4096 one row at a time (8192 0.92 against 0.84 with two in clusters). Rows
 // too wide for that are 384 threads' with 32 elements of each row, up to 12288
-// (12288 bf16 0.87 against 0.55 in clusters, 10240 float32 0.87 against 0.60), and
-// then clusters', which wait for their slowest block at every row (16384 bf16
-// 0.72, float32 0.80; 32768 bf16 0.65, 65536 0.53).
+// (12288 bf16 0.87 against 0.55 in clusters, 10240 float32 0.87 against 0.60).
+// Then they are clusters', which wait for their slowest block at every row: of
+// these blocks where they are fewer than of the first kinds (24576 bf16 0.75
+// against 0.57, 49152 0.70 against 0.48, float32 0.88 and 0.84 against 0.64 and
+// 0.53), else of those (16384 bf16 0.72, float32 0.80; 32768 bf16 0.66, 65536 0.53).
 struct BwdPlan {
   Layout l;
   int mode, threads, rowsAtOnce;
@@ -750,8 +752,13 @@ template <typename T>
 int planBackward(uint64_t rows, uint64_t cols, bool ragged, BwdPlan* p) {
   if (rows >= kMostRows) return NO_PLAN;
   if (cols > 8192 + 8 &&
-      planShape<T, 32, kWideRows<T>, 2, 168>(rows, cols, ragged, 384, 384, p) && p->mode == IN_BLOCK)
-    return WIDE;
+      planShape<T, 32, kWideRows<T>, 2, 168>(rows, cols, ragged, 384, 384, p)) {
+    const int ctas = p->l.ctas;
+    Layout l;  // of the shapes below
+    int mode;
+    if (ctas == 1 || !layoutFor(cols, kV<T>, 16 / kV<T>, 512, 512, ragged, &l, &mode) || ctas < l.ctas)
+      return WIDE;
+  }
   if constexpr (sizeof(T) == 2) {
     if (!ragged && cols > 256 && cols <= 768 &&
         planShape<T, 32, 2, 2, 168>(rows, cols, ragged, 384, 32, p))
@@ -792,9 +799,14 @@ bool backwardRows(BwdArgs& a, cudaStream_t st, vrResult_t* r) {
   if constexpr (sizeof(T) == 2)
     if (shape == ONE_WARP)
       k = (const void*)&vrLnBackwardRows<T, W, 32, 2, 2, IN_WARP, false, 168>;
-  if (shape == WIDE)
-    k = ragged ? (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, true, 168>
-               : (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, false, 168>;
+  if (shape == WIDE) {
+    if (p.mode == IN_BLOCK)
+      k = ragged ? (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, true, 168>
+                 : (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_BLOCK, false, 168>;
+    else
+      k = ragged ? (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_CLUSTER, true, 168>
+                 : (const void*)&vrLnBackwardRows<T, W, 32, kWideRows<T>, 2, IN_CLUSTER, false, 168>;
+  }
   if (!k) return false;
   if (!allowShared(k)) {
     *r = vrCudaError;
