@@ -323,8 +323,9 @@ __device__ uint64_t sumTiles(const T* g, uint64_t count, uint32_t k0, uint32_t k
     // the tiles are summed again in 64 bits. float16's squares always fit.
     const bool fits = sum.hi >= kLeast && sum.hi <= kMost;
     if (std::is_same_v<T, __half> || fits || (sum.hi < kLeast && !team_any<S>(bits != 0))) {
-      const bool bad = !(sum.hi <= kMost) || !(fabsf(sum.lo) <= kMost);  // float16 inf, NaN
-      return bad ? slotOf((double)sum.hi + (double)sum.lo) : slotOf(sum);
+      // hi is infinite or NaN where float16 elements are; lo, the difference of two
+      // infinities, is NaN for both.
+      return sum.hi <= kMost ? slotOf(sum) : slotOf((double)sum.hi);
     }
     if (S::warps > 1) __syncthreads();  // before `buf` is used again
   }

@@ -174,6 +174,26 @@ def test_not_finite_gradients_are_not_clipped(what, dtype):
         assert torch.equal(c.nan_to_num(nan=3.0), (t * 0.5).nan_to_num(nan=3.0))
 
 
+@pytest.mark.parametrize("counts", [[4000, 9, 20000], [4000, 9, 3_000_000], [700] * 70 + [3_000_000]],
+                         ids=["short", "long", "many"])
+@pytest.mark.parametrize("dtype", TYPES, ids=lambda t: str(t)[6:])
+def test_norms_of_infinities_are_infinite_and_of_nans_nan(dtype, counts):
+    last = len(counts) - 1
+    for t, at in ((0, 0), (1, 4), (last, counts[-1] // 2 + 1), (last, counts[-1] - 1)):
+        for what in ([math.inf], [-math.inf], [math.nan], [math.inf, math.nan]):
+            ts = tensors(5, counts, [dtype])
+            for i, v in enumerate(what):
+                ts[t][at - i] = v
+            norm, norms = training.grad_norm(ts, per_tensor=True)
+            clipped = training.clip_grad_norm([x.clone() for x in ts], 1.0)
+            for got in (norm.item(), norms[t].item(), clipped.item()):
+                if any(map(math.isnan, what)):
+                    assert math.isnan(got)
+                else:
+                    assert got == math.inf
+            assert all(math.isfinite(v) for i, v in enumerate(norms.tolist()) if i != t)
+
+
 def test_lists_are_checked():
     a, b = torch.zeros(8, device="cuda"), torch.zeros(9, device="cuda")
     for bad in ([a[::2]], [a.int()], [a, torch.zeros(8)], [torch.zeros(4, 4, device="cuda").t()[:, :2]]):
