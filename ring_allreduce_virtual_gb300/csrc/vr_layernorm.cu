@@ -348,7 +348,6 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
   if constexpr (MODE == IN_CLUSTER) cluster_sync();  // the others' buffers are there
   const T* gp = static_cast<const T*>(a.dy) + at.row * a.dyStride;
   const T* xp = static_cast<const T*>(a.x) + at.row * a.xStride;
-  T* op = static_cast<T*>(a.dx) + at.row * a.dxStride;
   const uint64_t gStep = a.l.step * a.dyStride, xStep = a.l.step * a.xStride,
                  oStep = a.l.step * a.dxStride;
   const int apart = (MODE == IN_WARP ? at.stripe : 32) * V;  // elements between a thread's packs
@@ -433,7 +432,8 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
     for (int j = 0; j < V / 2; ++j) dw[i][j] = db[i][j] = f2(0.f);
   const float c = 1.f / (float)cols;
   int left = at.n, stage = 0;
-  T* oo = op + at.column(0);
+  T* oo = static_cast<T*>(a.dx) + at.row * a.dxStride + at.column(0);
+  const int edgeAt = at.edge - at.column(0);
   for (int round = 0; round < at.rounds; round += ROWS) {
     const int back = stage == 0 ? STAGES - 1 : stage - 1;
     fetch(left - (STAGES - 1) * ROWS, gf, xf, back);
@@ -497,8 +497,9 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
       sum(s, a.l, at.group, turn);
 #pragma unroll
       for (int k = 0; k < ROWS; ++k) {
-        // dx = r g - r s - (x - m) r^2 p, s and p the means of g and of g (x - m)
-        const float c0 = -r[k] * (s[2 * k] * c), c1 = -r[k] * r[k] * (r[k] * (s[2 * k + 1] * c));
+        // dx = r (g - s - (x - m) r p), s and p the means of g and of g u. Never r^2, which
+        // leaves the range of a float long before dx does.
+        const float c0 = -(s[2 * k] * c), c1 = -(r[k] * (r[k] * (s[2 * k + 1] * c)));
         const F2 minus = f2(-m[k]), r2 = f2(r[k]), c02 = f2(c0), c12 = f2(c1);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -509,17 +510,16 @@ __global__ void __maxnreg__(REGS) vrLnBackwardRows(const __grid_constant__ BwdAr
             w[i].get(ww);
 #pragma unroll
             for (int j = 0; j < V / 2; ++j)
-              x[j] = fma2(x[j] + minus, c12, fma2(g[j] * ww[j], r2, c02));
+              x[j] = fma2(x[j] + minus, c12, fma2(g[j], ww[j], c02)) * r2;
             *reinterpret_cast<uint4*>(oo + k * oStep + i * apart) = pack<T>(x);
           }
         }
         if (edges && at.edge >= 0 && k < left)
-          op[k * oStep + at.edge] = from_f32<T>(fmaf(de[k], c1, fmaf(ge[k], r[k], c0)));
+          oo[k * oStep + edgeAt] = from_f32<T>(fmaf(de[k], c1, ge[k] + c0) * r[k]);
       }
     }
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     left -= ROWS;
-    op += ROWS * oStep;
     oo += ROWS * oStep;
   }
   if (!a.dw && !a.db) return;

@@ -209,6 +209,25 @@ def test_not_finite_values_stay_in_their_row(cols, what):
     assert torch.equal(dx[keep], gdx[keep]) and torch.isnan(dx[5]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("cols", [96, 600, 1001, 4096, 10240, 20000])
+@pytest.mark.parametrize("power", [-80, 60])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_gradients_of_scaled_rows_scale(cols, power, dtype, pad):
+    # x, mean and 1 / rstd times a power of two: u, dw and db are the same bits,
+    # dx the same over it (without eps the formula has no scale of its own)
+    x, w, _, dy = inputs(cols, 40, cols, dtype, torch.float32)
+    _, mean, rstd = training.layer_norm_forward(x, w, None, EPS)
+
+    def gradients(c):
+        out = matrix(0, 40, cols, dtype, pad)[1]
+        return training.layer_norm_backward(dy, x * c, mean * c, rstd / c, w, out)
+
+    dx, dw, db = gradients(1.0)
+    sx, sw, sb = gradients(2.0 ** power)
+    assert torch.equal(sx * 2.0 ** power, dx) and torch.equal(sw, dw) and torch.equal(sb, db)
+
+
 @pytest.mark.parametrize("cols", [24, 333, 4096])
 def test_gradients_against_differences(cols):
     # d/dt of sum(dy * LN(x + t a, w + t c, b + t e)) by central differences of
