@@ -11,7 +11,8 @@ addresses. There is no CPU fallback.
     grads = training.TensorList([p.grad for p in params])
     norm = training.clip_grad_norm(grads, 1.0, scale=1 / n_ranks)   # in place
 
-Calls are asynchronous on the current torch stream, or on `stream`; outputs and
+Calls are asynchronous on the current torch stream of the tensors' device (which
+need not be the current device), or on `stream` of that device; outputs and
 workspaces are allocated there, so that they may be freed at any time. As with
 any torch operation, tensors that were made or are freed on another stream
 need the caller's own ordering (wait_stream, record_stream).
@@ -33,8 +34,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(stream, f, *args):
-    """f(*args) on `stream`: allocations go to that stream's pool too."""
+# The library launches on the device that is current. Where that is not the tensors',
+# a call makes it so for its duration.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_device(index, f, *args):
+    with torch.cuda.device(index):
+        return f(*args)
+
+
+def _on(stream, index, f, *args):
+    """f(*args) on `stream` of the tensors' device: allocations go to that
+    stream's pool too."""
+    if stream.device_index != index:
+        raise ValueError("the stream is not on the tensors' device")
     with torch.cuda.stream(stream):
         return f(*args)
 
@@ -106,8 +120,10 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, stats=True, out=None
     x's leading shape) are what the backward pass needs, None with
     stats=False. `out`: a tensor of x's shape and type for y, x itself allowed."""
     if stream is not None:
-        return _on(stream, layer_norm_forward, x, weight, bias, eps, stats, out)
+        return _on(stream, x.get_device(), layer_norm_forward, x, weight, bias, eps, stats, out)
     cols, code, device = _check_x(x)
+    if device != _current_device():
+        return _on_device(device, layer_norm_forward, x, weight, bias, eps, stats, out)
     wcode = code
     if weight is not None:
         _check_param(weight, x, cols, device)
@@ -146,8 +162,12 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
     gradients have the weight's type (x's without a weight, or the given
     tensors')."""
     if stream is not None:
-        return _on(stream, layer_norm_backward, dy, x, mean, rstd, weight, dx, dweight, dbias)
+        return _on(stream, x.get_device(), layer_norm_backward, dy, x, mean, rstd, weight, dx,
+                   dweight, dbias)
     cols, code, device = _check_x(x)
+    if device != _current_device():
+        return _on_device(device, layer_norm_backward, dy, x, mean, rstd, weight, dx, dweight,
+                          dbias)
     rows, xs = _rows(x, "x")
     _check_like(dy, x, device, "dy")
     dys = _rows(dy, "dy")[1]
@@ -257,9 +277,11 @@ def grad_norm(grads, scale=1.0, per_tensor=False, stream=None):
     """The 2-norm of all elements of `grads` (a TensorList or a sequence of
     tensors) times |scale|, a float32 scalar tensor; with per_tensor also the
     norms of the single tensors, a float32 vector."""
-    if stream is not None:
-        return _on(stream, grad_norm, grads, scale, per_tensor)
     grads = _list(grads)
+    if stream is not None:
+        return _on(stream, grads.index, grad_norm, grads, scale, per_tensor)
+    if grads.index != _current_device():
+        return _on_device(grads.index, grad_norm, grads, scale, per_tensor)
     device, nbytes = grads.device, grads.workspace_bytes
     norm = torch.empty((), dtype=_F32, device=device)
     norms = torch.empty(len(grads), dtype=_F32, device=device) if per_tensor else None
@@ -278,9 +300,11 @@ def clip_grad_norm(grads, max_norm, scale=1.0, outs=None, stream=None):
     place, or into `outs`, as many tensors of the same sizes and types. Returns
     that norm, a float32 scalar tensor. If it is not finite, only `scale` is
     applied."""
-    if stream is not None:
-        return _on(stream, clip_grad_norm, grads, max_norm, scale, outs)
     grads = _list(grads)
+    if stream is not None:
+        return _on(stream, grads.index, clip_grad_norm, grads, max_norm, scale, outs)
+    if grads.index != _current_device():
+        return _on_device(grads.index, clip_grad_norm, grads, max_norm, scale, outs)
     to = grads if outs is None else _list(outs)
     device, nbytes = grads.device, grads.workspace_bytes
     if to is not grads and (to.device != device or to.shape != grads.shape):
