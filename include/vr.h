@@ -345,7 +345,9 @@ VR_API vrResult_t vrRedOpDestroy(vrRedOp_t op, vrComm_t comm);
  * that is current. Sums are held in 32 bits or more and added up in a fixed
  * order (no atomics), so equal calls on one GPU give equal bits; each result is
  * rounded once to its type. Outputs and workspaces overlap no other argument, except
- * where a call says so. The pages have no counterpart of them.
+ * where a call says so; the rows of matrices with one stride may lie side by side
+ * in one buffer, those of two strides may not interleave. The pages have no
+ * counterpart of them.
  * Common errors: vrInvalidArgument for a NULL or misaligned pointer (to the
  * element size; workspaces to 16 bytes), a type, size or stride outside what
  * is stated, a short workspace, or buffers that overlap where that is not
@@ -424,7 +426,8 @@ VR_API vrResult_t vrGradNorm(const void* const* grads, const size_t* counts,
  * or NaN nothing is clipped (the factor is `scale`): read `norm` and drop the
  * step.
  *  outs     [host array of nTensors device pointers]; outs[t] == grads[t] is
- *           allowed, other overlaps are not.
+ *           allowed, other overlaps are not: neither with another gradient nor
+ *           between two outputs (a tensor listed twice, in place).
  *  maxNorm  >= 0, may be infinite.   norm [device] one float, or NULL.
  * Other arguments as for vrGradNorm. */
 VR_API vrResult_t vrClipGradNorm(const void* const* grads, void* const* outs,

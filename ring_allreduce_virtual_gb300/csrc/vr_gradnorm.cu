@@ -18,6 +18,10 @@
 // of the measured copy peak: reads alone are a little faster than copies);
 // clipping 1.06 GB of float32 498 us and 1.15 GB of mixed odd-sized tensors 544
 // us, 0.94 of what two reads and a write take at that peak.
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "vr_ln_rows.cuh"
 
 namespace {
@@ -735,10 +739,83 @@ vrResult_t checkList(const void* const* in, const size_t* counts, const vrDataTy
   return vrSuccess;
 }
 
+size_t bytesOfTensor(const Call& c, int t) { return c.counts[t] * elemSizeOf(c.types[t]); }
+
+// Tensors that are written: one after another in memory, upwards or downwards, as
+// the views of a bucket are. The others' hull alone counts.
+struct Run {
+  uintptr_t lo = UINTPTR_MAX, hi = 0, lastLo = 0, lastHi = 0;
+  bool up = true, down = true;
+  void add(uintptr_t p, size_t n) {
+    if (hi) {
+      up = up && p >= lastHi;
+      down = down && p + n <= lastLo;
+    }
+    lastLo = p, lastHi = p + n;
+    lo = p < lo ? p : lo;
+    hi = p + n > hi ? p + n : hi;
+  }
+  bool apartFrom(const Run& r) const { return lo >= r.hi || r.lo >= hi; }
+};
+
+// Whether outs overlap each other, or gradients other than outs[t] == grads[t].
+// A run for each type, with the runs apart, is what buckets give and takes one walk;
+// anything else is sorted by address.
+vrResult_t checkOuts(const Call& c) {
+  constexpr int kTypes = vrFloat64 - vrFloat16 + 1;
+  Run reads[kTypes], writes[kTypes];
+  bool apart = true;
+  for (int t = 0; t < c.nTensors; ++t) {
+    const size_t n = bytesOfTensor(c, t);
+    if (!n) continue;
+    const int k = c.types[t] - vrFloat16;
+    writes[k].add((uintptr_t)c.out[t], n);
+    if (c.out[t] != c.in[t]) reads[k].add((uintptr_t)c.in[t], n);
+  }
+  for (int k = 0; k < kTypes; ++k) {
+    apart = apart && (writes[k].up || writes[k].down);
+    for (int j = 0; j < kTypes; ++j)
+      apart = apart && writes[k].apartFrom(reads[j]) && (j >= k || writes[k].apartFrom(writes[j]));
+  }
+  if (apart) return vrSuccess;
+  struct Range {
+    uintptr_t lo, hi;
+    bool write;
+  };
+  std::unique_ptr<Range[]> all(new (std::nothrow) Range[2 * (size_t)c.nTensors]);
+  if (!all) return vrInternalError;
+  size_t m = 0;
+  for (int t = 0; t < c.nTensors; ++t) {
+    const size_t n = bytesOfTensor(c, t);
+    if (!n) continue;
+    const uintptr_t i = (uintptr_t)c.in[t], o = (uintptr_t)c.out[t];
+    all[m++] = {o, o + n, true};
+    if (i != o) all[m++] = {i, i + n, false};
+  }
+  std::sort(&all[0], &all[0] + m, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t written = 0, touched = 0;  // to there
+  for (size_t i = 0; i < m; ++i) {
+    if (all[i].lo < (all[i].write ? touched : written)) return vrInvalidArgument;
+    touched = all[i].hi > touched ? all[i].hi : touched;
+    if (all[i].write) written = all[i].hi > written ? all[i].hi : written;
+  }
+  return vrSuccess;
+}
+
 vrResult_t runChecked(const Call& c, const void* workspace, size_t workspaceBytes) {
-  if (!workspace || misaligned(workspace, 16) ||
-      workspaceBytes < slotsBound(c.nTensors) * sizeof(uint64_t))
-    return vrInvalidArgument;
+  const size_t need = slotsBound(c.nTensors) * sizeof(uint64_t);
+  if (!workspace || misaligned(workspace, 16) || workspaceBytes < need) return vrInvalidArgument;
+  const Bytes outs[] = {bytesOf(c.norm, 4), bytesOf(c.tensorNorms, (size_t)c.nTensors * 4),
+                        bytesOf(workspace, need)};
+  if (anyOverlap(outs, 3, nullptr, 0)) return vrInvalidArgument;
+  for (int t = 0; t < c.nTensors; ++t) {
+    const size_t n = bytesOfTensor(c, t);
+    const Bytes in = bytesOf(c.in[t], n), out = bytesOf(c.out ? c.out[t] : nullptr, n);
+    for (const Bytes& o : outs)
+      if (overlap(o, in) || overlap(o, out)) return vrInvalidArgument;
+  }
+  const vrResult_t r = c.out ? checkOuts(c) : vrSuccess;
+  if (r != vrSuccess) return r;
   if (isShort(c)) return runShort(c);
   return c.nTensors <= kShortList ? runLong<kShortList>(c) : runLong<kLongList>(c);
 }
@@ -778,8 +855,6 @@ extern "C" VR_API vrResult_t vrClipGradNorm(const void* const* grads, void* cons
   for (int t = 0; t < nTensors; ++t) {
     const size_t es = (size_t)elemSizeOf(dtypes[t]);
     if (counts[t] && (!outs[t] || misaligned(outs[t], es))) return vrInvalidArgument;
-    if (outs[t] != grads[t] && overlap(grads[t], counts[t] * es, outs[t], counts[t] * es))
-      return vrInvalidArgument;
   }
   const Call c = {grads, outs, counts, dtypes, nTensors, scale, maxNorm, norm, nullptr,
                   (uint64_t*)workspace, (cudaStream_t)stream};

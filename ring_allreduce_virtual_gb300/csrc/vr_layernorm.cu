@@ -852,11 +852,6 @@ uint64_t mostSplits(uint64_t rows, uint64_t cols) {
   return most;
 }
 
-// Bytes from a matrix's first element to the end of its last.
-size_t extent(uint64_t rows, uint64_t cols, uint64_t stride, int es) {
-  return rows ? ((rows - 1) * stride + cols) * es : 0;
-}
-
 bool badMatrix(const void* p, uint64_t cols, uint64_t stride, int es) {
   return !p || misaligned(p, es) || stride < cols;
 }
@@ -877,9 +872,11 @@ extern "C" VR_API vrResult_t vrLayerNormForward(const void* x, const void* weigh
   if (badMatrix(x, cols, xStride, es) || badMatrix(y, cols, yStride, es) ||
       misaligned(weight, ws) || misaligned(bias, ws) || misaligned(mean, 4) || misaligned(rstd, 4))
     return vrInvalidArgument;
-  if (!(x == y && xStride == yStride) &&
-      overlap(x, extent(rows, cols, xStride, es), y, extent(rows, cols, yStride, es)))
-    return vrInvalidArgument;
+  const bool inPlace = x == y && xStride == yStride;
+  const Bytes outs[] = {bytesOf(y, rows, cols, yStride, es), bytesOf(mean, rows * 4), bytesOf(rstd, rows * 4)};
+  const Bytes ins[] = {bytesOf(inPlace ? nullptr : x, rows, cols, xStride, es), bytesOf(weight, cols * ws),
+                       bytesOf(bias, cols * ws)};
+  if (anyOverlap(outs, 3, ins, 3)) return vrInvalidArgument;
   FwdArgs a = {x, weight, bias, y, mean, rstd, rows, cols, xStride, yStride, eps, {}};
   return dispatch(dtype, weightType, [&](auto t, auto w) {
     using T = decltype(t);
@@ -925,10 +922,6 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
       misaligned(weight, ws) || !mean || !rstd || misaligned(mean, 4) || misaligned(rstd, 4) ||
       (dx && badMatrix(dx, cols, dxStride, es)))
     return vrInvalidArgument;
-  const size_t out = extent(rows, cols, dxStride, es);
-  if (overlap(dx, out, dy, extent(rows, cols, dyStride, es)) ||
-      overlap(dx, out, x, extent(rows, cols, xStride, es)))
-    return vrInvalidArgument;
   const bool params = dweight || dbias;
   BwdArgs a = {dy, x, weight, mean, rstd, dx, dweight, dbias, rows, cols,
                dyStride, xStride, dxStride, (float*)workspace, splitsFor(rows, cols), false, {}};
@@ -936,6 +929,11 @@ extern "C" VR_API vrResult_t vrLayerNormBackward(
   if (params && (vrLayerNormBackwardWorkspace(rows, cols, dtype, &need) != vrSuccess ||
                  !workspace || misaligned(workspace, 16) || workspaceBytes < need))
     return vrInvalidArgument;
+  const Bytes outs[] = {bytesOf(dx, rows, cols, dxStride, es), bytesOf(dweight, cols * ws),
+                        bytesOf(dbias, cols * ws), bytesOf(workspace, need)};
+  const Bytes ins[] = {bytesOf(dy, rows, cols, dyStride, es), bytesOf(x, rows, cols, xStride, es),
+                       bytesOf(weight, cols * ws), bytesOf(mean, rows * 4), bytesOf(rstd, rows * 4)};
+  if (anyOverlap(outs, 4, ins, 5)) return vrInvalidArgument;
   return dispatch(dtype, weightType, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);

@@ -37,10 +37,39 @@ inline int elemSizeOf(vrDataType_t t) {
 
 inline bool misaligned(const void* p, size_t to) { return (uintptr_t)p % to != 0; }
 
-// [a, a + an) and [b, b + bn) share a byte.
-inline bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return a && b && an && bn && x < y + bn && y < x + an;
+// The bytes of an argument: rows of `width` bytes, `stride` apart.
+struct Bytes {
+  uintptr_t at;
+  uint64_t rows, width, stride;
+  uintptr_t end() const { return at + (rows - 1) * stride + width; }
+};
+inline Bytes bytesOf(const void* p, uint64_t width) {
+  return {(uintptr_t)p, p && width ? 1u : 0u, width, width};
+}
+inline Bytes bytesOf(const void* p, uint64_t rows, uint64_t cols, uint64_t stride, int es) {
+  return {(uintptr_t)p, p ? rows : 0u, cols * es, stride * es};
+}
+
+// Whether two arguments share a byte. Matrices of one stride may lie side by
+// side; of two strides they may not even interleave.
+inline bool overlap(const Bytes& a, const Bytes& b) {
+  if (!a.rows || !b.rows || a.at >= b.end() || b.at >= a.end()) return false;
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
+  const uint64_t s = a.rows > 1 ? a.stride : b.stride;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const uint64_t r = b.at >= a.at ? (b.at - a.at) % s : (s - (a.at - b.at) % s) % s;
+  return r < a.width || r + b.width > s;
+}
+
+// Whether one of the outputs shares a byte with an input or another output.
+inline bool anyOverlap(const Bytes* outs, int nOuts, const Bytes* ins, int nIns) {
+  for (int i = 0; i < nOuts; ++i) {
+    for (int j = 0; j < nIns; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+  }
+  return false;
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

@@ -115,6 +115,30 @@ def test_nothing_but_empty_tensors():
     assert training.clip_grad_norm(ts, 1.0).item() == 0.0
 
 
+@pytest.mark.parametrize("n", [40, 300])
+def test_lists_in_any_order_in_one_buffer(n):
+    # gradients and outputs in turn in one bucket; upwards, downwards, shuffled; some in place
+    bucket = torch.empty(2 * n * 1001, device="cuda")
+    parts = torch.split(bucket, 1001)
+    for seed, order in enumerate((list(range(2 * n)), list(range(2 * n))[::-1], None)):
+        g = torch.Generator("cuda").manual_seed(seed)
+        bucket.copy_(torch.randn(bucket.shape, generator=g, device="cuda"))
+        order = order or torch.randperm(2 * n, generator=torch.Generator().manual_seed(n)).tolist()
+        ins, outs = ([parts[i] for i in order[k::2]] for k in (0, 1))
+        outs = [i if k % 7 == 3 else o for k, (i, o) in enumerate(zip(ins, outs))]
+        start = [t.clone() for t in ins]
+        others = bucket.clone()
+        norm = training.clip_grad_norm(ins, 1.0, outs=outs)
+        assert abs(norm.item() - norms64(start)[0]) <= 40 * U * norm.item()
+        for k, (i, o, s) in enumerate(zip(ins, outs, start)):
+            w = s.double() / norm.item()
+            assert ((o.double() - w).abs() <= 48 * U * w.abs()).all()
+            assert o is i or torch.equal(i, s)
+        for k in range(3, n, 7):  # outputs that were not asked for
+            at = order[2 * k + 1] * 1001
+            assert torch.equal(bucket[at: at + 1001], others[at: at + 1001])
+
+
 def test_zero_gradients_and_zero_bound():
     ts = [torch.zeros(70000, device="cuda"), torch.zeros(33, dtype=torch.bfloat16, device="cuda")]
     check_norm(ts)

@@ -160,6 +160,20 @@ def test_strides_alignments_and_guards(rows, cols, dtype, pad, shift):
     assert untouched(dbase, dxv) and untouched(dwbase, dwv) and untouched(dbbase, dbv)
 
 
+@pytest.mark.parametrize("cols", [8, 333, 1024])
+def test_matrices_side_by_side_in_one_buffer(cols):
+    x, w, b, dy = inputs(cols, 31, cols, torch.float32, torch.float32)
+    buf = torch.full((31, 4 * cols + 9), 7.0, device="cuda")
+    xv, yv, dyv, dxv = (buf[:, i * cols:(i + 1) * cols] for i in range(4))
+    xv.copy_(x)
+    dyv.copy_(dy)
+    _, mean, rstd = training.layer_norm_forward(xv, w, b, EPS, out=yv)
+    check_forward(x, w, b, yv, mean, rstd)
+    _, dw, db = training.layer_norm_backward(dyv, xv, mean, rstd, w, dxv)
+    check_backward(dy, x, mean, rstd, w, dxv, dw, db)
+    assert torch.equal(xv, x) and torch.equal(dyv, dy) and (buf[:, 4 * cols:] == 7.0).all()
+
+
 @pytest.mark.parametrize("cols", [5, 512, 1001, 4096, 20000])
 @pytest.mark.parametrize("has_w,has_b", [(False, False), (True, False), (False, True)])
 def test_without_weight_or_bias(cols, has_w, has_b):

@@ -2,6 +2,7 @@
 every refusal is vrInvalidArgument from the library or ValueError from the
 torch layer."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -63,6 +64,29 @@ def test_layer_norm_backward_refuses(vr, bad):
     refused(vr, vr.vrLayerNormBackward, *{**BWD, **bad}.values())
 
 
+@pytest.mark.parametrize("bad", [
+    {"y": 2 * A}, {"y": 3 * A + 16}, {"y": 4 * A}, {"y": 5 * A - 16},  # y over the parameters or the statistics
+    {"mean": A}, {"mean": 2 * A + 28}, {"rstd": 3 * A}, {"rstd": FAR + 28}, {"mean": 5 * A + 4},
+    {"y": A + 6, "cols": 4},  # side by side, but a byte too near
+    {"y": A + 6, "xStride": 16, "yStride": 16}, {"y": A + 18, "xStride": 16, "yStride": 16},
+    {"y": A + 16, "xStride": 16, "yStride": 24},  # strides that differ may not interleave
+    {"mean": A + 12, "xStride": 16}, {"mean": A + 28, "xStride": 16},
+])
+def test_layer_norm_forward_refuses_overlaps(vr, bad):
+    refused(vr, vr.vrLayerNormForward, *{**FWD, **bad}.values())
+
+
+@pytest.mark.parametrize("bad", [
+    {"dx": 3 * A}, {"dx": 4 * A}, {"dx": 5 * A}, {"dx": 6 * A}, {"dx": 7 * A + 14}, {"dx": 8 * A + 32},
+    {"dweight": 7 * A}, {"dbias": 6 * A + 14}, {"dweight": A}, {"dbias": 2 * A}, {"dweight": 3 * A},
+    {"dbias": 3 * A + 14}, {"dweight": 4 * A}, {"dbias": 5 * A + 4}, {"workspace": A}, {"workspace": 3 * A},
+    {"workspace": 6 * A}, {"workspace": 7 * A}, {"workspace": 4 * A}, {"workspace": 5 * A},
+    {"workspace": FAR}, {"workspace": 2 * A - 16},
+])
+def test_layer_norm_backward_refuses_overlaps(vr, bad):
+    refused(vr, vr.vrLayerNormBackward, *{**BWD, **bad}.values())
+
+
 def test_layer_norm_workspace(vr):
     assert vr.vrLayerNormBackwardWorkspace(2, 8, "float16") >= 64
     assert vr.vrLayerNormBackwardWorkspace(0, 8, "float32") >= 0
@@ -95,6 +119,54 @@ def test_clip_refuses(vr, outs, scale, most):
     arrays = norm_args(vr)[0]
     refused(vr, vr.vrClipGradNorm, arrays, (ctypes.c_void_p * 2)(*outs), scale, most, 4 * A, 6 * A,
             1 << 20)
+
+
+@pytest.mark.parametrize("bad", [{"norm": A}, {"norm": 2 * A + 12}, {"norms": A + 28}, {"norms": 4 * A - 4},
+                                 {"ws": A}, {"ws": 4 * A}, {"ws": 5 * A - 16}, {"ws": A - 4096}])
+def test_grad_norm_refuses_overlaps(vr, bad):
+    refused(vr, vr.vrGradNorm, *norm_args(vr, **bad))
+
+
+B = 4096  # bytes of a tensor of these lists, and their distance
+LISTS = {
+    "the same tensor twice": ([A, A + B, A], None),
+    "parts of each other": ([A, A + B, A + B + 64], None),
+    "swapped": ([A, A + B, A + 2 * B], [A + B, A, FAR]),
+    "shifted by one tensor": ([A, A + B, A + 2 * B], [A + B, A + 2 * B, A + 3 * B]),
+    "shifted by less": ([A, A + B, A + 2 * B], [A + 64, A + B + 64, A + 2 * B + 64]),
+    "one output twice": ([A, A + B, A + 2 * B], [FAR, FAR + B, FAR]),
+    "outputs over each other": ([A, A + B, A + 2 * B], [FAR, FAR + B - 64, FAR + 4 * B]),
+    "one in place, over another's": ([A, A + B, A + B + 128], [FAR, A + B, FAR + B]),
+}
+
+
+def clip_args(vr, ins, outs, types, n=B // 4, **kw):
+    k = {"norm": FAR - A, "ws": FAR + A, "nbytes": 1 << 20, **kw}
+    arrays = vr.tensor_arrays(ins, [n if t == "float32" else 2 * n for t in types], types)
+    return arrays, (ctypes.c_void_p * len(ins))(*(outs or ins)), 1.0, 1.0, k["norm"], k["ws"], k["nbytes"]
+
+
+@pytest.mark.parametrize("types", [["float32"] * 3, ["float32", "bfloat16", "float16"]], ids=["one", "mixed"])
+@pytest.mark.parametrize("name", LISTS)
+def test_clip_refuses_overlaps(vr, name, types):
+    refused(vr, vr.vrClipGradNorm, *clip_args(vr, *LISTS[name], types))
+
+
+@pytest.mark.parametrize("bad", [{"norm": A + B}, {"ws": A + 2 * B - 16}, {"norm": FAR + A}, {"ws": FAR}])
+def test_clip_refuses_norms_and_workspaces_over_tensors(vr, bad):
+    refused(vr, vr.vrClipGradNorm, *clip_args(vr, [A, A + B], [FAR, FAR + B], ["float32"] * 2, **bad))
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_clip_finds_one_overlap_in_a_long_list(vr, seed):
+    rng = random.Random(seed)
+    n = rng.choice([5, 100, 3000])
+    places = [A + 2 * i * B for i in range(2 * n)]
+    rng.shuffle(places)
+    ins, outs = places[:n], places[n:]
+    i, j = rng.sample(range(n), 2)
+    bad = rng.choice([ins, outs])[j] + rng.choice([0, 16, B - 16, 16 - B])
+    refused(vr, vr.vrClipGradNorm, *clip_args(vr, ins, [*outs[:i], bad, *outs[i + 1:]], ["float32"] * n, nbytes=1 << 22))
 
 
 def test_bindings_check_the_lengths_of_lists(vr):
