@@ -436,19 +436,25 @@ __global__ void __launch_bounds__(Block::threads)
 // came from.
 struct Factor {
   float norm, f;
+  float after = 1.f;  // the factor is f times this power of two
   bool clips;
   __device__ Factor(const Total& s, float scale, float maxNorm) {
     norm = s.norm(scale);
     clips = norm > maxNorm;
-    f = scale;
-    if (norm >= 0x1p-100f && norm <= 0x1p120f) {
-      if (clips) f *= maxNorm / norm;
-    } else {  // rare: in 64 bits
+    const float ratio = clips ? maxNorm / norm : 1.f;
+    f = scale * ratio;
+    // Rare: in 64 bits, also where the factor or its ratio is near the smallest normal
+    // float, below which bits are lost.
+    if (!(norm >= 0x1p-100f && norm <= 0x1p120f) ||
+        (clips && maxNorm > 0.f && !(ratio >= 0x1p-100f && fabsf(f) >= 0x1p-100f))) {
       const double n = s.wideNorm(scale);
       clips = n > (double)maxNorm && isfinite(n);
-      if (clips) f = (float)((double)scale * ((double)maxNorm / n));
+      const double d = clips ? (double)scale * ((double)maxNorm / n) : (double)scale;
+      after = clips && fabs(d) < 0x1p-100 ? 0x1p-64f : 1.f;
+      f = (float)(d / (double)after);
     }
   }
+  __device__ __forceinline__ float operator()(float x) const { return x * f * after; }
   // For elements of 64 bits.
   __device__ static double of(const Total& s, float scale, float maxNorm, bool clips) {
     return clips ? (double)scale * ((double)maxNorm / s.wideNorm(scale)) : (double)scale;
@@ -459,13 +465,13 @@ struct Factor {
 // 16 bytes, elements elsewhere. Each product is rounded once. `loaded`: `v` holds
 // the packs of a whole tile.
 template <typename S, typename T, typename F>
-__device__ __forceinline__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F factor,
+__device__ __forceinline__ void scaleTile(const T* g, T* out, uint64_t count, uint32_t k, F by,
                                           bool loaded, const uint4 (&v)[S::packs]) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr uint64_t E = S::tileBytes / sizeof(T);
-  auto mul = [factor](T x) -> T {
-    if constexpr (sizeof(T) == 8) return x * factor;
-    else return from_f32<T>(to_f32(x) * factor);
+  auto mul = [by](T x) -> T {
+    if constexpr (sizeof(T) == 8) return x * by;
+    else return from_f32<T>(by(to_f32(x)));
   };
   auto mulPack = [&](uint4 v) {
     T e[V];
@@ -524,10 +530,10 @@ __device__ __forceinline__ void scale(const A& a, const Tile<S>& at, const Facto
   void* o = a.out[at.t];
   const uint64_t n = a.count[at.t];
   switch (a.type[at.t]) {
-    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, at.k, by.f, at.whole, at.v);
+    case vrFloat16: return scaleTile<S>((const __half*)g, (__half*)o, n, at.k, by, at.whole, at.v);
     case vrBfloat16:
-      return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, at.k, by.f, at.whole, at.v);
-    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, at.k, by.f, at.whole, at.v);
+      return scaleTile<S>((const __nv_bfloat16*)g, (__nv_bfloat16*)o, n, at.k, by, at.whole, at.v);
+    case vrFloat32: return scaleTile<S>((const float*)g, (float*)o, n, at.k, by, at.whole, at.v);
     default:
       return scaleTile<S>((const double*)g, (double*)o, n, at.k,
                           Factor::of(s, a.scale, a.maxNorm, by.clips), at.whole, at.v);

@@ -172,6 +172,28 @@ def test_sizes_whose_squares_leave_32_bits(dtype, size):
         assert ((o.double() - w).abs() <= far * 1.01).all()
 
 
+@pytest.mark.parametrize("dtype,size,most,scale", [
+    (torch.float32, 1e30, 1e-9, 1.0),    # maxNorm / norm is below the normal floats
+    (torch.float32, 3e38, 1e-3, 1.0),    # and the norm above all floats
+    (torch.bfloat16, 1e38, 1e-5, 0.125),
+    (torch.float32, 1.0, 1e-12, 1e30),   # the ratio alone is
+    (torch.float32, 1e38, 1e-2, 1e-30),  # the factor alone is
+])
+@pytest.mark.parametrize("n", [100, 3_000_000])
+def test_factors_below_the_normal_floats_keep_their_bits(dtype, size, most, scale, n):
+    ts = [t * size for t in tensors(n, [n, 7], [dtype], std=1.0)]
+    ts = [t.clamp(-3e38, 3e38) for t in ts]
+    want = norms64(ts)[0] * scale
+    outs = [torch.empty_like(t) for t in ts]
+    training.clip_grad_norm(ts, most, scale=scale, outs=outs)
+    # the factor as in check_clip; the bound itself may be rounded
+    for t, o in zip(ts, outs):
+        w = t.double() * (scale * (most / want))
+        far = 46 * U * w.abs()
+        far = far + UT[dtype] * (w.abs() + far) + TINY[dtype]
+        assert ((o.double() - w).abs() <= far).all()
+
+
 def test_mixed_sizes_and_large_values_among_small_ones():
     ts = [torch.full((9000,), 1e-25, device="cuda"), torch.full((100,), 1e25, device="cuda"),
           torch.full((50000,), 1.0, device="cuda", dtype=torch.bfloat16)]
