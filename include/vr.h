@@ -422,9 +422,11 @@ VR_API vrResult_t vrGradNorm(const void* const* grads, const size_t* counts,
 
 /* Clipping by the norm of the list: with norm as above,
  *   outs[t] = grads[t] * (scale * (norm > maxNorm ? maxNorm / norm : 1)),
- * in the type of grads[t], each product rounded once. If the norm is infinite
- * or NaN nothing is clipped (the factor is `scale`): read `norm` and drop the
- * step.
+ * in the type of grads[t], each product rounded once. The norm that decides and
+ * divides is that of a double: one past the largest float (float32 elements of
+ * 1e38, float64 of 1e100) still clips, while *norm, a float, is infinite. If it
+ * is infinite or NaN in 64 bits as well (an element is) nothing is clipped, the
+ * factor is `scale`. Read `norm` and drop the step where it is not finite.
  *  outs     [host array of nTensors device pointers]; outs[t] == grads[t] is
  *           allowed, other overlaps are not: neither with another gradient nor
  *           between two outputs (a tensor listed twice, in place).

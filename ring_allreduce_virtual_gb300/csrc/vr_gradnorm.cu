@@ -431,9 +431,10 @@ __global__ void __launch_bounds__(Block::threads)
   if ((threadIdx.x & 31) == 0) a.tensorNorms[a.tensorBase + t] = s.norm(a.scale);
 }
 
-// What the gradients are multiplied by. A norm that is not finite clips nothing:
-// the caller sees it and drops the step, and the gradients still show where it
-// came from.
+// What the gradients are multiplied by. A norm that is not finite in 64 bits (an
+// element is not) clips nothing: the caller sees it and drops the step, and the
+// gradients still show where it came from. One that is too large for a float alone
+// is reported as infinite and clips like any other.
 struct Factor {
   float norm, f;
   float after = 1.f;  // the factor is f times this power of two

@@ -298,8 +298,9 @@ def clip_grad_norm(grads, max_norm, scale=1.0, outs=None, stream=None):
     """Multiply `grads` (a TensorList or a sequence of tensors) by `scale` and,
     where the norm of the result exceeds max_norm, by max_norm over that norm; in
     place, or into `outs`, as many tensors of the same sizes and types. Returns
-    that norm, a float32 scalar tensor. If it is not finite, only `scale` is
-    applied."""
+    that norm, a float32 scalar tensor. If an element is infinite or NaN, so is
+    the norm, and only `scale` is applied; a norm that leaves the range of
+    float32 alone is returned as infinity and clipped by in 64 bits."""
     grads = _list(grads)
     if stream is not None:
         return _on(stream, grads.index, clip_grad_norm, grads, max_norm, scale, outs)

@@ -194,6 +194,25 @@ def test_factors_below_the_normal_floats_keep_their_bits(dtype, size, most, scal
         assert ((o.double() - w).abs() <= far).all()
 
 
+@pytest.mark.parametrize("dtype,size", [(torch.float32, 1e38), (torch.bfloat16, 1e38), (torch.float64, 1e150)])
+@pytest.mark.parametrize("n", [100, 3_000_000])
+def test_norms_past_the_largest_float_clip_and_infinities_do_not(dtype, size, n):
+    # short and long lists; a scale that brings the norm back makes it finite
+    ts = [torch.full((n,), size, dtype=dtype, device="cuda"), torch.full((7,), -size, dtype=dtype, device="cuda")]
+    want = norms64(ts)[0]
+    outs = [torch.empty_like(t) for t in ts]
+    assert training.clip_grad_norm(ts, 2.0, outs=outs).item() == math.inf
+    for t, o in zip(ts, outs):
+        w = t.double() * (2.0 / want)
+        assert ((o.double() - w).abs() <= (44 * U + UT[dtype]) * w.abs() * 1.01).all()
+    if dtype != torch.float64:
+        norm = training.clip_grad_norm(ts, 2.0, scale=2.0 ** -20, outs=outs).item()
+        assert abs(norm - want * 2.0 ** -20) <= 40 * U * norm
+    ts[1][3] = math.inf
+    assert training.clip_grad_norm(ts, 2.0, scale=0.5, outs=outs).item() == math.inf
+    assert all(torch.equal(o, t * 0.5) for t, o in zip(ts, outs))
+
+
 def test_mixed_sizes_and_large_values_among_small_ones():
     ts = [torch.full((9000,), 1e-25, device="cuda"), torch.full((100,), 1e25, device="cuda"),
           torch.full((50000,), 1.0, device="cuda", dtype=torch.bfloat16)]
