@@ -15,11 +15,14 @@ Calls are asynchronous on the current torch stream of the tensors' device (which
 need not be the current device), or on `stream` of that device; outputs and
 workspaces are allocated there, so that they may be freed at any time. As with
 any torch operation, tensors that were made or are freed on another stream
-need the caller's own ordering (wait_stream, record_stream).
+need the caller's own ordering (wait_stream, record_stream). Tensors that are
+given to be written (out, dx, dweight, dbias, outs, gradients clipped in place)
+count as changed in place: autograd refuses a backward pass that saved them.
 """
 import functools
 
 import torch
+from torch.autograd.graph import increment_version as _written
 
 import ring_allreduce_virtual_gb300 as vr
 
@@ -146,6 +149,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, stats=True, out=None
                                      _raw_stream(device))
     if rc:
         raise vr.VrError(rc, "vrLayerNormForward")
+    if out is not None:
+        _written(out)
     return y, mean, rstd
 
 
@@ -168,6 +173,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
     if device != _current_device():
         return _on_device(device, layer_norm_backward, dy, x, mean, rstd, weight, dx, dweight,
                           dbias)
+    given = [t for t in (dx, dweight, dbias) if isinstance(t, torch.Tensor)]
     rows, xs = _rows(x, "x")
     _check_like(dy, x, device, "dy")
     dys = _rows(dy, "dy")[1]
@@ -211,6 +217,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
                                       _raw_stream(device))
     if rc:
         raise vr.VrError(rc, "vrLayerNormBackward")
+    if given:
+        _written(given)
     return dx, dw, db
 
 
@@ -268,6 +276,12 @@ class TensorList:
     def __len__(self):
         return len(self.tensors)
 
+    @functools.cached_property
+    def bases(self):
+        """What the tensors are views of, each once: views share its version."""
+        each = (t if t._base is None else t._base for t in self.tensors)
+        return list({id(t): t for t in each}.values())
+
 
 def _list(tensors):
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
@@ -301,12 +315,13 @@ def clip_grad_norm(grads, max_norm, scale=1.0, outs=None, stream=None):
     that norm, a float32 scalar tensor. If an element is infinite or NaN, so is
     the norm, and only `scale` is applied; a norm that leaves the range of
     float32 alone is returned as infinity and clipped by in 64 bits."""
-    grads = _list(grads)
+    given, grads = grads, _list(grads)
     if stream is not None:
         return _on(stream, grads.index, clip_grad_norm, grads, max_norm, scale, outs)
     if grads.index != _current_device():
         return _on_device(grads.index, clip_grad_norm, grads, max_norm, scale, outs)
     to = grads if outs is None else _list(outs)
+    kept = to is outs or to is given
     device, nbytes = grads.device, grads.workspace_bytes
     if to is not grads and (to.device != device or to.shape != grads.shape):
         raise ValueError("outs must match grads in number, sizes, types and device")
@@ -317,4 +332,5 @@ def clip_grad_norm(grads, max_norm, scale=1.0, outs=None, stream=None):
                                  norm.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(grads.index))
     if rc:
         raise vr.VrError(rc, "vrClipGradNorm")
+    _written(to.bases if kept else to.tensors)
     return norm

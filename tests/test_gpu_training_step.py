@@ -6,6 +6,8 @@ import os
 import pytest
 import torch
 
+from ring_allreduce_virtual_gb300 import training
+
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -16,6 +18,46 @@ def example():
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     return m
+
+
+def test_tensors_that_are_written_count_as_changed():
+    x = torch.randn(4, 64, device="cuda")
+    y, dx, bucket = torch.zeros_like(x), torch.zeros_like(x), torch.zeros(128, device="cuda")
+
+    def changes(t, f, *args, **kw):
+        v = t._version
+        r = f(*args, **kw)
+        assert t._version > v
+        return r
+
+    _, mean, rstd = changes(y, training.layer_norm_forward, x, out=y)
+    changes(dx, training.layer_norm_backward, x, x, mean, rstd, None, dx, False, False)
+    changes(bucket, training.layer_norm_backward, x, x, mean, rstd, None, False, bucket[:64], bucket[64:])
+    for parts in (torch.split(bucket, 50), [x]):
+        for grads in (parts, training.TensorList(parts)):
+            changes(parts[0], training.clip_grad_norm, grads, 1.0)
+            changes(parts[0], training.clip_grad_norm, [t.clone() for t in parts], 1.0, outs=grads)
+            kept = [t.clone() for t in parts]
+            outs = training.TensorList(kept)
+            for _ in range(2):
+                changes(kept[-1], training.clip_grad_norm, grads, 1.0, outs=outs)
+    v = x._version
+    training.grad_norm([x])
+    training.layer_norm_backward(x, x, mean, rstd)
+    assert x._version == v
+
+
+@pytest.mark.parametrize("write", [
+    lambda h: training.layer_norm_forward(h.detach(), out=h.detach()),
+    lambda h: training.clip_grad_norm([h.detach()], 0.1),
+])
+def test_autograd_refuses_saved_tensors_that_were_written(write):
+    w = torch.rand(8, 8, device="cuda", requires_grad=True)
+    h = torch.rand(4, 8, device="cuda")
+    y = (h @ w).sum()  # saves h
+    write(h)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
 
 
 def test_ranks_stay_equal_and_learn():
