@@ -80,6 +80,17 @@ def _rows(t, what):
     return rows, stride
 
 
+def _has_rows(t):
+    """Whether _rows takes t as it is."""
+    if t.is_contiguous():
+        return True
+    try:
+        _rows(t, "t")
+    except ValueError:
+        return False
+    return True
+
+
 def _bad_x(x):
     if x.dtype not in _NORM_CODE:
         raise ValueError(f"unsupported dtype {x.dtype}")
@@ -121,7 +132,9 @@ def _ptr(t):
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, stats=True, out=None, stream=None):
     """(y, mean, rstd): layer norm over x's last axis; mean and rstd (float32,
     x's leading shape) are what the backward pass needs, None with
-    stats=False. `out`: a tensor of x's shape and type for y, x itself allowed."""
+    stats=False. `out`: a tensor of x's shape and type for y, x itself allowed.
+    Tensors of x's shape, here and in the backward pass, have a dense last axis
+    and leading axes that are one row stride apart."""
     if stream is not None:
         return _on(stream, x.get_device(), layer_norm_forward, x, weight, bias, eps, stats, out)
     cols, code, device = _check_x(x)
@@ -225,6 +238,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=True, dweight=True, d
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
+        if x.dim() and x.shape[-1] and not _has_rows(x):
+            x = x.contiguous()
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps, any(ctx.needs_input_grad))
         ctx.save_for_backward(x, mean, rstd, weight)
         ctx.bias_type = None if bias is None else bias.dtype
@@ -245,7 +260,9 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """Layer norm over x's last axis, differentiable once with respect to x,
-    weight and bias; x's last axis is dense."""
+    weight and bias. An x whose last axis is not dense, or whose leading axes are
+    not one row stride apart (x[:, 1:] of three axes, an expanded one), is copied
+    first."""
     return _LayerNorm.apply(x, weight, bias, eps)
 
 

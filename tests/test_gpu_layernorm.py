@@ -279,6 +279,18 @@ def test_autograd_takes_only_what_is_needed_and_expanded_gradients():
         assert not training.layer_norm(x, w).requires_grad
 
 
+def test_differentiable_call_takes_any_layout():
+    x = torch.randn(3, 5, 48, device="cuda", requires_grad=True)
+    for view in (x[:, 1:], x.transpose(1, 2), x[:, :, ::2], x[:1].expand(4, 5, 48), x[:, 0]):
+        w = torch.rand(view.shape[-1], device="cuda", requires_grad=True)
+        dy = torch.randn(view.shape, device="cuda")
+        for got, want in zip(*(torch.autograd.grad(training.layer_norm(v, w), (x, w), dy)
+                               for v in (view, view.contiguous()))):
+            assert torch.equal(got, want)
+    with pytest.raises(ValueError):
+        training.layer_norm_forward(x[:, 1:])
+
+
 def test_other_stream_and_graph():
     x, w, b, dy = inputs(1, 700, 4096, torch.bfloat16, torch.float32)
     want = training.layer_norm_forward(x, w, b, EPS)
