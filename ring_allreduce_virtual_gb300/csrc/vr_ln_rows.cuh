@@ -150,6 +150,8 @@ __device__ __forceinline__ void copies_wait() {
 
 // The parameters of a thread's V columns from c0 on: packed as they are where
 // they have the rows' type, else as floats. `none` where the pointer is NULL.
+// Plain loads: the read-only path asks that nobody writes the parameters from the
+// kernel's launch on, and the stream's previous kernel may still be writing them then.
 template <typename T, typename W>
 struct Params {
   static constexpr int V = kV<T>;
@@ -160,7 +162,7 @@ struct Params {
     if (p && used && ((uintptr_t)(p + c0) & 15) == 0) {
 #pragma unroll
       for (int i = 0; i < (int)(V * sizeof(W) / 16); ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + c0) + i);
+        const uint4 q = reinterpret_cast<const uint4*>(p + c0)[i];
         memcpy(reinterpret_cast<char*>(e) + 16 * i, &q, 16);
       }
     } else {

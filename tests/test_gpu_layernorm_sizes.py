@@ -63,6 +63,33 @@ def test_small_calls_write_nothing_but_their_outputs(rows, cols):
     assert torch.equal(only, dw)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=lambda t: str(t)[6:])
+def test_parameters_that_the_call_before_wrote(dtype):
+    # the kernel that reads them starts while the one that writes them runs
+    g = torch.Generator("cuda").manual_seed(4)
+    x, rows = (torch.randn(n, 4096, device="cuda", generator=g).to(dtype) for n in (300, 40))
+    w, b = torch.zeros(4096, device="cuda", dtype=dtype), torch.zeros(4096, device="cuda", dtype=dtype)
+
+    def chain(wait):
+        out = []
+        for row in torch.split(rows, 1):
+            training.layer_norm_forward(row, out=w[None])
+            wait()
+            training.layer_norm_forward(row * 2, w, out=b[None])
+            wait()
+            out.append(training.layer_norm_forward(x, w, b)[0])
+            wait()
+            _, mean, rstd = training.layer_norm_forward(x)
+            wait()
+            training.layer_norm_backward(x, x, mean, rstd, None, False, w, b)
+            wait()
+            out.append(training.layer_norm_forward(x, w, b)[0])
+            wait()
+        return out
+
+    assert all(torch.equal(p, q) for p, q in zip(chain(lambda: None), chain(torch.cuda.synchronize)))
+
+
 def test_chains_of_calls_see_each_other():
     # every call starts while the last one ends; what it reads has to be there
     x = torch.randn(512, 4096, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
