@@ -277,17 +277,19 @@ struct Place {
   int packs;     // whole packs
   int pack0;     // the thread's first
   int edge;      // this thread's element outside the packs, -1: none
-  __device__ __forceinline__ Place(const Layout& l, uint64_t rows, int cols) {
+  // Of thread `thread` of block `block`, `rank` in its cluster.
+  __host__ __device__ __forceinline__ Place(const Layout& l, uint64_t rows, int cols, uint32_t block,
+                                            uint32_t thread, uint32_t rank) {
     uint64_t first;
     if constexpr (MODE == IN_CLUSTER) {
       group = 0;
-      lane = (int)(cluster_rank() * l.tpr + threadIdx.x);
-      row = first = blockIdx.x / l.ctas;
+      lane = (int)(rank * l.tpr + thread);
+      row = first = block / l.ctas;
     } else {
-      group = threadIdx.x / l.tpr;
-      lane = threadIdx.x - group * l.tpr;
-      row = (uint64_t)blockIdx.x * l.groups + group;
-      first = MODE == IN_WARP ? (uint64_t)blockIdx.x * l.groups + (threadIdx.x & ~31) / l.tpr : row;
+      group = thread / l.tpr;
+      lane = thread - group * l.tpr;
+      row = (uint64_t)block * l.groups + group;
+      first = MODE == IN_WARP ? (uint64_t)block * l.groups + (thread & ~31) / l.tpr : row;
     }
     // fewer than kMostRows rows: 32-bit divisions
     n = row < rows ? (int)(((uint32_t)(rows - row) + l.step - 1) / l.step) : 0;
@@ -301,11 +303,13 @@ struct Place {
     edge = lane < head ? lane : lane + packs * V;
     edge = edge < cols ? edge : -1;
   }
-  __device__ __forceinline__ int pack(int i) const {
+  __device__ __forceinline__ Place(const Layout& l, uint64_t rows, int cols)
+      : Place(l, rows, cols, blockIdx.x, threadIdx.x, MODE == IN_CLUSTER ? cluster_rank() : 0) {}
+  __host__ __device__ __forceinline__ int pack(int i) const {
     return pack0 + i * (MODE == IN_WARP ? stripe : 32);
   }
-  __device__ __forceinline__ int column(int i) const { return head + pack(i) * V; }
-  __device__ __forceinline__ bool used(int i) const { return pack(i) < packs; }
+  __host__ __device__ __forceinline__ int column(int i) const { return head + pack(i) * V; }
+  __host__ __device__ __forceinline__ bool used(int i) const { return pack(i) < packs; }
 };
 
 // ------------------------------------------------------------------ host
