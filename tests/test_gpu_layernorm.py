@@ -160,6 +160,29 @@ def test_strides_alignments_and_guards(rows, cols, dtype, pad, shift):
     assert untouched(dbase, dxv) and untouched(dwbase, dwv) and untouched(dbbase, dbv)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("rows,cols", [(3, 8), (37, 264), (33, 1001), (700, 1001), (130, 2051), (9, 4096),
+                                       (150, 9000), (75, 20001)])
+@pytest.mark.parametrize("pad,shift", [(8, 0), (16, 8), (3, 0), (0, 1), (5, 3), (1, 7)])
+def test_padded_and_shifted_rows_that_lie_alike(rows, cols, dtype, pad, shift):
+    # dy, x and dx start alike and their strides differ by whole packs: the rows
+    # stay on chip, with ends before and after the packs
+    x, w, _, dy = inputs(cols + pad, rows, cols, dtype, dtype)
+    _, mean, rstd = training.layer_norm_forward(x, w, None, EPS)
+    ybase, yv = matrix(0, rows, cols, dtype, pad + 8, shift)
+    _, xv = matrix(0, rows, cols, dtype, pad, shift, x)
+    y, mean, rstd = training.layer_norm_forward(xv, w, None, EPS, out=yv)
+    check_forward(x, w, None, y, mean, rstd)
+    assert untouched(ybase, yv)
+    _, dyv = matrix(0, rows, cols, dtype, pad + 16, shift, dy)
+    dbase, dxv = matrix(0, rows, cols, dtype, pad + 8, shift)
+    dwbase, dwv = matrix(0, 1, cols, dtype, 0, shift)
+    dbbase, dbv = matrix(0, 1, cols, dtype, 0, 3)
+    dx, dw, db = training.layer_norm_backward(dyv, xv, mean, rstd, w, dxv, dwv[0], dbv[0])
+    check_backward(dy, x, mean, rstd, w, dx, dw, db)
+    assert untouched(dbase, dxv) and untouched(dwbase, dwv) and untouched(dbbase, dbv)
+
+
 @pytest.mark.parametrize("cols", [8, 333, 1024])
 def test_matrices_side_by_side_in_one_buffer(cols):
     x, w, b, dy = inputs(cols, 31, cols, torch.float32, torch.float32)
@@ -335,6 +358,28 @@ def test_offsets_past_32_bits():
         assert torch.equal(p, q)
     training.layer_norm_forward(far, w, b, EPS, out=far)
     assert torch.equal(far, want[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("rows", [1, 130, 3001, 70001])
+@pytest.mark.parametrize("cols", [3, 64, 72, 264, 640, 1001, 1024, 2051])
+@pytest.mark.parametrize("dx", [False, True])
+def test_column_sums_of_whole_numbers_are_exact(rows, cols, dtype, dx):
+    # |dy u| <= 36 and 70001 rows: every partial sum is a whole number below 2^24, so
+    # a row left out or taken twice shows
+    g = torch.Generator("cuda").manual_seed(rows + cols)
+    x, dy = (torch.randint(-6, 7, (rows, cols), generator=g, device="cuda").to(dtype) for _ in range(2))
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dw, db = torch.empty(2, cols, device="cuda").unbind()
+    training.layer_norm_backward(dy, x, mean, rstd, None, dx, dw, db)
+    assert torch.equal(dw.double(), (dy.double() * x.double()).sum(0))
+    assert torch.equal(db.double(), dy.double().sum(0))
+
+
+@pytest.mark.parametrize("cols", [4096, 8192, 9000, 20000, 20001])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=lambda t: str(t)[6:])
+def test_column_sums_of_wide_rows_are_exact(cols, dtype):
+    test_column_sums_of_whole_numbers_are_exact(3001, cols, dtype, True)
 
 
 def test_many_rows():
