@@ -351,7 +351,10 @@ VR_API vrResult_t vrRedOpDestroy(vrRedOp_t op, vrComm_t comm);
  * Common errors: vrInvalidArgument for a NULL or misaligned pointer (to the
  * element size; workspaces to 16 bytes), a type, size or stride outside what
  * is stated, a short workspace, or buffers that overlap where that is not
- * allowed; vrCudaError if a launch fails. Nothing is enqueued then. */
+ * allowed: nothing is enqueued then. vrCudaError if a launch fails: of a call that
+ * takes several launches (backward passes, long lists) the earlier ones are
+ * enqueued and their outputs are written. vrInternalError if the host has no
+ * memory left to check a list. */
 
 /* Layer norm over the last axis: for each row of `cols` elements
  *   m = sum(x) / cols,  v = sum((x - m)^2) / cols,  r = 1 / sqrt(v + eps),

@@ -17,8 +17,9 @@
 
 namespace vrop {
 
-// Grids are sized for the 152 SMs of the one GPU this library is written for,
-// so that the order of every sum is the same wherever it runs.
+// Grids are sized for the 152 SMs of the one GPU this library is written for, not
+// asked of the device, so that sums have the same order wherever it runs -- but for
+// dw and db of rows over clusters, whose number the driver says (clustersAtOnce).
 constexpr int kSMs = 152;
 
 struct NvtxRange {

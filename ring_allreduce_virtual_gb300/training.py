@@ -269,9 +269,13 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
 # ------------------------------------------------- gradient norm, clipping
 class TensorList:
     """A list of gradients (or outputs) whose addresses have been checked and
-    marshalled once; it keeps the tensors alive. Make it for buffers that stay
-    where they are from step to step; a plain sequence of tensors works wherever
-    a TensorList does and is marshalled for the call."""
+    marshalled once, about 0.75 us a tensor; it keeps the tensors alive. Make it
+    for buffers that stay where they are from step to step. It does not follow
+    tensors that are replaced or moved: after zero_grad(set_to_none=True), which
+    gives every parameter a new gradient, it still names the old ones, and a
+    tensor given other memory (.data, resize_, set_) needs a new list. A plain
+    sequence of tensors works wherever a TensorList does and is marshalled for
+    the call."""
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
