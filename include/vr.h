@@ -336,7 +336,9 @@ VR_API vrResult_t vrRedOpDestroy(vrRedOp_t op, vrComm_t comm);
 
 /* ---- The operators of a data-parallel training step around the AllReduce.
  * Layer norm, whose backward pass sums the parameters' gradients over a
- * rank's rows (what the rank hands to the AllReduce), and the norm of a list
+ * rank's rows (what the rank hands to the AllReduce), dropout, the norm and
+ * rotation of query and key heads, the losses of policies and preferences with
+ * their gradients, and the norm of a list
  * of gradients with clipping by it (what follows the AllReduce). They have no
  * communicator and keep nothing between calls: calls on different streams,
  * with workspaces of their own, may overlap. They are asynchronous on `stream`
@@ -439,6 +441,167 @@ VR_API vrResult_t vrClipGradNorm(const void* const* grads, void* const* outs,
                                  const size_t* counts, const vrDataType_t* dtypes, int nTensors,
                                  float scale, float maxNorm, float* norm, void* workspace,
                                  size_t workspaceBytes, void* stream);
+
+/* Dropout by a counter-based generator, with an addition: the mask is a function of
+ * the seed and of each element's number, and is never stored.
+ *   y = residual + (u(n) >= round(p 2^32) ? x / (1 - p) : 0),  n = offset + row cols + column
+ * u(n), 32 random bits: with block(c0, c1, c2, c3) the four words of Philox4x32-10
+ * (Salmon and others, "Parallel random numbers: as easy as 1, 2, 3", 2011) under the key
+ * (seed mod 2^32, seed div 2^32), and m = n div 8, the upper half is halfword n mod 8
+ * (the lower half of each word first) of block(m mod 2^32, m div 2^32, 0, 0), the lower
+ * half the same of block(m mod 2^32, m div 2^32, 1, 0). So a rank that passes the number
+ * of its part's first element as offset drops what one rank with the whole batch drops,
+ * and the backward pass is the same call on dy, without a residual.
+ *  x, residual, y   [device] rows x cols of `dtype`, with row strides >= cols; residual
+ *           may be NULL (nothing is added). y == x and y == residual are allowed
+ *           with equal strides, other overlaps are not.
+ *  p        in [0, 1]; 1 drops everything.
+ *  seedDevice   [device] one uint64_t that is read by the kernel in place of `seed` (so
+ *           that a captured graph draws anew each time), or NULL.
+ *  offset   any; numbers wrap at 2^64.
+ *  dtype    vrFloat16, vrBfloat16 or vrFloat32.
+ * An element that is dropped counts for nothing, be it infinite or NaN. */
+VR_API vrResult_t vrDropout(const void* x, const void* residual, void* y, size_t rows, size_t cols,
+                            size_t xStride, size_t residualStride, size_t yStride, double p,
+                            uint64_t seed, const uint64_t* seedDevice, uint64_t offset,
+                            vrDataType_t dtype, void* stream);
+
+/* The root-mean-square norm of each query and key head, and its rotation by the token's
+ * position, in one pass: for each head x of `dim` elements
+ *   r = 1 / sqrt(sum(x^2) / dim + eps),  u = x r,  y = R (u weight)
+ * R turns pair i of the first rotaryDim elements, (a, b), into (a c - b s, b c + a s), with
+ * c and s the elements i of row `position` of the tables. Pair i is elements i and
+ * i + rotaryDim / 2, or with `interleaved` 2 i and 2 i + 1.
+ *  q, k     [device] heads of `dtype`: element i of head h of token t of batch b lies
+ *           at b strides[0] + t strides[1] + h strides[2] + i (strides [host], 3 each, in
+ *           elements; any, 0 too). kHeads may be 0, k is then not examined.
+ *  qWeight, kWeight   [device] dim elements of weightType, or NULL: ones.
+ *  qOut, kOut   [device] as q and k, with strides of their own, no two elements in one
+ *           place. In place (the same address and strides) is allowed, other overlaps are not.
+ *  cosTable, sinTable   [device] tableRows x rotaryDim / 2 floats each.
+ *  positions    [device] of positionType (vrInt32 or vrInt64), token t of batch b at
+ *           b positionStride + t (0: one for all batches). The rotated elements of a
+ *           token whose position is not in [0, tableRows) become NaN.
+ *  batch, tokens    batch tokens < 2^31; 0 returns vrSuccess and launches nothing.
+ *  dim      1 .. 1024.   rotaryDim   even, 0 .. dim; with 0 neither tables nor positions
+ *           are examined.   qHeads 1 .. 65535, kHeads 0 .. 65535.
+ *  eps      >= 0, finite.   dtype, weightType   as for vrLayerNormForward.
+ * Heads whose rows start on 16-byte boundaries and whose halves are whole 16 bytes are the
+ * fastest. */
+VR_API vrResult_t vrQkNormRopeForward(
+    const void* q, size_t qHeads, const size_t* qStrides, const void* k, size_t kHeads,
+    const size_t* kStrides, const void* qWeight, const void* kWeight, void* qOut,
+    const size_t* qOutStrides, void* kOut, const size_t* kOutStrides, const float* cosTable,
+    const float* sinTable, size_t tableRows, const void* positions, vrDataType_t positionType,
+    size_t positionStride, size_t batch, size_t tokens, size_t dim, size_t rotaryDim,
+    int interleaved, float eps, vrDataType_t dtype, vrDataType_t weightType, void* stream);
+
+/* Workspace bytes of vrQkNormRopeBackward, for any sizes. Host only. */
+VR_API vrResult_t vrQkNormRopeBackwardWorkspace(size_t dim, size_t* bytes);
+
+/* The backward pass of vrQkNormRopeForward, from its inputs: with g = R^T dy,
+ *   dx = r (g weight - u sum(g weight u) / dim)      for each head,
+ *   dweight = sum over tokens and heads of g u.
+ *  dq, dk       [device] the gradients of qOut and kOut, dqIn, dkIn [device] those of q and
+ *           k, of `dtype`, each with strides of its own; dqIn may be dq and dkIn dk with
+ *           the same strides, other overlaps are not allowed.
+ *  dqWeight, dkWeight   [device] dim elements of weightType, overwritten (zeros if there
+ *           are no tokens); NULL: not wanted.
+ *  workspace    [device] 16-byte aligned, of at least vrQkNormRopeBackwardWorkspace bytes;
+ *           may be NULL if dqWeight and dkWeight are.
+ * Other arguments as in the forward pass. */
+VR_API vrResult_t vrQkNormRopeBackward(
+    const void* dq, const size_t* dqStrides, const void* dk, const size_t* dkStrides,
+    const void* q, size_t qHeads, const size_t* qStrides, const void* k, size_t kHeads,
+    const size_t* kStrides, const void* qWeight, const void* kWeight, void* dqIn,
+    const size_t* dqInStrides, void* dkIn, const size_t* dkInStrides, void* dqWeight,
+    void* dkWeight, const float* cosTable, const float* sinTable, size_t tableRows,
+    const void* positions, vrDataType_t positionType, size_t positionStride, size_t batch,
+    size_t tokens, size_t dim, size_t rotaryDim, int interleaved, float eps, vrDataType_t dtype,
+    vrDataType_t weightType, void* workspace, size_t workspaceBytes, void* stream);
+
+/* The log probability of each row's target under its logits:
+ *   lse = log(sum(exp(x))),  logp = x[target] - lse
+ *  logits   [device] rows x cols of `dtype` (vrFloat16, vrBfloat16, vrFloat32), row stride
+ *           >= cols: what lies between cols and the stride is not read.
+ *  targets  [device] one of [0, cols) a row. A negative one says that the row counts for
+ *           nothing: it is not read, logp and lse are 0. One of cols or more makes logp NaN.
+ *  logp, lse, rest   [device] rows floats; rest, or lse and rest, may be NULL. rest is what lse
+ *           lost by being rounded: it matters where all logits of a row are large.
+ *  rows     0 returns vrSuccess and launches nothing.  cols >= 1.
+ * Logits of -inf are impossible tokens; +inf, NaN, or a row of -inf alone make the row NaN. */
+VR_API vrResult_t vrTokenLogProbsForward(const void* logits, const int64_t* targets, float* logp,
+                                         float* lse, float* rest, size_t rows, size_t cols,
+                                         size_t stride, vrDataType_t dtype, void* stream);
+
+/* The gradient of the logits from that by logp: with c = dlogp gain,
+ *   dlogits[j] = c ([j = target] - exp(x[j] - lse))
+ *  dlogp    [device] rows floats. A row of 0, or of a negative target, gives zeros,
+ *           whatever its logits hold; they are not read.
+ *  gain     [device] one float, or NULL: 1.
+ *  lse, rest    [device] as the forward pass wrote them; rest NULL: zeros.
+ *  dlogits  [device] rows x cols of `dtype`, row stride dStride; may be logits, with the
+ *           same stride; other overlaps are not allowed. */
+VR_API vrResult_t vrTokenLogProbsBackward(const float* dlogp, const float* gain,
+                                          const void* logits, const int64_t* targets,
+                                          const float* lse, const float* rest, void* dlogits,
+                                          size_t rows, size_t cols, size_t stride, size_t dStride,
+                                          vrDataType_t dtype, void* stream);
+
+/* Workspace bytes of vrPolicyLoss. Host only. */
+VR_API vrResult_t vrPolicyLossWorkspace(size_t rows, size_t* bytes);
+
+/* The clipped loss of a policy with a term that holds it to a reference policy, and its
+ * gradient: with logp as above and e = logp - oldLogp, a row's loss is
+ *   -min(exp(e) A, min(max(exp(e), 1 - clipLow), 1 + clipHigh) A)
+ *     + klCoef (exp(refLogp - logp) - (refLogp - logp) - 1)
+ * and loss = scale sum(weight times the row's loss). Where the clipped ratio decides the
+ * first term has no derivative.
+ *  oldLogp, advantages (A)   [device] rows floats.
+ *  weights  [device] rows floats, or NULL: ones. A row of weight 0, or of a negative
+ *           target, counts for nothing, whatever its other inputs hold.
+ *  refLogp  [device] rows floats, or NULL: no such term; nor is there one if klCoef is 0.
+ *  loss     [device] one float. 0 without rows.
+ *  logp, lse, rest, dlogp   [device] rows floats: the last is the loss's derivative by logp, for
+ *           vrTokenLogProbsBackward. Rows that count for nothing get zeros in all of them.
+ *  dlogits  [device] the gradient of the logits, or NULL: not wanted. May be logits, as in
+ *           vrTokenLogProbsBackward.
+ *  clipLow, clipHigh    >= 0, may be infinite.   klCoef, scale   finite.
+ *  workspace    [device] 16-byte aligned, of at least vrPolicyLossWorkspace bytes. */
+VR_API vrResult_t vrPolicyLoss(const void* logits, const int64_t* targets, const float* oldLogp,
+                               const float* advantages, const float* weights,
+                               const float* refLogp, float* loss, float* logp, float* lse,
+                               float* rest, float* dlogp, void* dlogits, size_t rows, size_t cols,
+                               size_t stride, size_t dStride, double clipLow, double clipHigh,
+                               float klCoef, float scale, vrDataType_t dtype, void* workspace,
+                               size_t workspaceBytes, void* stream);
+
+/* Workspace bytes of vrPreferenceLoss. Host only. */
+VR_API vrResult_t vrPreferenceLossWorkspace(size_t pairs, size_t* bytes);
+
+/* The loss of preferences between paired sequences, by the ratio of their probabilities
+ * under the policy to those under a reference, and its gradient. Sequence s < pairs is
+ * pair s's chosen one, pairs + s its rejected one; S is the sum of logp over a sequence's rows.
+ *   h = beta ((S - ref)[chosen] - (S - ref)[rejected])
+ *   loss = scale sum over pairs of (1 - labelSmoothing) log(1 + exp(-h)) + labelSmoothing log(1 + exp(h))
+ *  starts   [device] 2 pairs + 1 numbers of rows: sequence s is the rows from starts[s] to
+ *           before starts[s + 1], cut at the rows that there are; none where the second is
+ *           not larger. Rows of no sequence count for nothing. NULL: the rows in 2 pairs
+ *           equal parts.
+ *  targets  negative: the row (of a prompt, or padding) counts for nothing.
+ *  refLogps     [device] 2 pairs floats, or NULL: zeros.
+ *  loss     [device] one float.  logps   [device] 2 pairs floats, S.
+ *  logp, lse, rest, dlogp, dlogits   as in vrPolicyLoss, but that logp, lse and rest of rows
+ *           of no sequence are theirs.
+ *  pairs >= 1, rows any.  beta, scale   finite.  labelSmoothing   in [0, 1].
+ *  workspace    [device] 16-byte aligned, of at least vrPreferenceLossWorkspace bytes. */
+VR_API vrResult_t vrPreferenceLoss(const void* logits, const int64_t* targets,
+                                   const float* refLogps, const int64_t* starts, float* loss,
+                                   float* logps, float* logp, float* lse, float* rest, float* dlogp,
+                                   void* dlogits, size_t pairs, size_t rows, size_t cols,
+                                   size_t stride, size_t dStride, float beta,
+                                   float labelSmoothing, float scale, vrDataType_t dtype,
+                                   void* workspace, size_t workspaceBytes, void* stream);
 
 /* Static description of a result code. Never NULL. */
 VR_API const char* vrGetErrorString(vrResult_t result);

@@ -9,12 +9,15 @@ CPU fallback: if libvr.so has not been built, every call raises ImportError.
                            chunk_bytes=512 << 10)
     comm.all_reduce(send_tensors, recv_tensors, op="sum")   # on the current stream
 
-The operators of a training step around it (layer norm forward and backward,
-the norm of a list of gradients, clipping by it) are the module `training`.
+The operators of a training step around it (layer norm, dropout, the norm and
+rotation of query and key heads, the losses of policies and preferences, each
+forward and backward; the norm of a list of gradients, clipping by it) are the
+module `training`.
 
 Build the library with `python -m ring_allreduce_virtual_gb300.build`.
 """
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -82,8 +85,27 @@ def lib():
         L.vrGradNormWorkspace.argtypes = [i32, psz]
         L.vrGradNorm.argtypes = [pp, psz, pi32, i32, f32, vp, vp, vp, sz, vp]
         L.vrClipGradNorm.argtypes = [pp, pp, psz, pi32, i32, f32, f32, vp, vp, sz, vp]
+        f64 = ctypes.c_double
+        L.vrDropout.argtypes = [vp, vp, vp, sz, sz, sz, sz, sz, f64, u64, vp, u64, i32, vp]
+        rotation = [vp, vp, sz, vp, i32, sz, sz, sz, sz, sz, i32, f32, i32, i32]
+        L.vrQkNormRopeForward.argtypes = [vp, sz, psz, vp, sz, psz, vp, vp, vp, psz, vp, psz,
+                                          *rotation, vp]
+        L.vrQkNormRopeBackwardWorkspace.argtypes = [sz, psz]
+        L.vrQkNormRopeBackward.argtypes = [vp, psz, vp, psz, vp, sz, psz, vp, sz, psz, vp, vp,
+                                           vp, psz, vp, psz, vp, vp, *rotation, vp, sz, vp]
+        L.vrTokenLogProbsForward.argtypes = [vp, vp, vp, vp, vp, sz, sz, sz, i32, vp]
+        L.vrTokenLogProbsBackward.argtypes = [vp] * 7 + [sz, sz, sz, sz, i32, vp]
+        L.vrPolicyLossWorkspace.argtypes = [sz, psz]
+        L.vrPolicyLoss.argtypes = [vp] * 12 + [sz, sz, sz, sz, f64, f64, f32, f32, i32, vp, sz, vp]
+        L.vrPreferenceLossWorkspace.argtypes = [sz, psz]
+        L.vrPreferenceLoss.argtypes = [vp] * 11 + [sz, sz, sz, sz, sz, f32, f32, f32, i32, vp, sz,
+                                                   vp]
         for name in ("vrLayerNormForward", "vrLayerNormBackwardWorkspace", "vrLayerNormBackward",
-                     "vrGradNormWorkspace", "vrGradNorm", "vrClipGradNorm"):
+                     "vrGradNormWorkspace", "vrGradNorm", "vrClipGradNorm", "vrDropout",
+                     "vrQkNormRopeForward", "vrQkNormRopeBackwardWorkspace",
+                     "vrQkNormRopeBackward", "vrTokenLogProbsForward", "vrTokenLogProbsBackward",
+                     "vrPolicyLossWorkspace", "vrPolicyLoss", "vrPreferenceLossWorkspace",
+                     "vrPreferenceLoss"):
             getattr(L, name).restype = i32
         for name in ("vrCommCreate", "vrAllReduce", "vrCommDestroy", "vrCommGetAsyncError",
                      "vrCommSetTimeout", "vrCommGetInfo", "vrAllReduceNoAlloc",
@@ -330,6 +352,112 @@ def vrClipGradNorm(arrays, outs, scale, maxNorm, norm, workspace, workspaceBytes
     _check(lib().vrClipGradNorm(ptrs, outs, counts, types, len(ptrs), scale, maxNorm,
                                 norm or None, workspace or None, workspaceBytes, stream or None),
            "vrClipGradNorm")
+
+
+def vrDropout(x, residual, y, rows, cols, xStride, residualStride, yStride, p, seed, seedDevice,
+              offset, dtype, stream=0):
+    _check(lib().vrDropout(x or None, residual or None, y or None, rows, cols, xStride,
+                           residualStride, yStride, p, seed, seedDevice or None, offset,
+                           _code(DTYPES, dtype, "dtype"), stream or None), "vrDropout")
+
+
+@functools.lru_cache(maxsize=1024)
+def strides3(batch, token, head):
+    """The host array of a tensor's batch, token and head strides (elements) that
+    vrQkNormRopeForward and vrQkNormRopeBackward read, kept for the next call."""
+    return (ctypes.c_size_t * 3)(batch, token, head)
+
+
+def _strides(s):
+    return strides3(*s) if s is not None else None
+
+
+def vrQkNormRopeForward(q, qHeads, qStrides, k, kHeads, kStrides, qWeight, kWeight, qOut,
+                        qOutStrides, kOut, kOutStrides, cosTable, sinTable, tableRows, positions,
+                        positionType, positionStride, batch, tokens, dim, rotaryDim, interleaved,
+                        eps, dtype, weightType, stream=0):
+    """Strides: (batch, token, head) each, or None: NULL."""
+    _check(lib().vrQkNormRopeForward(
+        q or None, qHeads, _strides(qStrides), k or None, kHeads, _strides(kStrides),
+        qWeight or None, kWeight or None, qOut or None, _strides(qOutStrides), kOut or None,
+        _strides(kOutStrides), cosTable or None, sinTable or None, tableRows, positions or None,
+        _code(DTYPES, positionType, "dtype"), positionStride, batch, tokens, dim, rotaryDim,
+        interleaved, eps, _code(DTYPES, dtype, "dtype"), _code(DTYPES, weightType, "dtype"),
+        stream or None), "vrQkNormRopeForward")
+
+
+def _workspace(name, n):
+    b = ctypes.c_size_t()
+    _check(getattr(lib(), name)(n, ctypes.byref(b)), name)
+    return b.value
+
+
+def vrQkNormRopeBackwardWorkspace(dim):
+    """Workspace bytes of vrQkNormRopeBackward."""
+    return _workspace("vrQkNormRopeBackwardWorkspace", dim)
+
+
+def vrQkNormRopeBackward(dq, dqStrides, dk, dkStrides, q, qHeads, qStrides, k, kHeads, kStrides,
+                         qWeight, kWeight, dqIn, dqInStrides, dkIn, dkInStrides, dqWeight,
+                         dkWeight, cosTable, sinTable, tableRows, positions, positionType,
+                         positionStride, batch, tokens, dim, rotaryDim, interleaved, eps, dtype,
+                         weightType, workspace, workspaceBytes, stream=0):
+    _check(lib().vrQkNormRopeBackward(
+        dq or None, _strides(dqStrides), dk or None, _strides(dkStrides), q or None, qHeads,
+        _strides(qStrides), k or None, kHeads, _strides(kStrides), qWeight or None,
+        kWeight or None, dqIn or None, _strides(dqInStrides), dkIn or None,
+        _strides(dkInStrides), dqWeight or None, dkWeight or None, cosTable or None,
+        sinTable or None, tableRows, positions or None, _code(DTYPES, positionType, "dtype"),
+        positionStride, batch, tokens, dim, rotaryDim, interleaved, eps,
+        _code(DTYPES, dtype, "dtype"), _code(DTYPES, weightType, "dtype"), workspace or None,
+        workspaceBytes, stream or None), "vrQkNormRopeBackward")
+
+
+def vrTokenLogProbsForward(logits, targets, logp, lse, rest, rows, cols, stride, dtype, stream=0):
+    _check(lib().vrTokenLogProbsForward(logits or None, targets or None, logp or None,
+                                        lse or None, rest or None, rows, cols, stride,
+                                        _code(DTYPES, dtype, "dtype"), stream or None),
+           "vrTokenLogProbsForward")
+
+
+def vrTokenLogProbsBackward(dlogp, gain, logits, targets, lse, rest, dlogits, rows, cols, stride,
+                            dStride, dtype, stream=0):
+    _check(lib().vrTokenLogProbsBackward(dlogp or None, gain or None, logits or None,
+                                         targets or None, lse or None, rest or None,
+                                         dlogits or None, rows, cols, stride, dStride, _code(DTYPES, dtype, "dtype"),
+                                         stream or None), "vrTokenLogProbsBackward")
+
+
+def vrPolicyLossWorkspace(rows):
+    """Workspace bytes of vrPolicyLoss."""
+    return _workspace("vrPolicyLossWorkspace", rows)
+
+
+def vrPolicyLoss(logits, targets, oldLogp, advantages, weights, refLogp, loss, logp, lse, rest,
+                 dlogp, dlogits, rows, cols, stride, dStride, clipLow, clipHigh, klCoef, scale, dtype,
+                 workspace, workspaceBytes, stream=0):
+    _check(lib().vrPolicyLoss(logits or None, targets or None, oldLogp or None,
+                              advantages or None, weights or None, refLogp or None, loss or None,
+                              logp or None, lse or None, rest or None, dlogp or None,
+                              dlogits or None, rows, cols, stride, dStride, clipLow, clipHigh, klCoef, scale,
+                              _code(DTYPES, dtype, "dtype"), workspace or None, workspaceBytes,
+                              stream or None), "vrPolicyLoss")
+
+
+def vrPreferenceLossWorkspace(pairs):
+    """Workspace bytes of vrPreferenceLoss."""
+    return _workspace("vrPreferenceLossWorkspace", pairs)
+
+
+def vrPreferenceLoss(logits, targets, refLogps, starts, loss, logps, logp, lse, rest, dlogp,
+                     dlogits, pairs, rows, cols, stride, dStride, beta, labelSmoothing, scale, dtype,
+                     workspace, workspaceBytes, stream=0):
+    _check(lib().vrPreferenceLoss(logits or None, targets or None, refLogps or None,
+                                  starts or None, loss or None, logps or None, logp or None,
+                                  lse or None, rest or None, dlogp or None, dlogits or None, pairs, rows, cols,
+                                  stride, dStride, beta, labelSmoothing, scale,
+                                  _code(DTYPES, dtype, "dtype"), workspace or None,
+                                  workspaceBytes, stream or None), "vrPreferenceLoss")
 
 
 # ------------------------------------------------------------ torch helper

@@ -12,9 +12,7 @@
 // weights, and whose gradients' sums, it keeps in registers.
 #pragma once
 
-#include <mutex>
-
-#include "vr_opcommon.cuh"
+#include "vr_packs.cuh"
 
 namespace vrln {
 
@@ -33,98 +31,6 @@ struct Layout {
 };
 
 constexpr int kMaxWarps = 32;
-
-template <typename T>
-constexpr int kV = 16 / (int)sizeof(T);
-
-// Two floats in one 64-bit register pair: sm_103a adds and multiplies both in
-// one instruction, which halves the arithmetic of a row.
-struct F2 {
-  unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
-__device__ __forceinline__ void split(F2 a, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-}
-__device__ __forceinline__ float both(F2 a) {
-  float x, y;
-  split(a, x, y);
-  return x + y;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
-// One 32-bit word of T (two 16-bit elements) as floats.
-template <typename T>
-__device__ __forceinline__ F2 word2(uint32_t w) {
-  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  } else {
-    __half2 h;
-    memcpy(&h, &w, 4);
-    const float2 f = __half22float2(h);
-    return f2(f.x, f.y);
-  }
-}
-
-// A pack as pairs of floats, and back (the one rounding of a result).
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4& v, F2* f) {
-  if constexpr (sizeof(T) == 4) {
-    f[0] = f2(__uint_as_float(v.x), __uint_as_float(v.y));
-    f[1] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
-  } else {
-    f[0] = word2<T>(v.x);
-    f[1] = word2<T>(v.y);
-    f[2] = word2<T>(v.z);
-    f[3] = word2<T>(v.w);
-  }
-}
-template <typename T>
-__device__ __forceinline__ uint32_t round2(F2 a) {
-  float x, y;
-  split(a, x, y);
-  uint32_t w;
-  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    memcpy(&w, &h, 4);
-  } else {
-    const __half2 h = __floats2half2_rn(x, y);
-    memcpy(&w, &h, 4);
-  }
-  return w;
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const F2* f) {
-  uint4 v;
-  if constexpr (sizeof(T) == 4) {
-    float e[4];
-    split(f[0], e[0], e[1]);
-    split(f[1], e[2], e[3]);
-    memcpy(&v, e, 16);
-  } else {
-    v = make_uint4(round2<T>(f[0]), round2<T>(f[1]), round2<T>(f[2]), round2<T>(f[3]));
-  }
-  return v;
-}
 
 // Rows on their way into shared memory. Each thread copies the packs that it
 // will read itself, some rows ahead, so no barrier separates the copy from the
@@ -183,29 +89,6 @@ struct Params {
     }
   }
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void store_remote(float* p, uint32_t cta, float v) {
-  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(cta));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(r), "f"(v) : "memory");
-}
-
-__device__ __forceinline__ float load_remote(const float* p, uint32_t cta) {
-  uint32_t a = (uint32_t)__cvta_generic_to_shared(p), r;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(cta));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
-  return v;
-}
 
 // Sums of N values (N rows') over the threads of a row, the same in each of
 // them. In a warp the N values share the steps: after log2(N) of them a lane
@@ -328,31 +211,9 @@ inline int residentWarps(int regs, size_t smem, int threads) {
 // Dynamic shared memory of a block, at most.
 constexpr size_t kMostShared = 200 * 1024;
 
-// Sets an attribute of a kernel, once on each device.
-inline bool setOnce(const void* kernel, cudaFuncAttribute what, int value) {
-  constexpr int kSeen = 256;
-  static std::mutex m;
-  static const void* seen[kSeen];
-  static int device[kSeen], attribute[kSeen], n = 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  std::lock_guard<std::mutex> g(m);
-  for (int i = 0; i < n; ++i)
-    if (seen[i] == kernel && device[i] == dev && attribute[i] == (int)what) return true;
-  if (cudaFuncSetAttribute(kernel, what, value) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  if (n < kSeen) seen[n] = kernel, attribute[n] = (int)what, device[n++] = dev;
-  return true;
-}
 inline bool allowShared(const void* kernel) {
   return setOnce(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostShared);
 }
-inline bool allowLargeClusters(const void* kernel) {
-  return setOnce(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-}
-
 // How rows of `cols` elements are laid over threads: PACKS packs for each
 // thread, in a warp, a block, or a cluster of up to 8 blocks; blocks of as many
 // rows as blockThreads hold (smaller blocks that fill an SM better are slower:

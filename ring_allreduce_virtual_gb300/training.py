@@ -1,9 +1,10 @@
 """The operators of a data-parallel training step around the AllReduce, on
-torch tensors: layer norm (forward, backward, and as a differentiable call), the
-norm of a list of gradients, and clipping by it. Everything is computed by the
-kernels of libvr.so (include/vr.h states the formulas and the rules); this
-module checks the tensors, allocates outputs and workspaces, and passes
-addresses. There is no CPU fallback.
+torch tensors: layer norm, dropout, the norm and rotation of query and key heads,
+and the losses of policies and preferences (each forward, backward, and as a
+differentiable call), the norm of a list of gradients, and clipping by it.
+Everything is computed by the kernels of libvr.so (include/vr.h states the
+formulas and the rules); this module checks the tensors, allocates outputs and
+workspaces, and passes addresses. There is no CPU fallback.
 
     from ring_allreduce_virtual_gb300 import training
     y = training.layer_norm(x, weight, bias)            # differentiable
@@ -355,3 +356,565 @@ def clip_grad_norm(grads, max_norm, scale=1.0, outs=None, stream=None):
         raise vr.VrError(rc, "vrClipGradNorm")
     _written(to.bases if kept else to.tensors)
     return norm
+
+
+# ----------------------------------------------------------------- dropout
+def _seed(seed, x, device):
+    """(seed, address of the seed) of a number or of a CUDA tensor of one int64."""
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.get_device() != device:
+            raise ValueError("seed must be an integer or one int64 on x's device")
+        return 0, seed.data_ptr()
+    if not 0 <= seed < 1 << 64:
+        raise ValueError("seed must be in [0, 2^64)")
+    return seed, None
+
+
+def dropout_forward(x, p, seed, offset=0, residual=None, out=None, stream=None):
+    """x / (1 - p) where an element stays, 0 where it is dropped (probability p), plus
+    `residual` (of x's shape and type). Whether element i of x, counted along its
+    shape, stays is a function of `seed` and of offset + i alone: no mask is kept, and
+    a rank that gives the number of its part's first element as `offset` drops what
+    one rank would with the whole batch. `seed`: an integer of [0, 2^64), or a CUDA
+    tensor of one int64, read when the kernel runs, so that a captured graph draws
+    anew once that tensor is changed. `out`: a tensor of x's shape and type, x and
+    residual themselves allowed. Tensors of x's shape have a dense last axis and
+    leading axes that are one row stride apart."""
+    if stream is not None:
+        return _on(stream, x.get_device(), dropout_forward, x, p, seed, offset, residual, out)
+    cols, code, device = _check_x(x)
+    if device != _current_device():
+        return _on_device(device, dropout_forward, x, p, seed, offset, residual, out)
+    if not 0 <= p <= 1:
+        raise ValueError("p must be in [0, 1]")
+    if not 0 <= offset < 1 << 64:
+        raise ValueError("offset must be in [0, 2^64)")
+    seed, at = _seed(seed, x, device)
+    rows, xs = _rows(x, "x")
+    rs = cols
+    if residual is not None:
+        _check_like(residual, x, device, "residual")
+        rs = _rows(residual, "residual")[1]
+    if out is None:
+        y, ys = _dense_like(x), cols
+    else:
+        _check_like(out, x, device, "out")
+        y, ys = out, _rows(out, "out")[1]
+    rc = vr.lib().vrDropout(x.data_ptr(), _ptr(residual), y.data_ptr(), rows, cols, xs, rs, ys, p,
+                            seed, at, offset, code, _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrDropout")
+    if out is not None:
+        _written(out)
+    return y
+
+
+def dropout_backward(dy, p, seed, offset=0, out=None, stream=None):
+    """The gradient of dropout_forward's x from that of its result, with the same p,
+    seed and offset (the residual's gradient is dy). `out`: dy itself allowed."""
+    return dropout_forward(dy, p, seed, offset, None, out, stream)
+
+
+def _as_rows(t):
+    return t if not t.dim() or not t.shape[-1] or _has_rows(t) else t.contiguous()
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, residual):
+        tensor = isinstance(seed, torch.Tensor)
+        ctx.save_for_backward(*([seed] if tensor else []))
+        ctx.args = (p, None if tensor else seed, offset)
+        return dropout_forward(_as_rows(x), p, seed, offset,
+                               None if residual is None else _as_rows(residual))
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        p, seed, offset = ctx.args
+        if ctx.saved_tensors:
+            seed, = ctx.saved_tensors
+        dx = dropout_backward(_as_rows(dy), p, seed, offset) if ctx.needs_input_grad[0] else None
+        return dx, None, None, None, dy if ctx.needs_input_grad[4] else None
+
+
+def dropout(x, p, seed, offset=0, residual=None):
+    """dropout_forward, differentiable once with respect to x and residual; tensors of
+    other layouts are copied first. A seed tensor has to hold its value until the
+    backward pass; autograd refuses one that was changed in place."""
+    return _Dropout.apply(x, p, seed, offset, residual)
+
+
+# ---------------------------------------------- norm and rotation of heads
+def _heads(t, what, batch=None, tokens=None, dim=None, dtype=None, device=None):
+    """(batch, tokens, heads, dim, strides) of a tensor of (tokens, heads, dim) or
+    (batch, tokens, heads, dim)."""
+    n = t.dim()
+    if n != 3 and n != 4:
+        raise ValueError(f"{what} must be (tokens, heads, dim) or (batch, tokens, heads, dim)")
+    shape, st = t.shape, t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{what}: the last axis must be dense")
+    b = shape[0] if n == 4 else 1
+    if dim is not None and (b != batch or shape[-3] != tokens or shape[-1] != dim or
+                            t.dtype != dtype or t.get_device() != device):
+        raise ValueError(f"{what} does not match q in batch, tokens, dim, type or device")
+    return b, shape[-3], shape[-2], shape[-1], vr.strides3(st[0] if n == 4 else 0, st[-3], st[-2])
+
+
+def _rotation(cos, sin, positions, batch, tokens, dim, device):
+    """The arguments that describe the rotation, of the forward and the backward pass."""
+    if cos is None:
+        if sin is not None:
+            raise ValueError("cos and sin go together")
+        return None, None, 0, None, 4, 0, 0
+    if sin is None or positions is None:
+        raise ValueError("a rotation needs cos, sin and positions")
+    for t in (cos, sin):
+        if t.dtype != _F32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous() or \
+                t.get_device() != device or 2 * t.shape[1] > dim:
+            raise ValueError("cos and sin must be dense float32 (positions, rotary / 2) on q's device")
+    if positions.get_device() != device or positions.dtype not in _POSITION:
+        raise ValueError("positions must be int32 or int64 on q's device")
+    shape = tuple(positions.shape)
+    if shape == (batch, tokens) and (tokens <= 1 or positions.stride(1) == 1):
+        stride = positions.stride(0)
+    elif shape == (tokens,) and (tokens <= 1 or positions.stride(0) == 1):
+        stride = 0
+    else:
+        raise ValueError("positions must be (tokens,) or (batch, tokens), dense along tokens")
+    return (cos.data_ptr(), sin.data_ptr(), cos.shape[0], positions.data_ptr(),
+            _POSITION[positions.dtype], stride, 2 * cos.shape[1])
+
+
+_POSITION = {torch.int32: vr.DTYPES["int32"], torch.int64: vr.DTYPES["int64"]}
+
+
+def _head_weights(q, dim, device, *weights):
+    """The type code of the given weights, one type for all."""
+    first = None
+    for w in weights:
+        if w is None:
+            continue
+        _check_param(w, q, dim, device, first)
+        first = w
+    return _NORM_CODE[q.dtype if first is None else first.dtype]
+
+
+def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                         eps=1e-6, interleaved=False, q_out=None, k_out=None, stream=None):
+    """(q', k'): the root-mean-square norm of each head of q and k over its last axis,
+    times the weight, rotated by its token's position. q: (batch, tokens, heads, dim) or
+    (tokens, heads, dim), of any strides with a dense last axis, such as views of one
+    projection's output or of (batch, heads, tokens, dim); k the same with heads of its
+    own, or None. Weights: dense vectors of dim elements, shared by the heads. cos, sin:
+    float32 tables of (positions, rotary / 2), rotary <= dim elements are rotated, in
+    pairs of halves or, interleaved, of neighbours; None: no rotation. positions: int32
+    or int64, (batch, tokens) or (tokens,). q_out and k_out: tensors of q's and k's
+    shape, q and k themselves allowed."""
+    if stream is not None:
+        return _on(stream, q.get_device(), qk_norm_rope_forward, q, k, q_weight, k_weight, cos, sin,
+                   positions, eps, interleaved, q_out, k_out)
+    _, code, device = _check_x(q)
+    if device != _current_device():
+        return _on_device(device, qk_norm_rope_forward, q, k, q_weight, k_weight, cos, sin, positions,
+                          eps, interleaved, q_out, k_out)
+    batch, tokens, heads, dim, qs = _heads(q, "q")
+    like = (batch, tokens, dim, q.dtype, device)
+    kheads, ks, yk, yks = 0, None, None, None
+    wcode = _head_weights(q, dim, device, q_weight, k_weight)
+    if k is not None:
+        _, _, kheads, _, ks = _heads(k, "k", *like)
+        yk = torch.empty_like(k) if k_out is None else k_out
+        if yk.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        yks = _heads(yk, "k_out", *like)[4]
+    yq = torch.empty_like(q) if q_out is None else q_out
+    if yq.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    yqs = _heads(yq, "q_out", *like)[4]
+    c, s, table, at, kind, step, rot = _rotation(cos, sin, positions, batch, tokens, dim, device)
+    rc = vr.lib().vrQkNormRopeForward(
+        q.data_ptr(), heads, qs, _ptr(k), kheads, ks, _ptr(q_weight), _ptr(k_weight), yq.data_ptr(),
+        yqs, _ptr(yk), yks, c, s, table, at, kind, step, batch, tokens, dim, rot, interleaved, eps,
+        code, wcode, _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrQkNormRopeForward")
+    for t in (q_out, k_out):
+        if t is not None:
+            _written(t)
+    return yq, yk
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_workspace(dim):
+    return vr.vrQkNormRopeBackwardWorkspace(dim)
+
+
+def qk_norm_rope_backward(dq, dk, q, k, q_weight=None, k_weight=None, cos=None, sin=None,
+                          positions=None, eps=1e-6, interleaved=False, dq_weight=True,
+                          dk_weight=True, dq_in=None, dk_in=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight): the gradients of qk_norm_rope_forward's inputs from
+    those of its results. dq_weight and dk_weight may each be False (not wanted, None is
+    returned) or a tensor to write to, such as a view of the flat bucket that the AllReduce
+    takes; they have the weights' type (q's without). dq_in and dk_in: tensors for the
+    gradients of q and k, such as views of one projection's gradient; dq and dk themselves
+    allowed."""
+    if stream is not None:
+        return _on(stream, q.get_device(), qk_norm_rope_backward, dq, dk, q, k, q_weight, k_weight,
+                   cos, sin, positions, eps, interleaved, dq_weight, dk_weight, dq_in, dk_in)
+    _, code, device = _check_x(q)
+    if device != _current_device():
+        return _on_device(device, qk_norm_rope_backward, dq, dk, q, k, q_weight, k_weight, cos, sin,
+                          positions, eps, interleaved, dq_weight, dk_weight, dq_in, dk_in)
+    batch, tokens, heads, dim, qs = _heads(q, "q")
+    like = (batch, tokens, dim, q.dtype, device)
+    given = [t for t in (dq_weight, dk_weight, dq_in, dk_in) if isinstance(t, torch.Tensor)]
+    wcode = _head_weights(q, dim, device, q_weight, k_weight, *[
+        t for t in (dq_weight, dk_weight) if isinstance(t, torch.Tensor)])
+    wt = _TYPE[wcode]
+
+    def side(x, dy, dx, what):
+        st = _heads(x, what, *like)[4]
+        if dy.shape != x.shape or (dx is not None and dx.shape != x.shape):
+            raise ValueError(f"the gradients of {what} must have its shape")
+        dx = torch.empty_like(x) if dx is None else dx
+        return st, _heads(dy, f"d{what}", *like)[4], dx, _heads(dx, f"d{what}_in", *like)[4]
+
+    qs, dqs, dq_in, dqis = side(q, dq, dq_in, "q")
+    kheads, ks, dks, dkis = 0, None, None, None
+    if k is not None:
+        kheads = k.shape[-2]
+        ks, dks, dk_in, dkis = side(k, dk, dk_in, "k")
+    else:
+        dk, dk_in, dk_weight = None, None, False
+    grads = [dq_weight, dk_weight]
+    for i in (0, 1):
+        if grads[i] is True:
+            grads[i] = torch.empty(dim, dtype=wt, device=q.device)
+        elif not isinstance(grads[i], torch.Tensor):
+            grads[i] = None
+    ws, nbytes = None, 0
+    if grads[0] is not None or grads[1] is not None:
+        nbytes = _qk_workspace(dim)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    c, s, table, at, kind, step, rot = _rotation(cos, sin, positions, batch, tokens, dim, device)
+    rc = vr.lib().vrQkNormRopeBackward(
+        dq.data_ptr(), dqs, _ptr(dk), dks, q.data_ptr(), heads, qs, _ptr(k), kheads, ks,
+        _ptr(q_weight), _ptr(k_weight), dq_in.data_ptr(), dqis, _ptr(dk_in), dkis, _ptr(grads[0]),
+        _ptr(grads[1]), c, s, table, at, kind, step, batch, tokens, dim, rot, interleaved, eps, code,
+        wcode, _ptr(ws), nbytes, _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrQkNormRopeBackward")
+    if given:
+        _written(given)
+    return dq_in, dk_in, grads[0], grads[1]
+
+
+_TYPE = {c: t for t, c in _CODE.items()}
+
+
+def _as_heads(t):
+    return t if t is None or not t.dim() or t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        q, k = _as_heads(q), _as_heads(k)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.args = eps, interleaved
+        ctx.set_materialize_grads(False)
+        return qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dq is None and dk is None:
+            return (None,) * 9
+        dq = torch.zeros_like(q) if dq is None else _as_heads(dq)
+        if k is not None:
+            dk = torch.zeros_like(k) if dk is None else _as_heads(dk)
+        dq, dk, dqw, dkw = qk_norm_rope_backward(
+            dq, dk, q, k, q_weight, k_weight, cos, sin, positions, *ctx.args,
+            need[2] and q_weight is not None, need[3] and k_weight is not None)
+        return (dq if need[0] else None, dk if need[1] else None, dqw, dkw, None, None, None, None,
+                None)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
+                 interleaved=False):
+    """qk_norm_rope_forward, differentiable once with respect to q, k and the weights.
+    Heads whose last axis is not dense are copied first."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+
+# ------------------------------------------------------------------ losses
+def _check_logits(logits, targets):
+    """(columns, type code, device, rows, row stride) of a matrix of logits and its targets."""
+    cols, code, device = _check_x(logits)
+    if targets.dtype != torch.int64 or targets.get_device() != device or \
+            targets.shape != logits.shape[:-1] or not targets.is_contiguous():
+        raise ValueError("targets must be dense int64 of the logits' leading axes, on their device")
+    return (cols, code, device, *_rows(logits, "logits"))
+
+
+def _row_vector(t, like, what):
+    """The address of a dense float32 vector with a number for each row."""
+    if t is None:
+        return None
+    if t.dtype != _F32 or t.get_device() != like.get_device() or t.shape != like.shape or \
+            not t.is_contiguous():
+        raise ValueError(f"{what} must be dense float32 of the targets' shape, on their device")
+    return t.data_ptr()
+
+
+def _gradient_of(logits, out, device, cols):
+    """(a tensor for the logits' gradient, its row stride)"""
+    if out is None:
+        return _dense_like(logits), cols
+    _check_like(out, logits, device, "out")
+    return out, _rows(out, "out")[1]
+
+
+def token_logprobs_forward(logits, targets, rest=False, stream=None):
+    """(logp, lse): the log probability of each row's target, and the logarithm of the sum
+    of the row's exponentials (what the backward pass needs), float32. logits: (...,
+    vocabulary), a dense last axis and leading axes that are one row stride apart;
+    targets: int64 of the leading axes. A row of a negative target is not read: it gives 0.
+    rest=True: (logp, lse, rest), with what lse lost by being rounded, for gradients of
+    rows whose logits are all large (of 2^10 lse alone leaves them an error of 2^-14)."""
+    if stream is not None:
+        return _on(stream, logits.get_device(), token_logprobs_forward, logits, targets, rest)
+    cols, code, device, rows, xs = _check_logits(logits, targets)
+    if device != _current_device():
+        return _on_device(device, token_logprobs_forward, logits, targets, rest)
+    logp, lse = (torch.empty(targets.shape, dtype=_F32, device=logits.device) for _ in range(2))
+    rest = torch.empty_like(lse) if rest else None
+    rc = vr.lib().vrTokenLogProbsForward(logits.data_ptr(), targets.data_ptr(), logp.data_ptr(),
+                                         lse.data_ptr(), _ptr(rest), rows, cols, xs, code,
+                                         _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrTokenLogProbsForward")
+    return (logp, lse) if rest is None else (logp, lse, rest)
+
+
+def token_logprobs_backward(dlogp, logits, targets, lse, rest=None, gain=None, out=None,
+                            stream=None):
+    """The gradient of the logits from that by logp, times `gain` (a float32 scalar
+    tensor, such as a loss's gradient). Rows of dlogp 0 or of a negative target are 0
+    whatever their logits hold. `out`: a tensor of the logits' shape and type, logits
+    themselves allowed."""
+    if stream is not None:
+        return _on(stream, logits.get_device(), token_logprobs_backward, dlogp, logits, targets, lse,
+                   rest, gain, out)
+    cols, code, device, rows, xs = _check_logits(logits, targets)
+    if device != _current_device():
+        return _on_device(device, token_logprobs_backward, dlogp, logits, targets, lse, rest, gain, out)
+    if gain is not None and (gain.dtype != _F32 or gain.numel() != 1 or gain.get_device() != device):
+        raise ValueError("gain must be one float32 on the logits' device")
+    c, s, r = (_row_vector(t, targets, n) for t, n in ((dlogp, "dlogp"), (lse, "lse"), (rest, "rest")))
+    dx, ds = _gradient_of(logits, out, device, cols)
+    rc = vr.lib().vrTokenLogProbsBackward(c, _ptr(gain), logits.data_ptr(), targets.data_ptr(), s,
+                                          r, dx.data_ptr(), rows, cols, xs, ds, code,
+                                          _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrTokenLogProbsBackward")
+    if out is not None:
+        _written(out)
+    return dx
+
+
+def _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, clip_high, kl_coef,
+            scale, gradient, out):
+    """(loss, logp, lse, dlogp, rest, dlogits or None)"""
+    cols, code, device, rows, xs = _check_logits(logits, targets)
+    if device != _current_device():
+        return _on_device(device, _policy, logits, targets, old_logp, advantages, weights, ref_logp,
+                          clip_low, clip_high, kl_coef, scale, gradient, out)
+    if old_logp is None or advantages is None:
+        raise ValueError("a policy loss needs old_logp and advantages")
+    vectors = [_row_vector(t, targets, n) for t, n in
+               ((old_logp, "old_logp"), (advantages, "advantages"), (weights, "weights"),
+                (ref_logp, "ref_logp"))]
+    dx, ds = _gradient_of(logits, out, device, cols) if gradient else (None, 0)
+    loss = torch.empty((), dtype=_F32, device=logits.device)
+    logp = torch.empty(targets.shape, dtype=_F32, device=logits.device)
+    lse, dlogp, rest, at = _row_buffers(targets, rows)
+    rc = vr.lib().vrPolicyLoss(logits.data_ptr(), targets.data_ptr(), *vectors, loss.data_ptr(),
+                               logp.data_ptr(), lse.data_ptr(), rest.data_ptr(), dlogp.data_ptr(),
+                               _ptr(dx), rows, cols, xs, ds, clip_low, clip_high, kl_coef, scale,
+                               code, at, 4 * rows, _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrPolicyLoss")
+    if out is not None:
+        _written(out)
+    return loss, logp, lse, dlogp, rest, dx
+
+
+def _row_buffers(targets, rows, extra=0):
+    """(lse, dlogp, rest, address of a workspace): one allocation for what a call keeps of
+    its rows, an aligned workspace of a float a row and `extra` bytes behind it."""
+    n = (rows + 3) // 4 * 4
+    kept = torch.empty(4 * n + extra // 4, dtype=_F32, device=targets.device)
+    return (*(kept[i * n: i * n + rows].view(targets.shape) for i in range(3)),
+            kept.data_ptr() + 12 * n)
+
+
+def policy_loss_forward(logits, targets, old_logp, advantages, weights=None, ref_logp=None,
+                        clip_low=0.2, clip_high=0.2, kl_coef=0.0, scale=1.0, stream=None):
+    """(loss, logp, lse, dlogp): the clipped policy loss of the rows of `logits`, whose
+    tokens `targets` were sampled by a policy that gave them old_logp:
+        scale sum(weights (-min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+                           + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1)))
+    with ratio = exp(logp - old_logp). old_logp, advantages (A), weights and ref_logp are
+    float32 of the targets' shape; without weights a row's is 1, without ref_logp the
+    second term is left out. Rows of weight 0 or of a negative target count for nothing,
+    whatever they hold. For a mean give weights, or a scale, of 1 over the tokens that
+    count, of all ranks. dlogp is the loss's gradient by logp: token_logprobs_backward
+    makes the logits' of it."""
+    if stream is not None:
+        return _on(stream, logits.get_device(), policy_loss_forward, logits, targets, old_logp,
+                   advantages, weights, ref_logp, clip_low, clip_high, kl_coef, scale)
+    return _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, clip_high,
+                   kl_coef, scale, False, None)[:4]
+
+
+def policy_loss_gradient(logits, targets, old_logp, advantages, weights=None, ref_logp=None,
+                         clip_low=0.2, clip_high=0.2, kl_coef=0.0, scale=1.0, out=None,
+                         stream=None):
+    """(loss, logp, dlogits) of policy_loss_forward's loss and its gradient by the logits in
+    one pass over them: for a step that goes on with logits.backward(dlogits). `out`: a
+    tensor of the logits' shape and type for the gradient, logits themselves allowed."""
+    if stream is not None:
+        return _on(stream, logits.get_device(), policy_loss_gradient, logits, targets, old_logp,
+                   advantages, weights, ref_logp, clip_low, clip_high, kl_coef, scale, out)
+    kept = _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, clip_high,
+                   kl_coef, scale, True, out)
+    return kept[0], kept[1], kept[5]
+
+
+def _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale, gradient, out):
+    """(loss, logps, lse, dlogp, rest, dlogits or None)"""
+    cols, code, device, rows, xs = _check_logits(logits, targets)
+    if device != _current_device():
+        return _on_device(device, _preference, logits, targets, ref_logps, starts, beta,
+                          label_smoothing, scale, gradient, out)
+    if starts is not None:
+        if starts.dtype != torch.int64 or starts.dim() != 1 or starts.shape[0] < 3 or \
+                starts.shape[0] % 2 == 0 or not starts.is_contiguous() or \
+                starts.get_device() != device:
+            raise ValueError("starts must be a dense int64 vector of 2 pairs + 1, on the logits' device")
+        pairs = starts.shape[0] // 2
+    elif logits.dim() < 3 or logits.shape[0] < 2 or logits.shape[0] % 2:
+        raise ValueError("without starts, logits must be (2 pairs, tokens, vocabulary)")
+    else:
+        pairs = logits.shape[0] // 2
+    if ref_logps is not None and (ref_logps.dtype != _F32 or ref_logps.shape != (2, pairs) or
+                                  not ref_logps.is_contiguous() or ref_logps.get_device() != device):
+        raise ValueError("ref_logps must be dense float32 (2, pairs), on the logits' device")
+    dx, ds = _gradient_of(logits, out, device, cols) if gradient else (None, 0)
+    loss = torch.empty((), dtype=_F32, device=logits.device)
+    logps = torch.empty((2, pairs), dtype=_F32, device=logits.device)
+    n = (rows + 3) // 4 * 4
+    lse, dlogp, rest, at = _row_buffers(targets, rows, 16 * pairs)
+    rc = vr.lib().vrPreferenceLoss(logits.data_ptr(), targets.data_ptr(), _ptr(ref_logps),
+                                   _ptr(starts), loss.data_ptr(), logps.data_ptr(), at,
+                                   lse.data_ptr(), rest.data_ptr(), dlogp.data_ptr(), _ptr(dx),
+                                   pairs, rows, cols, xs, ds, beta, label_smoothing, scale, code,
+                                   at + 4 * n, 16 * pairs, _raw_stream(device))
+    if rc:
+        raise vr.VrError(rc, "vrPreferenceLoss")
+    if out is not None:
+        _written(out)
+    return loss, logps, lse, dlogp, rest, dx
+
+
+def preference_loss_forward(logits, targets, ref_logps=None, starts=None, beta=0.1,
+                            label_smoothing=0.0, scale=1.0, stream=None):
+    """(loss, logps, lse, dlogp): the loss of preferences between pairs of sequences by the
+    ratio of their probabilities under the policy to those under a reference,
+        h = beta ((logps - ref_logps)[0] - (logps - ref_logps)[1])
+        scale sum over pairs ((1 - label_smoothing) log(1 + exp(-h)) + label_smoothing log(1 + exp(h)))
+    with logps (2, pairs) the sums of the sequences' log probabilities, row 0 of the chosen
+    ones, row 1 of the rejected ones. The sequences are the rows of `logits` in that order:
+    (2 pairs, tokens, vocabulary), or packed with starts, int64, of 2 pairs + 1 rows where
+    sequences begin and end. Tokens of negative targets (prompts, padding) count for nothing.
+    ref_logps: float32 (2, pairs), None: zeros. dlogp is the loss's gradient by the tokens'
+    log probabilities: token_logprobs_backward makes the logits' of it."""
+    if stream is not None:
+        return _on(stream, logits.get_device(), preference_loss_forward, logits, targets, ref_logps,
+                   starts, beta, label_smoothing, scale)
+    return _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale, False,
+                       None)[:4]
+
+
+def preference_loss_gradient(logits, targets, ref_logps=None, starts=None, beta=0.1,
+                             label_smoothing=0.0, scale=1.0, out=None, stream=None):
+    """(loss, logps, dlogits) of preference_loss_forward's loss and its gradient by the
+    logits, for a step that goes on with logits.backward(dlogits). `out`: a tensor of the
+    logits' shape and type for the gradient, logits themselves allowed."""
+    if stream is not None:
+        return _on(stream, logits.get_device(), preference_loss_gradient, logits, targets, ref_logps,
+                   starts, beta, label_smoothing, scale, out)
+    kept = _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale, True, out)
+    return kept[0], kept[1], kept[5]
+
+
+class _TokenLogProbs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets):
+        logits, targets = _as_rows(logits), targets.contiguous()
+        logp, lse, rest = token_logprobs_forward(logits, targets, True)
+        ctx.save_for_backward(logits, targets, lse, rest)
+        return logp
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogp):
+        return token_logprobs_backward(dlogp.contiguous(), *ctx.saved_tensors), None
+
+
+class _Loss(torch.autograd.Function):
+    """A loss of rows of logits, of which forward keeps the gradient by each row's logp."""
+
+    @staticmethod
+    def forward(ctx, logits, targets, loss, *args):
+        logits, targets = _as_rows(logits), targets.contiguous()
+        value, logp, lse, dlogp, rest, _ = loss(logits, targets, *args, False, None)
+        ctx.save_for_backward(logits, targets, lse, dlogp, rest)
+        ctx.mark_non_differentiable(logp)
+        ctx.rest = len(args)
+        return value, logp
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gain, _):
+        logits, targets, lse, dlogp, rest = ctx.saved_tensors
+        d = token_logprobs_backward(dlogp, logits, targets, lse, rest, gain.contiguous())
+        return (d, None, None) + (None,) * ctx.rest
+
+
+def token_logprobs(logits, targets):
+    """The log probability of each row's target, float32, differentiable once with respect
+    to the logits; logits of layouts other than token_logprobs_forward's are copied first."""
+    return _TokenLogProbs.apply(logits, targets)
+
+
+def policy_loss(logits, targets, old_logp, advantages, weights=None, ref_logp=None, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, scale=1.0):
+    """(loss, logp) of policy_loss_forward, the loss differentiable once with respect to the
+    logits. It reads the logits forward and again backward; policy_loss_gradient does
+    both in one pass."""
+    return _Loss.apply(logits, targets, _policy, old_logp, advantages, weights, ref_logp,
+                       clip_low, clip_high, kl_coef, scale)
+
+
+def preference_loss(logits, targets, ref_logps=None, starts=None, beta=0.1, label_smoothing=0.0,
+                    scale=1.0):
+    """(loss, logps) of preference_loss_forward, the loss differentiable once with respect to
+    the logits."""
+    return _Loss.apply(logits, targets, _preference, ref_logps, starts, beta,
+                       label_smoothing, scale)
