@@ -48,12 +48,6 @@ __device__ __forceinline__ void each(F f) {
     each<N, I + 1>(f);
   }
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // The parameters of a thread's V columns from c0 on: packed as they are where
 // they have the rows' type, else as floats. `none` where the pointer is NULL.
 // Plain loads: the read-only path asks that nobody writes the parameters from the

@@ -37,8 +37,11 @@ struct LossArgs {
   // the gradient's kernel
   const float* dlogp;
   const float* gain;  // multiplies dlogp, or NULL
-  uint64_t slots;     // packs that a row can touch
+  uint64_t segments;  // blocks of a row
   bool alike;         // dx's rows lie as x's modulo 16 bytes
+  // the kernel that keeps a row on chip
+  int ctas;           // blocks of a row
+  uint32_t part;      // packs of a block
   // preferences
   const float* refSums;
   const int64_t* starts;
@@ -114,34 +117,58 @@ __device__ __forceinline__ double log_of(float s) {
 
 enum { LOGP = 0, POLICY = 1 };
 
-// What a row comes to whose exponentials sum to s over its largest element m. lse is that
-// element and a logarithm, and where the first is large (an offset of all logits, masks of
-// the lowest number) their rounded sum has lost the second: `rest` is what it lost, and
-// logp is made of the distance from the largest.
-template <int KIND>
-__device__ __forceinline__ void finish_row(const LossArgs& a, uint64_t row, float m, float s, double at) {
-  const double l = log_of(s), lp = (at - (double)m) - l;
-  a.logp[row] = (float)lp;
-  if (a.lse) {
-    const float lse = (float)((double)m + l);
-    a.lse[row] = lse;
-    if (a.rest) a.rest[row] = (float)(((double)m - (double)lse) + l);
+// What one thread loads of a row ahead of the row's sum.
+struct RowIn {
+  float at, old, advantage, weight, ref;  // at: the target's logit
+  template <int KIND, typename T>
+  __device__ __forceinline__ void load(const LossArgs& a, uint64_t row, const T* x, int64_t target) {
+    at = (uint64_t)target < a.cols ? to_f32(x[target]) : __int_as_float(0x7fffffff);
+    if constexpr (KIND == POLICY) {
+      old = a.old[row];
+      advantage = a.advantage[row];
+      weight = a.weight ? a.weight[row] : 1.f;
+      ref = a.ref ? a.ref[row] : 0.f;
+    }
   }
+};
+
+// What a row comes to whose exponentials sum to s over its largest element m: logp is
+// returned with the loss's derivative by it. lse is that element and a logarithm, and where
+// the first is large (an offset of all logits, masks of the lowest number) their rounded sum
+// has lost the second: `rest` is what it lost, and logp is made of the distance from the
+// largest. Of a cluster's blocks one writes.
+template <int KIND>
+__device__ __forceinline__ float2 finish_row(const LossArgs& a, uint64_t row, const RowIn& in, float m, float s,
+                                             bool write = true) {
+  const double l = log_of(s), lp = ((double)in.at - (double)m) - l;
+  float loss = 0.f, c = 0.f;
   if constexpr (KIND == POLICY) {
-    const float A = a.advantage[row], w = a.weight ? a.weight[row] : 1.f;
-    const double e = lp - (double)a.old[row];
-    float loss = 0.f, c = 0.f;
+    const float A = in.advantage;
+    const double e = lp - (double)in.old;
     if (A > 0.f && e > a.high) loss = -(a.most * A);
     else if (A < 0.f && e < a.low) loss = -(a.least * A);
     else if (A != 0.f) loss = c = -(expf((float)e) * A);
     if (a.ref) {
-      const float r = (float)((double)a.ref[row] - lp), x = expm1f(r);
+      const float r = (float)((double)in.ref - lp), x = expm1f(r);
       loss = fmaf(a.kl, x - r, loss);
       c = fmaf(-a.kl, x, c);
     }
-    a.rowLoss[row] = w * loss;
-    a.coef[row] = a.scale * w * c;
+    loss *= in.weight;
+    c *= a.scale * in.weight;
   }
+  if (write) {
+    a.logp[row] = (float)lp;
+    if (a.lse) {
+      const float lse = (float)((double)m + l);
+      a.lse[row] = lse;
+      if (a.rest) a.rest[row] = (float)(((double)m - (double)lse) + l);
+    }
+    if constexpr (KIND == POLICY) {
+      a.rowLoss[row] = loss;
+      a.coef[row] = c;
+    }
+  }
+  return make_float2((float)lp, c);
 }
 // A row that counts for nothing: its logits are not read.
 template <int KIND>
@@ -152,8 +179,8 @@ __device__ __forceinline__ void skip_row(const LossArgs& a, uint64_t row) {
   if constexpr (KIND == POLICY) a.rowLoss[row] = a.coef[row] = 0.f;
 }
 template <int KIND>
-__device__ __forceinline__ bool skipped(const LossArgs& a, uint64_t row) {
-  return a.target[row] < 0 || (KIND == POLICY && a.weight && a.weight[row] == 0.f);
+__device__ __forceinline__ bool skipped(const LossArgs& a, uint64_t row, int64_t target) {
+  return target < 0 || (KIND == POLICY && a.weight && a.weight[row] == 0.f);
 }
 
 // A row, cut at memory's 16-byte boundaries: `head` elements, whole packs, and the rest.
@@ -174,128 +201,278 @@ struct Cut {
   }
 };
 
-// A block for each row, read once.
+// The sums of a block's threads joined, in an order fixed by the lanes; the same in all.
+struct Joined {
+  float tops[16], sums[16];
+  __device__ __forceinline__ void warp(Online& o, int width) const {
+    float m = o.m;
+    for (int k = width / 2; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
+    float s = o.s * exp2_fast((o.m - m) * kLog2e);
+    for (int k = width / 2; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
+    o.m = m, o.s = s;
+  }
+  __device__ __forceinline__ void operator()(Online& o) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    warp(o, 32);
+    if (warps == 1) return;
+    if (lane == 0) tops[threadIdx.x >> 5] = o.m, sums[threadIdx.x >> 5] = o.s;
+    __syncthreads();
+    const bool in = (lane & 15) < warps;
+    o.m = in ? tops[lane & 15] : -FLT_MAX;
+    o.s = in ? sums[lane & 15] : 0.f;
+    warp(o, 16);
+  }
+};
+
+constexpr int kRowThreads = 256;
+
+// A block for each row, read once, the next packs on their way while the last are summed.
 template <typename T, int KIND>
-__global__ void __launch_bounds__(512) vrRowLogs(const __grid_constant__ LossArgs a) {
-  __shared__ float tops[16], sums[16];
+__global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constant__ LossArgs a) {
+  constexpr int U = 4;
+  __shared__ Joined joined;
   begin_kernel();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    if (skipped<KIND>(a, row)) {
+    const int64_t target = a.target[row];
+    if (skipped<KIND>(a, row, target)) {
       if (tid == 0) skip_row<KIND>(a, row);
       continue;
     }
     const T* x = static_cast<const T*>(a.x) + row * a.stride;
     const Cut<T> cut(x, a.cols);
+    RowIn in;
+    if (tid == 0) in.load<KIND>(a, row, x, target);
     Online o;
+    const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + tid;
+    int64_t left = (int64_t)cut.packs - tid;  // a pack of this thread is every threads-th
+    uint4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (k * threads < left) v[k] = p[k * threads];
     const int64_t edge = cut.edge(tid, a.cols);
     if (edge >= 0) o.add(to_f32(x[edge]));
-    const uint4* p = reinterpret_cast<const uint4*>(x + cut.head);
-    uint64_t i = tid;
-    for (; i + 3 * threads < cut.packs; i += 4 * threads) {
-      uint4 v[4];
+    while (left > 0) {
+      uint4 w[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = p[i + k * threads];
+      for (int k = 0; k < U; ++k)
+        if ((k + U) * threads < left) w[k] = p[(k + U) * threads];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o.add<T>(v[k]);
+      for (int k = 0; k < U; ++k)
+        if (k * threads < left) o.add<T>(v[k]);
+#pragma unroll
+      for (int k = 0; k < U; ++k) v[k] = w[k];
+      p += U * threads;
+      left -= U * threads;
     }
-    for (; i < cut.packs; i += threads) o.add<T>(p[i]);
-#pragma unroll
-    for (int k = 16; k; k >>= 1)
-      o.join(__shfl_xor_sync(~0u, o.m, k), __shfl_xor_sync(~0u, o.s, k));
-    if (threads > 32) {
-      if (lane == 0) tops[warp] = o.m, sums[warp] = o.s;
-      __syncthreads();
-      if (warp == 0) {
-        const bool in = lane < threads / 32;
-        o.m = in ? tops[lane] : -FLT_MAX;
-        o.s = in ? sums[lane] : 0.f;
-#pragma unroll
-        for (int k = 8; k; k >>= 1)
-          o.join(__shfl_xor_sync(~0u, o.m, k), __shfl_xor_sync(~0u, o.s, k));
-      }
-    }
-    if (tid == 0) {
-      const uint64_t t = (uint64_t)a.target[row];
-      finish_row<KIND>(a, row, o.m, o.s, t < a.cols ? (double)to_f32(x[t]) : (double)NAN);
-    }
+    joined(o);
+    if (tid == 0) finish_row<KIND>(a, row, in, o.m, o.s);
     if (threads > 32) __syncthreads();
   }
 }
 
-// dx from the rows' logarithms: a thread takes U packs of dx, as in dropout.
+// f exp(x - m - rest) of a pack's elements.
+template <typename T>
+__device__ __forceinline__ void scaled_exps(const uint4& v, float m, float rest, float f, float (&e)[kV<T>]) {
+  constexpr int V = kV<T>;
+  F2 x[V / 2];
+  unpack<T>(v, x);
+  const F2 less = f2(-m), less2 = f2(-rest), scale = f2(kLog2e);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    float p, q;
+    split((x[i] + less + less2) * scale, p, q);
+    split(f2(exp2_fast(p), exp2_fast(q)) * f2(f), e[2 * i], e[2 * i + 1]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_pack(T* p, const float (&e)[kV<T>], bool alike) {
+  constexpr int V = kV<T>;
+  if (alike) {
+    F2 f[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = f2(e[2 * i], e[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = pack<T>(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = from_f32<T>(e[i]);
+  }
+}
+
+// The logarithms and the gradient of a row in one pass over it: its packs are copied to
+// shared memory, each by the thread that reads it (no barrier between), summed as they
+// come, and read again there for the gradient. A row is a block's, or a cluster's, each
+// block with its part of it.
+template <typename T, int KIND, bool CLUSTER>
+__global__ void __launch_bounds__(kRowThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
+  constexpr int V = kV<T>, GROUPS = 4;
+  extern __shared__ uint4 packs[];
+  __shared__ Joined joined;
+  __shared__ float parts[2][8];  // the cluster's blocks'
+  __shared__ float4 result;
+  begin_kernel();
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int ctas = CLUSTER ? a.ctas : 1, rank = CLUSTER ? (int)cluster_rank() : 0;
+  if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  for (uint64_t row = blockIdx.x / ctas; row < a.rows; row += gridDim.x / ctas) {
+    const T* x = static_cast<const T*>(a.x) + row * a.stride;
+    T* dx = static_cast<T*>(a.dx) + row * a.dStride;
+    const int64_t target = a.target[row];
+    const Cut<T> cut(x, a.cols);
+    const int first = rank * (int)a.part, all = (int)cut.packs - first;
+    const int n = all < 0 ? 0 : all < (int)a.part ? all : (int)a.part;  // this block's packs
+    const int64_t edge = rank == 0 ? cut.edge(tid, a.cols) : -1;
+    T* const dp = dx + cut.head + (int64_t)first * V;
+    if (skipped<KIND>(a, row, target)) {
+      const float zero[V] = {};
+      for (int i = tid; i < n; i += threads) store_pack<T>(dp + (int64_t)i * V, zero, a.alike);
+      if (edge >= 0) dx[edge] = from_f32<T>(0.f);
+      if (tid == 0 && rank == 0) skip_row<KIND>(a, row);
+      continue;
+    }
+    const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + first;
+    const int each = ((n + threads - 1) / threads + GROUPS - 1) / GROUPS * threads;  // packs of a group
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(packs + i)),
+                     "l"(p + i)
+                     : "memory");
+      copies_commit();
+    }
+    RowIn in;
+    if (tid == 0) in.load<KIND>(a, row, x, target);
+    Online o;
+    float e = 0.f;
+    if (edge >= 0) {
+      e = to_f32(x[edge]);
+      o.add(e);
+    }
+    const auto sum = [&](int g) {
+      for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads) o.add<T>(packs[i]);
+    };
+    copies_wait<3>();
+    sum(0);
+    copies_wait<2>();
+    sum(1);
+    copies_wait<1>();
+    sum(2);
+    copies_wait<0>();
+    sum(3);
+    joined(o);
+    if (CLUSTER) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the others are there
+      if (tid < ctas) {
+        store_remote(&parts[0][rank], tid, o.m);
+        store_remote(&parts[1][rank], tid, o.s);
+      }
+      cluster_sync();
+      o = Online{};
+      for (int i = 0; i < ctas; ++i) o.join(parts[0][i], parts[1][i]);
+    }
+    if (tid == 0) {
+      const float2 r = finish_row<KIND>(a, row, in, o.m, o.s, rank == 0);
+      result = make_float4(r.x, r.y, -r.y / o.s, 0.f);
+    }
+    __syncthreads();
+    const float lp = result.x, c = result.y, f = result.z;
+    // The target's element is c (1 - p) without the difference of two numbers near 1. Of a
+    // target that is none c is NaN.
+    const bool none = c == 0.f;
+    const int64_t t = target - cut.head - (int64_t)first * V;
+    const int targetPack = t >= 0 && t < (int64_t)n * V ? (int)(t / V) : -1;
+    for (int i = tid; i < n; i += threads) {
+      float d[V];
+      scaled_exps<T>(packs[i], o.m, 0.f, f, d);
+      if (i == targetPack) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (j == (int)(t % V)) d[j] = -c * expm1f(lp);
+      }
+      if (none) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[j] = 0.f;
+      }
+      store_pack<T>(dp + (int64_t)i * V, d, a.alike);
+    }
+    if (edge >= 0)
+      dx[edge] = from_f32<T>(none             ? 0.f
+                             : edge == target ? -c * expm1f(lp)
+                                              : f * exp2_fast((e - o.m) * kLog2e));
+    if (CLUSTER) break;  // one row a cluster
+    __syncthreads();
+  }
+}
+
+// dx from the rows' logarithms, read by an earlier kernel: a block takes some rows' parts,
+// from the last row on, which that kernel read last.
 constexpr int kGradThreads = 256;
 template <typename T, int U>
 __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant__ LossArgs a) {
   constexpr int V = kV<T>;
   begin_kernel();
-  const uint64_t first = (uint64_t)blockIdx.x * (kGradThreads * U) + threadIdx.x;
-  const uint64_t all = a.rows * a.slots;
-  const float gain = a.gain ? *a.gain : 1.f;
-  const T* x[U];
-  T* dx[U];
-  int64_t col[U], target[U];
-  float c[U], lse[U], rest[U];
-  bool some[U], whole[U];
-  uint4 v[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const uint64_t slot = first + u * kGradThreads;
-    some[u] = whole[u] = false;
-    if (slot >= all) continue;
-    const uint64_t row = all >> 32 ? slot / a.slots : (uint32_t)slot / (uint32_t)a.slots;
-    T* d0 = static_cast<T*>(a.dx) + row * a.dStride;
-    col[u] = (int64_t)((slot - row * a.slots) * V) - (int64_t)(((uintptr_t)d0 & 15) / sizeof(T));
-    dx[u] = d0 + col[u];
-    x[u] = static_cast<const T*>(a.x) + row * a.stride + col[u];
-    some[u] = col[u] < (int64_t)a.cols;
-    whole[u] = col[u] >= 0 && col[u] + V <= (int64_t)a.cols;
-    target[u] = a.target[row];
-    c[u] = target[u] < 0 ? 0.f : a.dlogp[row];
-    if (c[u] != 0.f) c[u] *= gain;  // a row of 0 stays one, whatever it holds and the gain is
-    lse[u] = a.lse[row];
-    rest[u] = a.rest ? a.rest[row] : 0.f;
-    if (whole[u] && c[u] != 0.f) {
-      if (a.alike) {
-        v[u] = *reinterpret_cast<const uint4*>(x[u]);
-      } else {
-        T e[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = x[u][i];
-        memcpy(&v[u], e, 16);
-      }
+  const uint64_t line = blockIdx.x / a.segments;  // of rows
+  const uint64_t back = line * blockDim.y + threadIdx.y;
+  if (back >= a.rows) return;
+  const uint64_t row = a.rows - 1 - back;
+  const T* x = static_cast<const T*>(a.x) + row * a.stride;
+  T* dx = static_cast<T*>(a.dx) + row * a.dStride;
+  const int64_t target = a.target[row];
+  float c = target < 0 ? 0.f : a.dlogp[row];
+  if (c != 0.f && a.gain) c *= *a.gain;  // a row of 0 stays one, whatever the gain is
+  if (target >= (int64_t)a.cols && c != 0.f) c = __int_as_float(0x7fffffff);
+  const float lse = a.lse[row], rest = a.rest ? a.rest[row] : 0.f;
+  const Cut<T> cut(x, a.cols);
+  const uint64_t segment = blockIdx.x - line * a.segments;
+  const bool none = c == 0.f;
+  if (segment == 0) {
+    const int64_t edge = cut.edge(threadIdx.x, a.cols);
+    if (edge >= 0) {
+      const float d = none ? 0.f : (to_f32(x[edge]) - lse) - rest;
+      dx[edge] = from_f32<T>(none ? 0.f : edge == target ? -c * expm1f(d) : -c * exp2_fast(d * kLog2e));
     }
   }
+  const int threads = blockDim.x;
+  const uint64_t first = segment * a.part + threadIdx.x;
+  const uint64_t end = first - threadIdx.x + a.part < cut.packs ? first - threadIdx.x + a.part : cut.packs;
+  const uint4* p = reinterpret_cast<const uint4*>(x + cut.head);
+  T* const dp = dx + cut.head;
+  if (none) {
+    const float zero[V] = {};
+    for (uint64_t i = first; i < end; i += threads) store_pack<T>(dp + i * V, zero, a.alike);
+    return;
+  }
+  uint4 v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (!some[u]) continue;
-    const int64_t t = target[u] - col[u];
-    // At the target 1 - p without the difference of two numbers near 1.
-    auto one = [&](float e, int i) {
-      if (c[u] == 0.f) return 0.f;
-      if (target[u] >= (int64_t)a.cols) return __int_as_float(0x7fffffff);
-      const float d = (e - lse[u]) - rest[u];
-      return i == t ? -c[u] * expm1f(d) : -c[u] * exp2_fast(d * kLog2e);
-    };
-    if (whole[u]) {
-      float e[V];
-      F2 f[V / 2];
-      if (c[u] != 0.f) {
+  for (int u = 0; u < U; ++u)
+    if (first + u * threads < end) v[u] = p[first + u * threads];
+  for (uint64_t i0 = first; i0 < end; i0 += U * threads) {
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + (U + u) * threads < end) w[u] = p[i0 + (U + u) * threads];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint64_t i = i0 + u * threads;
+      if (i >= end) break;
+      float d[V];
+      scaled_exps<T>(v[u], lse, rest, -c, d);
+      const int64_t t = target - cut.head - (int64_t)(i * V);
+      if (t >= 0 && t < V) {
+        F2 f[V / 2];
+        float e[V];
         unpack<T>(v[u], f);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) split(f[i], e[2 * i], e[2 * i + 1]);
-      }
+        for (int j = 0; j < V / 2; ++j) split(f[j], e[2 * j], e[2 * j + 1]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) e[i] = one(e[i], i);
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) f[i] = f2(e[2 * i], e[2 * i + 1]);
-      *reinterpret_cast<uint4*>(dx[u]) = pack<T>(f);
-    } else {
-      for (int i = 0; i < V; ++i) {
-        if (col[u] + i < 0 || col[u] + i >= (int64_t)a.cols) continue;
-        dx[u][i] = from_f32<T>(one(c[u] == 0.f ? 0.f : to_f32(x[u][i]), i));
+        for (int j = 0; j < V; ++j)
+          if (j == (int)t) d[j] = -c * expm1f((e[j] - lse) - rest);
       }
+      store_pack<T>(dp + i * V, d, a.alike);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = w[u];
   }
 }
 
@@ -384,27 +561,63 @@ vrResult_t dispatch(vrDataType_t t, F f) {
 
 template <typename T, int KIND>
 vrResult_t rowLogs(LossArgs& a, cudaStream_t st) {
-  // Eight packs a thread, up to 512 threads.
+  // Eight packs a thread, up to 256 threads.
   uint64_t threads = (a.cols / kV<T> / 8 + 31) / 32 * 32;
-  threads = threads < 32 ? 32 : threads > 512 ? 512 : threads;
+  threads = threads < 32 ? 32 : threads > kRowThreads ? kRowThreads : threads;
   const uint64_t most = 1u << 20;
   return launch((const void*)&vrRowLogs<T, KIND>, dim3((unsigned)(a.rows < most ? a.rows : most)),
                 dim3((unsigned)threads), 0, st, a);
 }
 
 template <typename T>
-vrResult_t rowGrads(LossArgs& a, cudaStream_t st) {
-  constexpr uint64_t V = kV<T>;
-  a.slots = (a.cols + 2 * (V - 1)) / V;
+void alikeRows(LossArgs& a) {
   a.alike = (((uintptr_t)a.x - (uintptr_t)a.dx) & 15) == 0 &&
             (a.rows == 1 || (((a.stride - a.dStride) * sizeof(T)) & 15) == 0);
-  const uint64_t slots = a.rows * a.slots;
-  const bool many = slots >= (uint64_t)kSMs * 8 * kGradThreads * 2;
-  const uint64_t each = many ? 4 * kGradThreads : kGradThreads;
-  const void* k = many ? (const void*)&vrRowGrads<T, 4> : (const void*)&vrRowGrads<T, 1>;
-  const uint64_t blocks = (slots + each - 1) / each;
+}
+
+template <typename T>
+vrResult_t rowGrads(LossArgs& a, cudaStream_t st) {
+  alikeRows<T>(a);
+  const uint64_t packs = a.cols / kV<T> ? a.cols / kV<T> : 1;
+  // A row's threads, a power of two, up to a block; parts of 4096 packs, of 1024 where those
+  // are few.
+  unsigned x = 32;
+  while (x < kGradThreads && x * 4 < packs) x *= 2;
+  const unsigned y = kGradThreads / x;
+  a.part = a.rows * packs >= (uint64_t)kSMs * 16 * 4096 ? 4096 : 1024;
+  a.segments = (packs + a.part - 1) / a.part;
+  const uint64_t blocks = (a.rows + y - 1) / y * a.segments;
   if (blocks > 0x7fffffffu) return vrInvalidArgument;
-  return launch(k, dim3((unsigned)blocks), dim3(kGradThreads), 0, st, a);
+  return launch((const void*)&vrRowGrads<T, 4>, dim3((unsigned)blocks), dim3(x, y), 0, st, a);
+}
+
+// Logarithms and gradient in one pass; false if a row is too large for a cluster.
+constexpr size_t kMostShared = 200 * 1024;
+template <typename T, int KIND>
+bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
+  alikeRows<T>(a);
+  const uint64_t packs = a.cols / kV<T> ? a.cols / kV<T> : 1;
+  constexpr uint64_t kBest = 72 * 1024 / 16, kLargest = kMostShared / 16;
+  int ctas = 1;
+  while (ctas < 8 && (packs + ctas - 1) / ctas > kBest) ctas *= 2;
+  // Few rows are spread over more SMs, in parts of 8 KB at least.
+  while (ctas < 8 && a.rows * ctas < 2 * kSMs && packs / ctas >= 1024) ctas *= 2;
+  const uint64_t part = (packs + ctas - 1) / ctas;
+  if (part > kLargest || a.rows * ctas > 0x7fffffffu) return false;
+  a.ctas = ctas;
+  a.part = (uint32_t)part;
+  uint64_t threads = (part / 8 + 31) / 32 * 32;
+  threads = threads < 32 ? 32 : threads > kRowThreads ? kRowThreads : threads;
+  const uint64_t rowsEach = ctas > 1 ? 1 : (1024 + part - 1) / part;  // 16 KB a block
+  const uint64_t blocks = (a.rows + rowsEach - 1) / rowsEach * ctas;
+  const void* k = ctas > 1 ? (const void*)&vrRowLossGrads<T, KIND, true> : (const void*)&vrRowLossGrads<T, KIND, false>;
+  if (!setOnce(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostShared) ||
+      !setOnce(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) {
+    *r = vrCudaError;
+    return true;
+  }
+  *r = launch(k, dim3((unsigned)blocks), dim3((unsigned)threads), part * 16, st, a, ctas);
+  return true;
 }
 
 bool sizesOk(uint64_t rows, uint64_t cols) { return cols >= 1 && cols <= kMost && rows <= kMost / cols; }
@@ -502,8 +715,11 @@ extern "C" VR_API vrResult_t vrPolicyLoss(const void* logits, const int64_t* tar
     a.low = clipLow < 1.0 ? log1p(-clipLow) : -INFINITY, a.high = log1p(clipHigh);
     a.kl = klCoef;
     const vrResult_t r = dispatch(dtype, [&](auto t) {
-      const vrResult_t rc = rowLogs<decltype(t), POLICY>(a, st);
-      return rc == vrSuccess && dlogits ? rowGrads<decltype(t)>(a, st) : rc;
+      using T = decltype(t);
+      vrResult_t rc;
+      if (dlogits && rowLossGrads<T, POLICY>(a, st, &rc)) return rc;
+      rc = rowLogs<T, POLICY>(a, st);
+      return rc == vrSuccess && dlogits ? rowGrads<T>(a, st) : rc;
     });
     if (r != vrSuccess) return r;
   }

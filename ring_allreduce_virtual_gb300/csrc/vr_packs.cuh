@@ -36,6 +36,11 @@ __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
   F2 r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -99,6 +104,14 @@ __device__ __forceinline__ uint4 pack(const F2* f) {
     v = make_uint4(round2<T>(f[0]), round2<T>(f[1]), round2<T>(f[2]), round2<T>(f[3]));
   }
   return v;
+}
+
+// Copies to shared memory on their way (cp.async): a group of them, and the wait for all
+// but the last N groups.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -172,7 +172,7 @@ def check_policy(x, t, old, adv, w, ref, dlogp, dlogits, loss, logp, kl=KL):
     if dlogits is not None:
         lim = torch.where(c != 0, off / c.abs().clamp(min=1e-300), 0.0)
         check_grad(dlogits, x, t, c, want, far, lim + 4 * U)
-    return c
+    return off
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
@@ -181,7 +181,7 @@ def test_policy(rows, cols, dtype):
     x, t, g = make(rows * cols, rows, cols, dtype)
     args = policy_inputs(x, t, g)
     loss, logp, dlogits = training.policy_loss_gradient(x, t, *args, LOW, HIGH, KL, SCALE)
-    check_policy(x, t, *args, None, None, loss, logp)
+    off = check_policy(x, t, *args, None, None, loss, logp)
     l2, lp2, lse, dlogp = training.policy_loss_forward(x, t, *args, LOW, HIGH, KL, SCALE)
     check_policy(x, t, *args, dlogp, None, l2, lp2)
     used = args[2] != 0
@@ -189,7 +189,8 @@ def test_policy(rows, cols, dtype):
     # the gradient, from this row's derivative
     want = torch.logsumexp(x.double(), 1)
     far = lse_far(x, want)
-    check_grad(dlogits, x, t, dlogp.double(), want, far, 64 * E2)
+    # both calls' derivatives are within `off` of the exact one
+    check_grad(dlogits, x, t, dlogp.double(), want, far, torch.where(used, 2 * off / dlogp.double().abs().clamp(min=1e-300), 0.0) + 8 * U)
     z = x.clone()
     got = training.policy_loss_gradient(z, t, *args, LOW, HIGH, KL, SCALE, out=z)
     assert got[2] is z and same(z, dlogits) and same(got[0], loss) and same(got[1], logp)
@@ -475,10 +476,13 @@ def test_more_than_two_to_the_31_elements():
     t = torch.zeros(rows, device="cuda", dtype=torch.int64)
     t[-3:] = t1
     logp, lse = training.token_logprobs_forward(x, t)
-    assert same(logp[-3:], training.token_logprobs_forward(last, t1)[0])
+    # few rows are summed by more threads, in another order: by lse_far's roundings apart
+    assert (logp[-3:] - training.token_logprobs_forward(last, t1)[0]).abs().max() <= 1e-5
     assert (logp[:-3] + math.log(cols)).abs().max() <= 1e-5
     w = torch.zeros(rows, device="cuda")
     w[-3:] = 1.0
     loss, lp, dx = training.policy_loss_gradient(x, t, logp, torch.ones(rows, device="cuda"), w, out=x)
     alone = training.policy_loss_gradient(last, t1, logp[-3:].clone(), torch.ones(3, device="cuda"))
-    assert same(dx[-3:], alone[2]) and bool((dx[:-3] == 0).all()) and same(loss, alone[0])
+    near = alone[2].float()
+    assert ((dx[-3:].float() - near).abs() <= 2 * UT[x.dtype] * near.abs()).all() and bool((dx[:-3] == 0).all())
+    assert abs(float(loss - alone[0])) <= 1e-4
