@@ -23,44 +23,65 @@ struct DropArgs {
   void* y;
   uint64_t rows, cols, xStride, rStride, yStride;
   const uint64_t* seedDevice;  // the seed where it is not NULL
-  uint64_t seed, offset;
-  uint64_t slots;  // packs that a row can touch
+  uint32_t keys[20];           // of the ten rounds, without it
+  uint64_t offset;
+  uint64_t slots;  // packs that a row can touch; units
+  uint64_t head;   // elements before the first unit
   uint32_t least;  // upper halves from here on are kept
+  uint32_t below;  // least << 16, less one
   uint32_t tie;    // the one that leaves it to the lower half; above 65535: none does
   uint32_t lower;  // which is kept from here on
+  uint32_t ties;   // the tying half twice
+  uint32_t c65536, one;  // constants that keep products products
   float scale;
   bool xAlike, rAlike;  // x's and the residual's rows lie as y's modulo 16 bytes
 };
 
+
 constexpr int kThreads = 256;
 constexpr uint64_t kBlocks = (1ull << 61) - 1;  // numbers wrap at 2^64
 
-// The block of counter (n, stream) under `seed`.
-__device__ __forceinline__ void philox(uint64_t n, uint32_t stream, uint64_t seed, uint32_t* w) {
+// The keys of the rounds: from the host, constants of the launch that the instructions
+// take as they are, or with a seed on the device from that one (18 additions a block).
+template <bool DEVICE>
+struct Keys {
+  uint32_t k0, k1;
+  __device__ __forceinline__ Keys(const DropArgs& a) {
+    if (DEVICE) k0 = (uint32_t)*a.seedDevice, k1 = (uint32_t)(*a.seedDevice >> 32);
+  }
+  __device__ __forceinline__ uint32_t first(const DropArgs& a, int r) const {
+    return DEVICE ? k0 + r * 0x9E3779B9u : a.keys[2 * r];
+  }
+  __device__ __forceinline__ uint32_t second(const DropArgs& a, int r) const {
+    return DEVICE ? k1 + r * 0xBB67AE85u : a.keys[2 * r + 1];
+  }
+};
+
+// The block of counter (n, stream).
+template <bool DEVICE>
+__device__ __forceinline__ void philox(const DropArgs& a, const Keys<DEVICE>& keys, uint64_t n, uint32_t stream,
+                                       uint32_t* w) {
   uint32_t c0 = (uint32_t)n, c1 = (uint32_t)(n >> 32), c2 = stream, c3 = 0;
-  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-    c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
-    c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+    const uint64_t p = (uint64_t)0xD2511F53u * c0, q = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(q >> 32) ^ c1 ^ keys.first(a, r);
+    c1 = (uint32_t)q;
+    c2 = (uint32_t)(p >> 32) ^ c3 ^ keys.second(a, r);
+    c3 = (uint32_t)p;
   }
   w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
 }
 
 // The halfwords of the V elements from number n on, two in a word.
-template <int V>
-__device__ __forceinline__ void halfwords(uint64_t n, uint32_t stream, uint64_t seed,
-                                          uint32_t (&h)[V / 2]) {
+template <int V, bool DEVICE>
+__device__ __forceinline__ void halfwords(const DropArgs& a, const Keys<DEVICE>& keys, uint64_t n,
+                                          uint32_t stream, uint32_t (&h)[V / 2]) {
   uint32_t w[8];
   const uint32_t first = (uint32_t)n & 7;
-  philox(n >> 3, stream, seed, w);
+  philox(a, keys, n >> 3, stream, w);
   w[4] = w[5] = w[6] = w[7] = 0;
-  if (first + V > 8) philox(((n >> 3) + 1) & kBlocks, stream, seed, w + 4);
+  if (first + V > 8) philox(a, keys, ((n >> 3) + 1) & kBlocks, stream, w + 4);
   if (first) {
 #pragma unroll
     for (int i = 0; i < 7; ++i) w[i] = first & 2 ? w[i + 1] : w[i];
@@ -74,10 +95,10 @@ __device__ __forceinline__ void halfwords(uint64_t n, uint32_t stream, uint64_t 
 }
 
 // Which of the V elements from number n on stay: a bit for each.
-template <int V>
-__device__ __forceinline__ uint32_t kept(const DropArgs& a, uint64_t n, uint64_t seed) {
+template <int V, bool DEVICE>
+__device__ __forceinline__ uint32_t kept(const DropArgs& a, const Keys<DEVICE>& keys, uint64_t n) {
   uint32_t h[V / 2], keep = 0, ties = 0;
-  halfwords<V>(n, 0, seed, h);
+  halfwords<V>(a, keys, n, 0, h);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const uint32_t u = i & 1 ? h[i / 2] >> 16 : h[i / 2] & 0xffff;
@@ -85,7 +106,7 @@ __device__ __forceinline__ uint32_t kept(const DropArgs& a, uint64_t n, uint64_t
     ties |= (u == a.tie ? 1u : 0u) << i;
   }
   if (ties) {
-    halfwords<V>(n, 1, seed, h);
+    halfwords<V>(a, keys, n, 1, h);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t u = i & 1 ? h[i / 2] >> 16 : h[i / 2] & 0xffff;
@@ -95,14 +116,167 @@ __device__ __forceinline__ uint32_t kept(const DropArgs& a, uint64_t n, uint64_t
   return keep;
 }
 
-// A thread takes U packs of y, cut at memory's 16-byte boundaries; a row's first and
-// last may be parts. Bound by HBM: 2 or 3 tensors, and about 90 instructions for 32 or
-// 48 bytes of them.
-template <typename T, int U, bool ADD>
+// An element that is kept: one rounding in 32 bits, wherever it lies.
+template <bool ADD>
+__device__ __forceinline__ float apply(float x, float scale, float add) {
+  return ADD ? __fmaf_rn(x, scale, add) : __fmul_rn(x, scale);
+}
+
+// One element's fate.
+template <bool DEVICE>
+__device__ __forceinline__ bool keeps(const DropArgs& a, const Keys<DEVICE>& keys, uint64_t n) {
+  uint32_t w[4];
+  const auto half = [&](uint32_t stream) {
+    philox(a, keys, n >> 3, stream, w);
+    const uint32_t v = n & 4 ? (n & 2 ? w[3] : w[2]) : (n & 2 ? w[1] : w[0]);
+    return n & 1 ? v >> 16 : v & 0xffff;
+  };
+  const uint32_t u = half(0);
+  return u == a.tie ? half(1) >= a.lower : u >= a.least;
+}
+
+// The four words of a unit that starts FW words and `first` mod 2 halfwords behind the start
+// of this lane's block, from that and the next lane's.
+template <int FW>
+__device__ __forceinline__ void shifted(const uint32_t (&now)[4], const uint32_t (&next)[4], uint32_t first,
+                                        uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+  uint32_t all[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    all[i] = i + FW < 4 ? now[(i + FW) & 3]
+                        : __shfl_sync(~0u, lane == 0 ? next[(i + FW) & 3] : now[(i + FW) & 3], (lane + 1) & 31);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(all[i], all[i + 1], (first & 1) * 16);
+}
+
+// A pack's elements. The kernel's time is that of the pipe that compares, selects and
+// shifts: what can be a product here is one.
+template <typename T>
+__device__ __forceinline__ void floats(const uint4& v, uint32_t c65536, float (&e)[kV<T>]) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[2 * i] = __uint_as_float(w[i] * c65536);
+      e[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    F2 f[kV<T> / 2];
+    unpack<T>(v, f);
+#pragma unroll
+    for (int i = 0; i < kV<T> / 2; ++i) split(f[i], e[2 * i], e[2 * i + 1]);
+  }
+}
+
+// h > below ? x scale + add : add. Not a product with 0: x may be infinite.
+template <bool ADD>
+__device__ __forceinline__ float if_above(uint32_t h, uint32_t below, float x, float scale, float add) {
+  float y = add;
+  if (ADD)
+    asm("{\n.reg .pred p;\nsetp.gt.u32 p, %1, %2;\n@p fma.rn.f32 %0, %3, %4, %0;\n}"
+        : "+f"(y) : "r"(h), "r"(below), "f"(x), "f"(scale));
+  else
+    asm("{\n.reg .pred p;\nsetp.gt.u32 p, %1, %2;\n@p mul.rn.f32 %0, %3, %4;\n}"
+        : "+f"(y) : "r"(h), "r"(below), "f"(x), "f"(scale));
+  return y;
+}
+
+// Tensors without gaps that lie alike: a warp takes U x 32 units of 8 elements, a lane
+// every 32nd. Where the units' numbers start at a multiple of 8, a unit's randomness is one
+// block of the generator; else (SHIFTED) parts of two, and a lane takes the second from
+// the next lane, so that U + 1 blocks serve U units. Bound by HBM, with 100 instructions
+// for 32 or 48 bytes.
+template <typename T, int U, bool ADD, bool SHIFTED, bool DEVICE>
+__global__ void __launch_bounds__(kThreads, 3) vrDropFlat(const __grid_constant__ DropArgs a) {
+  constexpr int N = 8 * (int)sizeof(T) / 16;  // packs of a unit
+  constexpr int V = kV<T>;
+  begin_kernel();
+  const Keys<DEVICE> keys(a);
+  const int lane = threadIdx.x & 31;
+  const T* x = static_cast<const T*>(a.x);
+  const T* r = static_cast<const T*>(a.residual);
+  T* y = static_cast<T*>(a.y);
+  if (blockIdx.x == 0 && threadIdx.x < 16) {  // what lies before the first unit and after the last
+    const uint64_t i = threadIdx.x < 8 ? threadIdx.x : a.head + 8 * a.slots + (threadIdx.x - 8);
+    if (threadIdx.x < 8 ? i < a.head : i < a.cols) {
+      const float add = ADD ? to_f32(r[i]) : 0.f;
+      y[i] = from_f32<T>(keeps(a, keys, a.offset + i) ? apply<ADD>(to_f32(x[i]), a.scale, add) : add);
+    }
+  }
+  const uint64_t unit0 = ((uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * (U * 32) + lane;
+  x += a.head + unit0 * 8;
+  y += a.head + unit0 * 8;
+  if (ADD) r += a.head + unit0 * 8;
+  uint4 vx[U][N], vr[U][N];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (unit0 + u * 32 < a.slots) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        vx[u][k] = reinterpret_cast<const uint4*>(x + u * 256)[k];
+        if (ADD) vr[u][k] = reinterpret_cast<const uint4*>(r + u * 256)[k];
+      }
+    }
+  const uint64_t n0 = a.offset + a.head + unit0 * 8;
+  const uint32_t first = SHIFTED ? (uint32_t)n0 & 7 : 0;  // the same in all threads
+  uint32_t now[4], next[4];
+  if (SHIFTED) philox(a, keys, n0 >> 3, 0, now);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t w[4];
+    if (SHIFTED) {
+      philox(a, keys, ((n0 >> 3) + (u + 1) * 32) & kBlocks, 0, next);
+      switch (first >> 1) {
+        case 0: shifted<0>(now, next, first, w); break;
+        case 1: shifted<1>(now, next, first, w); break;
+        case 2: shifted<2>(now, next, first, w); break;
+        default: shifted<3>(now, next, first, w);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) now[i] = next[i];
+    } else {
+      philox(a, keys, ((n0 >> 3) + u * 32) & kBlocks, 0, w);
+    }
+    // Upper halves are compared where they stand in a word, or multiplied there; ties are
+    // halfwords that are 0 after an exclusive or.
+    uint32_t h[8], below = a.below, ties = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[2 * i] = w[i] * a.c65536;
+      h[2 * i + 1] = w[i];
+      const uint32_t z = w[i] ^ a.ties;
+      ties |= (z * a.one + 0xfffeffffu) & ~z;
+    }
+    if (((ties & 0x80008000u) && a.lower) || a.least == 0) {  // one unit of 8192; or p == 0
+      below = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = a.least == 0 || keeps(a, keys, n0 + u * 256 + i);
+    }
+    if (unit0 + u * 32 < a.slots) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        F2 f[V / 2];
+        float e[V], add[V];
+        floats<T>(vx[u][k], a.c65536, e);
+        if (ADD) floats<T>(vr[u][k], a.c65536, add);
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = if_above<ADD>(h[k * V + i], below, e[i], a.scale, ADD ? add[i] : 0.f);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) f[i] = f2(e[2 * i], e[2 * i + 1]);
+        reinterpret_cast<uint4*>(y + u * 256)[k] = pack<T>(f);
+      }
+    }
+  }
+}
+
+// Rows with other elements between them, or tensors that do not lie alike: a thread takes U
+// packs of y, cut at memory's 16-byte boundaries; a row's first and last may be parts.
+template <typename T, int U, bool ADD, bool DEVICE>
 __global__ void __launch_bounds__(kThreads) vrDropKernel(const __grid_constant__ DropArgs a) {
   constexpr int V = kV<T>;
   begin_kernel();
-  const uint64_t seed = a.seedDevice ? *a.seedDevice : a.seed;
+  const Keys<DEVICE> keys(a);
   const uint64_t first = (uint64_t)blockIdx.x * (kThreads * U) + threadIdx.x;
   const uint64_t all = a.rows * a.slots;
   const T* x[U];
@@ -147,32 +321,31 @@ __global__ void __launch_bounds__(kThreads) vrDropKernel(const __grid_constant__
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (!some[u]) continue;
-    const uint32_t keep = kept<V>(a, n[u], seed);
+    const uint32_t keep = kept<V>(a, keys, n[u]);
     if (whole[u]) {
-      F2 f[V / 2], add[V / 2];
-      unpack<T>(vx[u], f);
-      if (ADD) unpack<T>(vr[u], add);
+      F2 f[V / 2];
+      float e[V], add[V];
+      floats<T>(vx[u], a.c65536, e);
+      if (ADD) floats<T>(vr[u], a.c65536, add);
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        float p, q;
-        split(f[i] * f2(a.scale), p, q);  // selected, not multiplied by 0: x may be infinite
-        f[i] = f2(keep >> (2 * i) & 1 ? p : 0.f, keep >> (2 * i + 1) & 1 ? q : 0.f);
-        if (ADD) f[i] = f[i] + add[i];
+      for (int i = 0; i < V; ++i) {
+        const float r = ADD ? add[i] : 0.f;
+        e[i] = keep >> i & 1 ? apply<ADD>(e[i], a.scale, r) : r;
       }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) f[i] = f2(e[2 * i], e[2 * i + 1]);
       *reinterpret_cast<uint4*>(y[u]) = pack<T>(f);
     } else {
       for (int i = 0; i < V; ++i) {
         if (col[u] + i < 0 || col[u] + i >= (int64_t)a.cols) continue;
-        // two roundings, as in whole packs: no element depends on how its row lies
-        float f = keep >> i & 1 ? __fmul_rn(to_f32(x[u][i]), a.scale) : 0.f;
-        if (ADD) f = __fadd_rn(f, to_f32(r[u][i]));
-        y[u][i] = from_f32<T>(f);
+        const float add = ADD ? to_f32(r[u][i]) : 0.f;
+        y[u][i] = from_f32<T>(keep >> i & 1 ? apply<ADD>(to_f32(x[u][i]), a.scale, add) : add);
       }
     }
   }
 }
 
-template <typename T, bool ADD>
+template <typename T, bool ADD, bool DEVICE>
 vrResult_t run(DropArgs& a, cudaStream_t st) {
   constexpr uint64_t V = kV<T>;
   // As one row where nothing lies between rows.
@@ -180,20 +353,35 @@ vrResult_t run(DropArgs& a, cudaStream_t st) {
     a.cols *= a.rows;
     a.rows = 1;
   }
-  a.slots = (a.cols + 2 * (V - 1)) / V;
   const auto alike = [&](const void* p, uint64_t stride) {
     return (((uintptr_t)p - (uintptr_t)a.y) & 15) == 0 &&
            (a.rows == 1 || (((stride - a.yStride) * sizeof(T)) & 15) == 0);
   };
   a.xAlike = alike(a.x, a.xStride);
   a.rAlike = ADD && alike(a.residual, a.rStride);
-  const uint64_t slots = a.rows * a.slots;
-  // Four packs a thread, all loaded before the first is computed, where they fill the
-  // GPU at least twice; else one, on more SMs.
-  const bool many = slots >= (uint64_t)kSMs * 8 * kThreads * 2;
-  const uint64_t each = many ? 4 * kThreads : kThreads;
-  const void* k = many ? (const void*)&vrDropKernel<T, 4, ADD> : (const void*)&vrDropKernel<T, 1, ADD>;
-  const uint64_t blocks = (slots + each - 1) / each;
+  const void* k;
+  uint64_t blocks;
+  if (a.rows == 1 && a.xAlike && (!ADD || a.rAlike)) {
+    a.head = ((16 - ((uintptr_t)a.x & 15)) & 15) / sizeof(T);
+    if (a.head > a.cols) a.head = a.cols;
+    a.slots = (a.cols - a.head) / 8;
+    const bool shifted = (a.offset + a.head) % 8 != 0;
+    // Four units a thread, all loaded before the first is computed, where they fill the GPU
+    // at least twice; else one, on more SMs.
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    const bool many = a.slots >= (uint64_t)kSMs * 8 * kThreads * 2;
+    const uint64_t each = (many ? U : 1) * kThreads;
+    blocks = (a.slots + each - 1) / each;
+    if (!blocks) blocks = 1;
+    k = many ? (shifted ? (const void*)&vrDropFlat<T, U, ADD, true, DEVICE>
+                        : (const void*)&vrDropFlat<T, U, ADD, false, DEVICE>)
+             : (shifted ? (const void*)&vrDropFlat<T, 1, ADD, true, DEVICE>
+                        : (const void*)&vrDropFlat<T, 1, ADD, false, DEVICE>);
+  } else {
+    a.slots = (a.cols + 2 * (V - 1)) / V;
+    blocks = (a.rows * a.slots + 2 * kThreads - 1) / (2 * kThreads);
+    k = (const void*)&vrDropKernel<T, 2, ADD, DEVICE>;
+  }
   if (blocks > 0x7fffffffu) return vrInvalidArgument;
   return launch(k, dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
 }
@@ -226,13 +414,18 @@ extern "C" VR_API vrResult_t vrDropout(const void* x, const void* residual, void
   // round(p 2^32), its upper half and its lower
   const uint64_t threshold = (uint64_t)llrint(p * 4294967296.0);
   const uint32_t upper = (uint32_t)(threshold >> 16), lower = (uint32_t)threshold & 0xffff;
-  DropArgs a = {x, residual, y, rows, cols, xStride, residualStride, yStride, seedDevice, seed, offset,
-                0, lower ? upper + 1 : upper, lower ? upper : ~0u, lower,
+  const uint32_t least = lower ? upper + 1 : upper;
+  DropArgs a = {x, residual, y, rows, cols, xStride, residualStride, yStride, seedDevice, {}, offset,
+                0, 0, least, (least << 16) - 1, lower ? upper : ~0u, lower,
+                upper << 16 | (upper & 0xffff), 65536, 1,
                 p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f, false, false};
+  for (int i = 0; i < 20; ++i)
+    a.keys[i] = (uint32_t)(i % 2 ? seed >> 32 : seed) + (uint32_t)(i / 2) * (i % 2 ? 0xBB67AE85u : 0x9E3779B9u);
   cudaStream_t st = (cudaStream_t)stream;
   const auto pick = [&](auto t) {
     using T = decltype(t);
-    return residual ? run<T, true>(a, st) : run<T, false>(a, st);
+    if (seedDevice) return residual ? run<T, true, true>(a, st) : run<T, false, true>(a, st);
+    return residual ? run<T, true, false>(a, st) : run<T, false, false>(a, st);
   };
   if (dtype == vrFloat32) return pick(float{});
   return dtype == vrFloat16 ? pick(__half{}) : pick(__nv_bfloat16{});

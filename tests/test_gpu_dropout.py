@@ -1,6 +1,8 @@
 """Dropout on the GPU against the generator written out in whole numbers. Results
-are compared bit for bit: x / (1 - p) is one product in 32 bits, the addition one
-sum, and the result is rounded once."""
+are compared bit for bit: an element that stays is x / (1 - p), or with an addition the
+sum of that product and the other, in one rounding of 32 bits (here of 64 bits and then of 32: the
+same but where the first lands on the middle between two numbers of the second, once in 2^28),
+and is rounded once to its type."""
 import pytest
 import torch
 
@@ -62,8 +64,8 @@ def test_numbers_are_the_blocks_halfwords():
 def want(x, p, seed, offset=0, residual=None):
     keep = numbers(x.numel(), seed, offset, x.device).view(x.shape) >= round(p * 2.0 ** 32)
     scale = torch.tensor(1 / (1 - p) if p < 1 else 0.0, dtype=torch.float32, device=x.device)
-    y = torch.where(keep, x.float() * scale, 0.0)
-    return (y if residual is None else y + residual.float()).to(x.dtype)
+    r = torch.zeros_like(x) if residual is None else residual
+    return torch.where(keep, (x.double() * scale.double() + r.double()).float(), r.float()).to(x.dtype)
 
 
 def same(a, b):
