@@ -38,8 +38,10 @@ struct QkArgs {
   // the layout of the kernels of whole packs
   int lanes;       // of a head, a power of two
   int pairs;       // of packs of a head, one a lane
-  uint32_t steps[2];  // of a warp for a token's heads of each kind
-  uint32_t chunk, chunks;  // steps of a warp, warps of a token
+  uint32_t steps[2];  // of a warp: a token's queries, all of its heads
+  uint32_t warps, rounds;  // each warp has so many tokens in full
+  uint32_t quota, extra;   // its steps of the other tokens; how many warps have one more
+  bool wideTable;  // rows of the tables are whole 16 bytes
   float* partials;  // [blocks][2][dim]: sums of g u
   uint32_t blocks;
   void* dw[2];
@@ -48,13 +50,20 @@ struct QkArgs {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-// The row of the tables of a token; tableRows where the position is outside of them.
-__device__ __forceinline__ uint64_t table_row(const QkArgs& a, uint32_t b, uint32_t t) {
-  if (!a.rot) return 0;
+// A token's position as it was loaded (whoever waits for it does that later), and its row of
+// the tables; tableRows where it is outside of them.
+__device__ __forceinline__ int2 load_position(const QkArgs& a, uint32_t b, uint32_t t) {
+  if (!a.rot) return make_int2(0, 0);
   const uint64_t at = b * a.positionStride + t;
-  const int64_t p = a.wide ? static_cast<const int64_t*>(a.positions)[at]
-                           : static_cast<const int32_t*>(a.positions)[at];
+  return a.wide ? static_cast<const int2*>(a.positions)[at]
+                : make_int2(static_cast<const int32_t*>(a.positions)[at], 0);
+}
+__device__ __forceinline__ uint64_t table_row(const QkArgs& a, int2 v) {
+  const int64_t p = a.wide ? (int64_t)((uint64_t)(uint32_t)v.y << 32 | (uint32_t)v.x) : (int64_t)v.x;
   return p >= 0 && (uint64_t)p < a.tableRows ? (uint64_t)p : a.tableRows;
+}
+__device__ __forceinline__ uint64_t table_row(const QkArgs& a, uint32_t b, uint32_t t) {
+  return table_row(a, load_position(a, b, t));
 }
 __device__ __forceinline__ float nan32() { return __int_as_float(0x7fffffff); }
 
@@ -78,244 +87,359 @@ struct Packs {
     }
     a *= V, b *= V;
   }
-  // The angles of the lane's pairs: of halves one for each element of a pack, of
-  // neighbours V / 2 for each pack. Past the rotated part, no rotation.
-  __device__ __forceinline__ void angles(const QkArgs& q, uint64_t row, float (&c)[V], float (&s)[V]) const {
-    const float* cp = q.cos + row * (q.rot / 2);
-    const float* sp = q.sin + row * (q.rot / 2);
-    const bool out = row == q.tableRows;
+};
+
+// A lane's angles of a token, from the rows of the tables in shared memory: of halves one
+// for each element of a pack, of neighbours one for both elements of a pair. Past the
+// rotated part, no rotation. BACK: the opposite angles.
+template <typename T, bool INTER, bool BACK>
+struct Angles {
+  static constexpr int V = kV<T>, N = INTER ? V : V / 2;
+  F2 c[N], s[N];
+  __device__ __forceinline__ void load(const Packs<T, INTER>& at, const float* cosRow, const float* sinRow, int half) {
+    if constexpr (INTER) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      int at = a + i;
-      bool in = hasA && a < (int)q.rot / 2;
-      if (INTER) {
-        at = (i < V / 2 ? a : b) / 2 + i % (V / 2);
-        in = (i < V / 2 ? hasA : hasB) && at < (int)q.rot / 2;
+      for (int i = 0; i < V; ++i) {
+        const int pair = (i < V / 2 ? at.a : at.b) / 2 + i % (V / 2);
+        const bool in = (i < V / 2 ? at.hasA : at.hasB) && pair < half;
+        const float sn = in ? (BACK ? -sinRow[pair] : sinRow[pair]) : 0.f;
+        c[i] = f2(in ? cosRow[pair] : 1.f);
+        s[i] = f2(-sn, sn);
       }
-      c[i] = !in ? 1.f : out ? nan32() : cp[at];
-      s[i] = !in ? 0.f : out ? nan32() : sp[at];
+    } else {
+      const bool in = at.a < half;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 cs = in ? *reinterpret_cast<const float2*>(cosRow + at.a + 2 * i) : make_float2(1.f, 1.f);
+        const float2 sn = in ? *reinterpret_cast<const float2*>(sinRow + at.a + 2 * i) : make_float2(0.f, 0.f);
+        c[i] = f2(cs.x, cs.y);
+        s[i] = BACK ? f2(-sn.x, -sn.y) : f2(sn.x, sn.y);
+      }
+    }
+  }
+  // Both packs turned.
+  __device__ __forceinline__ void turn(F2 (&x)[V / 2], F2 (&y)[V / 2]) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if constexpr (INTER) {
+        float p, q;
+        split(x[i], p, q);
+        x[i] = fma2(f2(q, p), s[i], x[i] * c[i]);
+        split(y[i], p, q);
+        y[i] = fma2(f2(q, p), s[V / 2 + i], y[i] * c[V / 2 + i]);
+      } else {
+        const F2 p = x[i];
+        x[i] = p * c[i] - y[i] * s[i];
+        y[i] = fma2(p, s[i], y[i] * c[i]);
+      }
     }
   }
 };
 
-// Pairs (x, y) turned by (c, s); BACK: by the opposite angle.
-template <int V, bool INTER, bool BACK>
-__device__ __forceinline__ void turn(float (&x)[V], float (&y)[V], const float (&c)[V], const float (&s)[V]) {
-  if constexpr (INTER) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float s0 = BACK ? -s[i] : s[i], s1 = BACK ? -s[V / 2 + i] : s[V / 2 + i];
-      const float p = x[2 * i], q = x[2 * i + 1], t = y[2 * i], v = y[2 * i + 1];
-      x[2 * i] = p * c[i] - q * s0;
-      x[2 * i + 1] = q * c[i] + p * s0;
-      y[2 * i] = t * c[V / 2 + i] - v * s1;
-      y[2 * i + 1] = v * c[V / 2 + i] + t * s1;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float si = BACK ? -s[i] : s[i];
-      const float p = x[i], q = y[i];
-      x[i] = p * c[i] - q * si;
-      y[i] = q * c[i] + p * si;
+// A warp's steps, token after token. First whole tokens, the warps' next to each other in
+// memory; then what is left of the tokens shared out by steps, so that all warps end at
+// the same time.
+struct Walk {
+  uint32_t token, step, end;  // the present token's steps; none: no token is left
+  uint32_t rounds, left;      // whole tokens after this one, steps of the rest after this token's
+  __device__ __forceinline__ void rest(const QkArgs& a, uint32_t warp) {
+    left = a.quota + (warp < a.extra ? 1 : 0);
+    const uint32_t first = warp * a.quota + min(warp, a.extra);
+    token = first / a.steps[1];
+    step = first - token * a.steps[1];
+    token += a.rounds * a.warps;
+    end = min(a.steps[1], step + left);
+    left -= end - step;
+    left |= 1u << 31;  // the rest has begun
+  }
+  __device__ __forceinline__ void start(const QkArgs& a, uint32_t warp) {
+    rounds = a.rounds;
+    left = 0;
+    if (rounds) {
+      --rounds;
+      token = warp, step = 0, end = a.steps[1];
+    } else {
+      rest(a, warp);
     }
   }
-}
-
-template <typename T>
-__device__ __forceinline__ void to_floats(const uint4& v, float (&f)[kV<T>]) {
-  F2 p[kV<T> / 2];
-  unpack<T>(v, p);
-#pragma unroll
-  for (int i = 0; i < kV<T> / 2; ++i) split(p[i], f[2 * i], f[2 * i + 1]);
-}
-template <typename T>
-__device__ __forceinline__ uint4 to_pack(const float (&f)[kV<T>]) {
-  F2 p[kV<T> / 2];
-#pragma unroll
-  for (int i = 0; i < kV<T> / 2; ++i) p[i] = f2(f[2 * i], f[2 * i + 1]);
-  return pack<T>(p);
-}
-
-// Sum over the lanes of a head.
-__device__ __forceinline__ float head_sum(float v, int lanes) {
-  for (int o = 1; o < lanes; o <<= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-
-template <typename W, int V>
-__device__ __forceinline__ void weights(const void* w, int at, bool has, float (&f)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = w && has ? to_f32(static_cast<const W*>(w)[at + i]) : 1.f;
-}
-
-// Whole packs: a warp takes 32 / lanes heads of a token at a step, U steps' loads before
-// the first is computed.
-template <typename T, typename W, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) vrQkForward(const __grid_constant__ QkArgs a) {
-  constexpr int V = kV<T>;
-  begin_kernel();
-  const uint64_t unit = (uint64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const uint32_t token = (uint32_t)(unit / a.chunks);
-  if (token >= a.all) return;
-  const int lane = threadIdx.x & 31, group = lane / a.lanes, groups = 32 / a.lanes;
-  const uint32_t b = token / a.tokens, t = token - b * a.tokens;
-  const Packs<T, INTER> at(a, lane % a.lanes);
-  float c[V], s[V];
-  at.angles(a, table_row(a, b, t), c, s);
-  const uint32_t from = (uint32_t)(unit % a.chunks) * a.chunk;
-  const uint32_t to = from + a.chunk;
-  uint32_t before = 0;  // steps of the kinds before
-  const float mean = 1.f / (float)a.dim;
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    const uint32_t first = from > before ? from - before : 0;
-    const uint32_t last = to < before + a.steps[kind] ? to - (to > before ? before : to) : a.steps[kind];
-    before += a.steps[kind];
-    if (first >= last) continue;
-    float wa[V], wb[V];
-    weights<W, V>(a.w[kind], at.a, at.hasA, wa);
-    weights<W, V>(a.w[kind], at.b, at.hasB, wb);
-    const Side &x = a.x[kind], &y = a.out[kind];
-    const T* xp = static_cast<const T*>(x.p) + b * x.batch + t * x.token;
-    T* yp = static_cast<T*>(const_cast<void*>(y.p)) + b * y.batch + t * y.token;
-    for (uint32_t step = first; step < last; step += U) {
-      uint4 va[U], vb[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t head = (step + u) * groups + group;
-        const bool in = step + u < last && head < a.heads[kind];
-        va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-        if (in && at.hasA) va[u] = *reinterpret_cast<const uint4*>(xp + head * x.head + at.a);
-        if (in && at.hasB) vb[u] = *reinterpret_cast<const uint4*>(xp + head * x.head + at.b);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (step + u >= last) break;
-        const uint32_t head = (step + u) * groups + group;
-        float fa[V], fb[V], q = 0.f;
-        to_floats<T>(va[u], fa);
-        to_floats<T>(vb[u], fb);
-#pragma unroll
-        for (int i = 0; i < V; ++i) q = fmaf(fb[i], fb[i], fmaf(fa[i], fa[i], q));
-        const float r = rsqrtf(head_sum(q, a.lanes) * mean + a.eps);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          fa[i] = fa[i] * r * wa[i];
-          fb[i] = fb[i] * r * wb[i];
-        }
-        turn<V, INTER, false>(fa, fb, c, s);
-        if (head < a.heads[kind]) {
-          if (at.hasA) *reinterpret_cast<uint4*>(yp + head * y.head + at.a) = to_pack<T>(fa);
-          if (at.hasB) *reinterpret_cast<uint4*>(yp + head * y.head + at.b) = to_pack<T>(fb);
-        }
-      }
+  __device__ __forceinline__ bool done() const { return step == end; }
+  __device__ __forceinline__ void next(const QkArgs& a, uint32_t warp) {
+    step = 0, end = a.steps[1];
+    if (rounds) {
+      --rounds;
+      token += a.warps;
+    } else if (left >> 31) {
+      ++token;
+      end = min(end, left & 0x7fffffff);
+      left -= end;
+    } else {
+      rest(a, warp);
     }
   }
+};
+struct Token {
+  uint32_t b, t;
+  __device__ __forceinline__ Token(const QkArgs& a, uint32_t token) : b(0), t(token) {
+    if (a.all != a.tokens) {
+      b = token / a.tokens;
+      t = token - b * a.tokens;
+    }
+  }
+};
+template <typename T>
+__device__ __forceinline__ T* place(const Side& s, const Token& k, uint32_t head) {
+  return static_cast<T*>(const_cast<void*>(s.p)) + k.b * s.batch + k.t * s.token + head * s.head;
 }
 
-// The same backward. Each warp's tokens are blocks' warps apart, so that its sums of
-// g u stay in registers until the last; a block leaves one set.
-template <typename T, typename W, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) vrQkBackward(const __grid_constant__ QkArgs a) {
-  constexpr int V = kV<T>;
-  extern __shared__ float sums[];  // [warps][2][dim], then added up
+// Whole packs, forward or backward. A warp takes a token's queries, then its keys, U times
+// 32 / lanes heads at a step: the chains of one head (its sums over lanes, its root) are
+// long, and side by side they fill each other's gaps. Each lane copies its own packs
+// to shared memory STAGES - 1 steps ahead, across tokens too, and a token's angles come with
+// its first step: nothing is waited for but what was asked for long before, and what is on
+// its way takes no registers. Backward, a warp's sums of g u stay in registers until its
+// last token; a block leaves one set.
+constexpr int kStages = 3, kAtOnce = 2;
+template <bool BACK>
+constexpr int kBlocks = BACK ? 1 : 2;  // on an SM: 255 registers a thread, or 128
+template <typename T, typename W, bool INTER, bool BACK>
+__global__ void __launch_bounds__(kThreads, kBlocks<BACK>) vrQkHeads(const __grid_constant__ QkArgs a) {
+  constexpr int V = kV<T>, NP = BACK ? 4 : 2, H = V / 2, U = kAtOnce;
+  extern __shared__ uint4 shared[];  // rings, then the tables' rows, then the weights
   begin_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int group = lane / a.lanes, groups = 32 / a.lanes;
+  const int group = lane / a.lanes, groups = 32 / a.lanes, half = a.rot / 2;
   const Packs<T, INTER> at(a, lane % a.lanes);
-  const float mean = 1.f / (float)a.dim;
-#pragma unroll 1
-  for (int kind = 0; kind < 2; ++kind) {
-    float wa[V], wb[V], da[V], db[V];
-    weights<W, V>(a.w[kind], at.a, at.hasA, wa);
-    weights<W, V>(a.w[kind], at.b, at.hasB, wb);
-#pragma unroll
-    for (int i = 0; i < V; ++i) da[i] = db[i] = 0.f;
-    const Side &x = a.x[kind], &g = a.dy[kind], &o = a.out[kind];
-    const uint64_t units = (uint64_t)a.all * a.chunks;
-    for (uint64_t unit = (uint64_t)blockIdx.x * kWarps + warp; unit < units; unit += (uint64_t)gridDim.x * kWarps) {
-      const uint32_t token = (uint32_t)(unit / a.chunks), from = (uint32_t)(unit % a.chunks) * a.chunk;
-      const uint32_t last = min(from + a.chunk, a.steps[kind]);
-      if (from >= last) continue;
-      const uint32_t b = token / a.tokens, t = token - b * a.tokens;
-      float c[V], s[V];
-      at.angles(a, table_row(a, b, t), c, s);
-      const T* xp = static_cast<const T*>(x.p) + b * x.batch + t * x.token;
-      const T* gp = static_cast<const T*>(g.p) + b * g.batch + t * g.token;
-      T* op = static_cast<T*>(const_cast<void*>(o.p)) + b * o.batch + t * o.token;
-      for (uint32_t step = from; step < last; step += U) {
-        uint4 xa[U], xb[U], ga[U], gb[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t head = (step + u) * groups + group;
-          const bool in = step + u < last && head < a.heads[kind];
-          xa[u] = xb[u] = ga[u] = gb[u] = make_uint4(0, 0, 0, 0);
-          if (in && at.hasA) {
-            xa[u] = *reinterpret_cast<const uint4*>(xp + head * x.head + at.a);
-            ga[u] = *reinterpret_cast<const uint4*>(gp + head * g.head + at.a);
-          }
-          if (in && at.hasB) {
-            xb[u] = *reinterpret_cast<const uint4*>(xp + head * x.head + at.b);
-            gb[u] = *reinterpret_cast<const uint4*>(gp + head * g.head + at.b);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (step + u >= last) break;
-          const uint32_t head = (step + u) * groups + group;
-          float fa[V], fb[V], ha[V], hb[V], q = 0.f, p = 0.f;
-          to_floats<T>(xa[u], fa);
-          to_floats<T>(xb[u], fb);
-          to_floats<T>(ga[u], ha);
-          to_floats<T>(gb[u], hb);
-          turn<V, INTER, true>(ha, hb, c, s);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            q = fmaf(fb[i], fb[i], fmaf(fa[i], fa[i], q));
-            p = fmaf(hb[i] * wb[i], fb[i], fmaf(ha[i] * wa[i], fa[i], p));
-          }
-          const float r = rsqrtf(head_sum(q, a.lanes) * mean + a.eps);
-          // never r^2, which leaves the range of a float before dx does
-          const float k = -(r * (r * (head_sum(p, a.lanes) * mean)));
-          if (head < a.heads[kind]) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              da[i] = fmaf(ha[i], fa[i] * r, da[i]);
-              db[i] = fmaf(hb[i], fb[i] * r, db[i]);
-              fa[i] = r * fmaf(fa[i], k, ha[i] * wa[i]);
-              fb[i] = r * fmaf(fb[i], k, hb[i] * wb[i]);
-            }
-            if (at.hasA) *reinterpret_cast<uint4*>(op + head * o.head + at.a) = to_pack<T>(fa);
-            if (at.hasB) *reinterpret_cast<uint4*>(op + head * o.head + at.b) = to_pack<T>(fb);
-          }
-        }
-      }
-    }
-    if (!a.partials) continue;
-    // over the heads of a warp, then over the warps
-    for (int o = a.lanes; o < 32; o <<= 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        da[i] += __shfl_xor_sync(~0u, da[i], o);
-        db[i] += __shfl_xor_sync(~0u, db[i], o);
-      }
-    }
-    if (group == 0) {
-      float* mine = sums + (warp * 2 + kind) * a.dim;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (at.hasA) mine[at.a + i] = da[i];
-        if (at.hasB) mine[at.b + i] = db[i];
-      }
-    }
-  }
-  if (!a.partials) return;
-  __syncthreads();
+  uint4* const ring = shared + warp * (kStages * U * NP * 32) + lane;
+  float* const rows = reinterpret_cast<float*>(shared + kWarps * kStages * U * NP * 32) + warp * (kStages * 2 * half);
+  float* const w = reinterpret_cast<float*>(shared + kWarps * kStages * U * NP * 32) + kWarps * (kStages * 2 * half);
   for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += kThreads) {
-    float t = 0.f;
-    for (int w = 0; w < kWarps; ++w) t += sums[w * 2 * a.dim + i];
-    a.partials[(uint64_t)blockIdx.x * 2 * a.dim + i] = t;
+    const W* p = static_cast<const W*>(a.w[i >= a.dim]);
+    w[i] = p ? to_f32(p[i < a.dim ? i : i - a.dim]) : 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kStages * U * NP; ++i)
+    if (i % 2 ? !at.hasB : !at.hasA) ring[i * 32] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+
+  const uint32_t me = blockIdx.x * kWarps + warp, keys = a.steps[0];
+  Walk now;
+  now.start(a, me);
+  Walk ahead = now, after = now;  // of the copies; of the positions, which are loaded a token before
+  int2 position = make_int2(0, 0);
+  const auto look = [&]() {
+    if (after.done()) return;
+    const Token k(a, after.token);
+    position = load_position(a, k.b, k.t);
+  };
+  look();
+  bool fresh = true;
+  uint32_t into = 0;  // a token's place among the tables' rows
+  const T *xp = nullptr, *gp = nullptr;
+  uint64_t xStep = 0, gStep = 0;
+  uint32_t left = 0;  // heads from this lane's next one on
+  const auto fetch = [&](int stage) {
+    if (!ahead.done()) {
+      if (fresh || ahead.step == keys) {
+        const Token k(a, ahead.token);
+        const int kind = ahead.step >= keys;
+        const uint32_t head = (kind ? ahead.step - keys : ahead.step) * U * groups + group;
+        left = a.heads[kind] - head;  // "negative" where there is none
+        xp = place<const T>(a.x[kind], k, head);
+        xStep = groups * a.x[kind].head;
+        if (BACK) {
+          gp = place<const T>(a.dy[kind], k, head);
+          gStep = groups * a.dy[kind].head;
+        }
+      }
+      if (fresh) {
+        fresh = false;
+        float* to = rows + into * 2 * half;
+        into = into + 1 == kStages ? 0 : into + 1;
+        const uint64_t row = half ? table_row(a, position) : 0;
+        const bool none = row == a.tableRows;
+        const float *cp = a.cos + row * half, *sp = a.sin + row * half;
+        if (!none && a.wideTable) {  // 16 bytes a lane
+          for (int i = lane * 4; i < 2 * half; i += 128)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to + i)),
+                         "l"(i < half ? cp + i : sp + (i - half))
+                         : "memory");
+        } else {
+          for (int i = lane; i < 2 * half; i += 32) {
+            if (none)
+              to[i] = nan32();
+            else
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to + i)),
+                           "l"(i < half ? cp + i : sp + (i - half))
+                           : "memory");
+          }
+        }
+        after.next(a, me);
+        look();
+      }
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + stage * (U * NP * 32));
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if ((int)left > 0) {
+          const auto copy = [&](int p, const T* from) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (u * NP + p) * 512), "l"(from) : "memory");
+          };
+          if (at.hasA) copy(0, xp + at.a);
+          if (at.hasB) copy(1, xp + at.b);
+          if (BACK && at.hasA) copy(2, gp + at.a);
+          if (BACK && at.hasB) copy(3, gp + at.b);
+        }
+        left -= groups;
+        xp += xStep;
+        if (BACK) gp += gStep;
+      }
+      if (++ahead.step == ahead.end) {
+        ahead = after;
+        fresh = true;
+      }
+    }
+    copies_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+
+  F2 sa[2][BACK ? H : 1], sb[2][BACK ? H : 1];  // sums of g u
+  if (BACK) {
+#pragma unroll
+    for (int i = 0; i < H; ++i) sa[0][i] = sb[0][i] = sa[1][i] = sb[1][i] = f2(0.f);
+  }
+  const float mean = 1.f / (float)a.dim;
+  Angles<T, INTER, BACK> angles;
+  int stage = 0;
+  uint32_t from = 0;
+  bool first;
+  // Steps [now.step, end) of the present token, which are of one kind.
+  const auto run = [&](auto kindOf, uint32_t end) {
+    constexpr int kind = decltype(kindOf)::value;
+    uint32_t head = (now.step - (kind ? keys : 0)) * U * groups + group;
+    T* op = place<T>(a.out[kind], Token(a, now.token), head);
+    const uint64_t oStep = groups * a.out[kind].head;
+    F2 wa[H], wb[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const float* p = w + kind * a.dim;
+      wa[i] = at.hasA ? f2(p[at.a + 2 * i], p[at.a + 2 * i + 1]) : f2(1.f);
+      wb[i] = at.hasB ? f2(p[at.b + 2 * i], p[at.b + 2 * i + 1]) : f2(1.f);
+    }
+#pragma unroll 1
+    for (; now.step < end; ++now.step) {
+      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      copies_wait<kStages - 1>();
+      if (first) {
+        first = false;
+        __syncwarp();  // the row was copied by all lanes
+        const float* r = rows + from * 2 * half;
+        angles.load(at, r, r + half, half);
+        from = from + 1 == kStages ? 0 : from + 1;
+      }
+      const uint4* in = ring + stage * (U * NP * 32);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      F2 fa[U][H], fb[U][H];
+      [[maybe_unused]] F2 ga[U][H], gb[U][H];
+      [[maybe_unused]] float q[U], p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        F2 q2 = f2(0.f), p2 = f2(0.f);
+        unpack<T>(in[u * NP * 32], fa[u]);
+        unpack<T>(in[u * NP * 32 + 32], fb[u]);
+#pragma unroll
+        for (int i = 0; i < H; ++i) q2 = fma2(fb[u][i], fb[u][i], fma2(fa[u][i], fa[u][i], q2));
+        q[u] = both(q2);
+        if constexpr (BACK) {
+          unpack<T>(in[u * NP * 32 + 64], ga[u]);
+          unpack<T>(in[u * NP * 32 + 96], gb[u]);
+          angles.turn(ga[u], gb[u]);
+#pragma unroll
+          for (int i = 0; i < H; ++i)
+            p2 = fma2(gb[u][i] * wb[i], fb[u][i], fma2(ga[u][i] * wa[i], fa[u][i], p2));
+          p[u] = both(p2);
+        }
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1)
+        if (d < a.lanes) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            q[u] += __shfl_xor_sync(~0u, q[u], d);
+            if (BACK) p[u] += __shfl_xor_sync(~0u, p[u], d);
+          }
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool mine = head < a.heads[kind];
+        head += groups;
+        const float r = rsqrtf(q[u] * mean + a.eps);
+        const F2 r2 = f2(r);
+        if constexpr (BACK) {
+          // never r^2, which leaves the range of a float before dx does
+          const F2 k2 = f2(-(r * (r * (p[u] * mean))));
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              sa[kind][i] = fma2(ga[u][i], fa[u][i] * r2, sa[kind][i]);
+              sb[kind][i] = fma2(gb[u][i], fb[u][i] * r2, sb[kind][i]);
+              fa[u][i] = fma2(fa[u][i], k2, ga[u][i] * wa[i]) * r2;
+              fb[u][i] = fma2(fb[u][i], k2, gb[u][i] * wb[i]) * r2;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            fa[u][i] = fa[u][i] * r2 * wa[i];
+            fb[u][i] = fb[u][i] * r2 * wb[i];
+          }
+          angles.turn(fa[u], fb[u]);
+        }
+        if (mine) {
+          if (at.hasA) *reinterpret_cast<uint4*>(op + at.a) = pack<T>(fa[u]);
+          if (at.hasB) *reinterpret_cast<uint4*>(op + at.b) = pack<T>(fb[u]);
+        }
+        op += oStep;
+      }
+    }
+  };
+  for (; !now.done(); now.next(a, me)) {
+    first = true;
+    if (now.step < keys) run(std::integral_constant<int, 0>{}, min(keys, now.end));
+    if (now.step < now.end) run(std::integral_constant<int, 1>{}, now.end);
+  }
+  if constexpr (BACK) {
+    if (!a.partials) return;
+    copies_wait<0>();
+    __syncthreads();  // the sums take the rings' place
+    float* const sums = reinterpret_cast<float*>(shared);  // [warps][2][dim]
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      float sum[2 * V];
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        split(sa[kind][i], sum[2 * i], sum[2 * i + 1]);
+        split(sb[kind][i], sum[V + 2 * i], sum[V + 2 * i + 1]);
+      }
+      // over the heads of a warp, then over the warps
+      for (int d = a.lanes; d < 32; d <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) sum[i] += __shfl_xor_sync(~0u, sum[i], d);
+      }
+      if (group == 0) {
+        float* mine = sums + (warp * 2 + kind) * a.dim;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (at.hasA) mine[at.a + i] = sum[i];
+          if (at.hasB) mine[at.b + i] = sum[V + i];
+        }
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += kThreads) {
+      float t = 0.f;
+      for (int v = 0; v < kWarps; ++v) t += sums[v * 2 * a.dim + i];
+      a.partials[(uint64_t)blockIdx.x * 2 * a.dim + i] = t;
+    }
   }
 }
 
@@ -563,17 +687,39 @@ bool layOut(QkArgs& a, bool backward) {
   if (a.pairs > 32) return false;
   a.lanes = 1;
   while (a.lanes < a.pairs) a.lanes *= 2;
-  const uint32_t groups = 32 / a.lanes;
-  for (int k = 0; k < 2; ++k) a.steps[k] = (a.heads[k] + groups - 1) / groups;
-  const uint32_t steps = backward ? (a.steps[0] > a.steps[1] ? a.steps[0] : a.steps[1]) : a.steps[0] + a.steps[1];
-  // A token is one warp's, which reads its angles once, but where few tokens would leave
-  // SMs without work.
-  const uint64_t warps = (uint64_t)kSMs * 16;
-  uint64_t chunk = (uint64_t)steps * a.all / warps;
-  chunk = chunk < 1 ? 1 : chunk > steps ? steps : chunk;
-  a.chunk = (uint32_t)chunk;
-  a.chunks = (uint32_t)((steps + chunk - 1) / chunk);
+  a.wideTable = (((uintptr_t)a.cos | (uintptr_t)a.sin | a.rot * 2) & 15) == 0;
+  // Batches whose tokens follow one another are one.
+  bool one = !a.rot || a.positionStride == a.tokens;
+  for (int k = 0; k < 2; ++k)
+    for (const Side* s : {&a.x[k], &a.dy[k], &a.out[k]}) one = one && (!s->p || s->batch == a.tokens * s->token);
+  if (one) a.tokens = a.all;
   return true;
+}
+
+template <typename T, typename W, bool BACK>
+vrResult_t wholeHeads(QkArgs& a, cudaStream_t st) {
+  const void* f = a.inter ? (const void*)&vrQkHeads<T, W, true, BACK> : (const void*)&vrQkHeads<T, W, false, BACK>;
+  const uint32_t at = kAtOnce * (32 / a.lanes);
+  a.steps[0] = (a.heads[0] + at - 1) / at;
+  a.steps[1] = a.steps[0] + (a.heads[1] + at - 1) / at;
+  // One round of blocks; of few steps, a warp for each.
+  const uint64_t need = ((uint64_t)a.all * a.steps[1] + kWarps - 1) / kWarps, most = (uint64_t)kSMs * kBlocks<BACK>;
+  a.blocks = (uint32_t)(need < most ? need : most);
+  a.warps = a.blocks * kWarps;
+  a.rounds = a.all / a.warps;
+  const uint32_t rest = a.all % a.warps * a.steps[1];  // below 2^12 tokens of below 2^17 steps
+  a.quota = rest / a.warps;
+  a.extra = rest % a.warps;
+  size_t smem = (size_t)kWarps * kStages * ((BACK ? 4 : 2) * 512 * kAtOnce + a.rot * sizeof(float)) +
+                2 * a.dim * sizeof(float);
+  if constexpr (BACK) {
+    const size_t sums = (size_t)kWarps * 2 * a.dim * sizeof(float);
+    if (smem < sums) smem = sums;
+  }
+  if (!setOnce(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ||
+      !setOnce(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared))
+    return vrCudaError;
+  return launch(f, dim3(a.blocks), dim3(kThreads), smem, st, a);
 }
 
 struct Call {
@@ -676,12 +822,7 @@ extern "C" VR_API vrResult_t vrQkNormRopeForward(
     using T = decltype(t);
     using W = decltype(w);
     cudaStream_t st = (cudaStream_t)stream;
-    if (layOut<T>(a, false)) {
-      const uint64_t blocks = ((uint64_t)a.all * a.chunks + kWarps - 1) / kWarps;
-      const void* f = a.inter ? (const void*)&vrQkForward<T, W, true, 4> : (const void*)&vrQkForward<T, W, false, 4>;
-      if (blocks > 0x7fffffffu) return vrInvalidArgument;
-      return launch(f, dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
-    }
+    if (layOut<T>(a, false)) return wholeHeads<T, W, false>(a, st);
     const uint64_t units = (uint64_t)a.all * (a.heads[0] + a.heads[1]);
     const uint64_t blocks = (units + kWarps - 1) / kWarps, most = (uint64_t)kSMs * 8;
     return launch((const void*)&vrQkForwardAny<T, W>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads),
@@ -755,16 +896,17 @@ extern "C" VR_API vrResult_t vrQkNormRopeBackward(
   return dispatch(dtype, weightType, [&](auto t, auto w) {
     using T = decltype(t);
     using W = decltype(w);
-    const size_t smem = params ? (size_t)kWarps * 2 * dim * sizeof(float) : 0;
-    const bool whole = layOut<T>(a, true);
-    const uint64_t units = whole ? (uint64_t)a.all * a.chunks : (uint64_t)a.all * (a.heads[0] + a.heads[1]);
-    const uint64_t blocks = (units + kWarps - 1) / kWarps;
-    a.blocks = (unsigned)(blocks < kBackwardBlocks ? blocks : kBackwardBlocks);
-    const void* f = !whole    ? (const void*)&vrQkBackwardAny<T, W>
-                    : a.inter ? (const void*)&vrQkBackward<T, W, true, 2>
-                              : (const void*)&vrQkBackward<T, W, false, 2>;
-    if (smem > 48 * 1024 && !setOnce(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024)) return vrCudaError;
-    vrResult_t r = launch(f, dim3(a.blocks), dim3(kThreads), smem, st, a);
+    vrResult_t r;
+    if (layOut<T>(a, true)) {
+      r = wholeHeads<T, W, true>(a, st);
+    } else {
+      const size_t smem = params ? (size_t)kWarps * 2 * dim * sizeof(float) : 0;
+      const uint64_t blocks = ((uint64_t)a.all * (a.heads[0] + a.heads[1]) + kWarps - 1) / kWarps;
+      a.blocks = (unsigned)(blocks < kBackwardBlocks ? blocks : kBackwardBlocks);
+      const void* f = (const void*)&vrQkBackwardAny<T, W>;
+      if (smem > 48 * 1024 && !setOnce(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024)) return vrCudaError;
+      r = launch(f, dim3(a.blocks), dim3(kThreads), smem, st, a);
+    }
     if (r == vrSuccess && params)
       r = launch((const void*)&vrQkJoin<W>, dim3((unsigned)((dim + 31) / 32), 2), dim3(32 * kJoinWarps), 0, st, a);
     return r;
