@@ -446,20 +446,32 @@ def dropout(x, p, seed, offset=0, residual=None):
 
 
 # ---------------------------------------------- norm and rotation of heads
-def _heads(t, what, batch=None, tokens=None, dim=None, dtype=None, device=None):
-    """(batch, tokens, heads, dim, strides) of a tensor of (tokens, heads, dim) or
-    (batch, tokens, heads, dim)."""
-    n = t.dim()
+@functools.lru_cache(maxsize=1024)
+def _head_layout(shape, strides):
+    """(batch, tokens, heads, dim, batch, token and head strides) of a tensor of (tokens,
+    heads, dim) or (batch, tokens, heads, dim)."""
+    n = len(shape)
     if n != 3 and n != 4:
-        raise ValueError(f"{what} must be (tokens, heads, dim) or (batch, tokens, heads, dim)")
-    shape, st = t.shape, t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"{what}: the last axis must be dense")
-    b = shape[0] if n == 4 else 1
-    if dim is not None and (b != batch or shape[-3] != tokens or shape[-1] != dim or
-                            t.dtype != dtype or t.get_device() != device):
-        raise ValueError(f"{what} does not match q in batch, tokens, dim, type or device")
-    return b, shape[-3], shape[-2], shape[-1], vr.strides3(st[0] if n == 4 else 0, st[-3], st[-2])
+        raise ValueError("heads must be (tokens, heads, dim) or (batch, tokens, heads, dim)")
+    if strides[-1] != 1 and shape[-1] != 1:
+        raise ValueError("the last axis of heads must be dense")
+    batch, stride = (shape[0], strides[0]) if n == 4 else (1, 0)
+    return (batch, *shape[-3:], vr.strides3(stride, strides[-3], strides[-2]))
+
+
+def _heads(t, shape, dtype, device, what):
+    """The strides of a tensor that has to have this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what} does not match in shape, type or device")
+    return _head_layout(shape, t.stride())[4]
+
+
+def _keys(k, q, batch, tokens, dim, device):
+    """(heads, strides) of the keys that go with q."""
+    b, t, heads, d, strides = _head_layout(k.shape, k.stride())
+    if b != batch or t != tokens or d != dim or k.dtype is not q.dtype or k.get_device() != device:
+        raise ValueError("k does not match q in batch, tokens, dim, type or device")
+    return heads, strides
 
 
 def _rotation(cos, sin, positions, batch, tokens, dim, device):
@@ -470,21 +482,22 @@ def _rotation(cos, sin, positions, batch, tokens, dim, device):
         return None, None, 0, None, 4, 0, 0
     if sin is None or positions is None:
         raise ValueError("a rotation needs cos, sin and positions")
-    for t in (cos, sin):
-        if t.dtype != _F32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous() or \
-                t.get_device() != device or 2 * t.shape[1] > dim:
-            raise ValueError("cos and sin must be dense float32 (positions, rotary / 2) on q's device")
-    if positions.get_device() != device or positions.dtype not in _POSITION:
+    shape = cos.shape
+    if sin.shape != shape or len(shape) != 2 or 2 * shape[1] > dim or cos.dtype is not _F32 or \
+            sin.dtype is not _F32 or not cos.is_contiguous() or not sin.is_contiguous() or \
+            cos.get_device() != device or sin.get_device() != device:
+        raise ValueError("cos and sin must be dense float32 (positions, rotary / 2) on q's device")
+    kind = _POSITION.get(positions.dtype)
+    if kind is None or positions.get_device() != device:
         raise ValueError("positions must be int32 or int64 on q's device")
-    shape = tuple(positions.shape)
-    if shape == (batch, tokens) and (tokens <= 1 or positions.stride(1) == 1):
-        stride = positions.stride(0)
-    elif shape == (tokens,) and (tokens <= 1 or positions.stride(0) == 1):
-        stride = 0
+    at, strides = positions.shape, positions.stride()
+    if at == (batch, tokens) and (tokens <= 1 or strides[1] == 1):
+        step = strides[0]
+    elif at == (tokens,) and (tokens <= 1 or strides[0] == 1):
+        step = 0
     else:
         raise ValueError("positions must be (tokens,) or (batch, tokens), dense along tokens")
-    return (cos.data_ptr(), sin.data_ptr(), cos.shape[0], positions.data_ptr(),
-            _POSITION[positions.dtype], stride, 2 * cos.shape[1])
+    return cos.data_ptr(), sin.data_ptr(), shape[0], positions.data_ptr(), kind, step, 2 * shape[1]
 
 
 _POSITION = {torch.int32: vr.DTYPES["int32"], torch.int64: vr.DTYPES["int64"]}
@@ -519,20 +532,16 @@ def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None,
     if device != _current_device():
         return _on_device(device, qk_norm_rope_forward, q, k, q_weight, k_weight, cos, sin, positions,
                           eps, interleaved, q_out, k_out)
-    batch, tokens, heads, dim, qs = _heads(q, "q")
-    like = (batch, tokens, dim, q.dtype, device)
-    kheads, ks, yk, yks = 0, None, None, None
+    batch, tokens, heads, dim, qs = _head_layout(q.shape, q.stride())
+    dtype = q.dtype
     wcode = _head_weights(q, dim, device, q_weight, k_weight)
+    kheads, ks, yk, yks = 0, None, None, None
     if k is not None:
-        _, _, kheads, _, ks = _heads(k, "k", *like)
+        kheads, ks = _keys(k, q, batch, tokens, dim, device)
         yk = torch.empty_like(k) if k_out is None else k_out
-        if yk.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        yks = _heads(yk, "k_out", *like)[4]
+        yks = _heads(yk, k.shape, dtype, device, "k_out")
     yq = torch.empty_like(q) if q_out is None else q_out
-    if yq.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    yqs = _heads(yq, "q_out", *like)[4]
+    yqs = _heads(yq, q.shape, dtype, device, "q_out")
     c, s, table, at, kind, step, rot = _rotation(cos, sin, positions, batch, tokens, dim, device)
     rc = vr.lib().vrQkNormRopeForward(
         q.data_ptr(), heads, qs, _ptr(k), kheads, ks, _ptr(q_weight), _ptr(k_weight), yq.data_ptr(),
@@ -567,31 +576,28 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight=None, k_weight=None, cos=None, 
     if device != _current_device():
         return _on_device(device, qk_norm_rope_backward, dq, dk, q, k, q_weight, k_weight, cos, sin,
                           positions, eps, interleaved, dq_weight, dk_weight, dq_in, dk_in)
-    batch, tokens, heads, dim, qs = _heads(q, "q")
-    like = (batch, tokens, dim, q.dtype, device)
+    batch, tokens, heads, dim, qs = _head_layout(q.shape, q.stride())
+    dtype = q.dtype
     given = [t for t in (dq_weight, dk_weight, dq_in, dk_in) if isinstance(t, torch.Tensor)]
     wcode = _head_weights(q, dim, device, q_weight, k_weight, *[
         t for t in (dq_weight, dk_weight) if isinstance(t, torch.Tensor)])
-    wt = _TYPE[wcode]
-
-    def side(x, dy, dx, what):
-        st = _heads(x, what, *like)[4]
-        if dy.shape != x.shape or (dx is not None and dx.shape != x.shape):
-            raise ValueError(f"the gradients of {what} must have its shape")
-        dx = torch.empty_like(x) if dx is None else dx
-        return st, _heads(dy, f"d{what}", *like)[4], dx, _heads(dx, f"d{what}_in", *like)[4]
-
-    qs, dqs, dq_in, dqis = side(q, dq, dq_in, "q")
+    dqs = _heads(dq, q.shape, dtype, device, "dq")
+    dq_in = torch.empty_like(q) if dq_in is None else dq_in
+    dqis = _heads(dq_in, q.shape, dtype, device, "dq_in")
     kheads, ks, dks, dkis = 0, None, None, None
     if k is not None:
-        kheads = k.shape[-2]
-        ks, dks, dk_in, dkis = side(k, dk, dk_in, "k")
+        kheads, ks = _keys(k, q, batch, tokens, dim, device)
+        dks = _heads(dk, k.shape, dtype, device, "dk")
+        dk_in = torch.empty_like(k) if dk_in is None else dk_in
+        dkis = _heads(dk_in, k.shape, dtype, device, "dk_in")
     else:
         dk, dk_in, dk_weight = None, None, False
     grads = [dq_weight, dk_weight]
     for i in (0, 1):
         if grads[i] is True:
-            grads[i] = torch.empty(dim, dtype=wt, device=q.device)
+            like = (q_weight, k_weight)[i]
+            grads[i] = torch.empty(dim, dtype=_TYPE[wcode], device=q.device) if like is None else \
+                torch.empty_like(like)
         elif not isinstance(grads[i], torch.Tensor):
             grads[i] = None
     ws, nbytes = None, 0
@@ -653,22 +659,31 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
 
 # ------------------------------------------------------------------ losses
 def _check_logits(logits, targets):
-    """(columns, type code, device, rows, row stride) of a matrix of logits and its targets."""
-    cols, code, device = _check_x(logits)
-    if targets.dtype != torch.int64 or targets.get_device() != device or \
-            targets.shape != logits.shape[:-1] or not targets.is_contiguous():
+    """(columns, type code, device index, rows, row stride) of a matrix of logits and its
+    targets."""
+    shape = logits.shape
+    code = _NORM_CODE.get(logits.dtype)
+    if code is None or not logits.is_cuda or not shape or not shape[-1]:
+        _bad_x(logits)
+    device = logits.get_device()
+    if targets.dtype is not torch.int64 or targets.get_device() != device or \
+            targets.shape != shape[:-1] or not targets.is_contiguous():
         raise ValueError("targets must be dense int64 of the logits' leading axes, on their device")
-    return (cols, code, device, *_rows(logits, "logits"))
+    rows, stride = (targets.numel(), shape[-1]) if logits.is_contiguous() else _rows(logits, "logits")
+    return shape[-1], code, device, rows, stride
 
 
-def _row_vector(t, like, what):
-    """The address of a dense float32 vector with a number for each row."""
-    if t is None:
-        return None
-    if t.dtype != _F32 or t.get_device() != like.get_device() or t.shape != like.shape or \
-            not t.is_contiguous():
-        raise ValueError(f"{what} must be dense float32 of the targets' shape, on their device")
-    return t.data_ptr()
+def _row_vectors(device, shape, *tensors):
+    """The addresses of dense float32 vectors with a number for each row; None stays None."""
+    at = []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        if t.dtype is not _F32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+            raise ValueError("numbers of rows must be dense float32 of the targets' shape, on their device")
+        at.append(t.data_ptr())
+    return at
 
 
 def _gradient_of(logits, out, device, cols):
@@ -691,8 +706,9 @@ def token_logprobs_forward(logits, targets, rest=False, stream=None):
     cols, code, device, rows, xs = _check_logits(logits, targets)
     if device != _current_device():
         return _on_device(device, token_logprobs_forward, logits, targets, rest)
-    logp, lse = (torch.empty(targets.shape, dtype=_F32, device=logits.device) for _ in range(2))
-    rest = torch.empty_like(lse) if rest else None
+    logp = torch.empty_like(targets, dtype=_F32)
+    lse = torch.empty_like(logp)
+    rest = torch.empty_like(logp) if rest else None
     rc = vr.lib().vrTokenLogProbsForward(logits.data_ptr(), targets.data_ptr(), logp.data_ptr(),
                                          lse.data_ptr(), _ptr(rest), rows, cols, xs, code,
                                          _raw_stream(device))
@@ -715,7 +731,9 @@ def token_logprobs_backward(dlogp, logits, targets, lse, rest=None, gain=None, o
         return _on_device(device, token_logprobs_backward, dlogp, logits, targets, lse, rest, gain, out)
     if gain is not None and (gain.dtype != _F32 or gain.numel() != 1 or gain.get_device() != device):
         raise ValueError("gain must be one float32 on the logits' device")
-    c, s, r = (_row_vector(t, targets, n) for t, n in ((dlogp, "dlogp"), (lse, "lse"), (rest, "rest")))
+    if dlogp is None or lse is None:
+        raise ValueError("the gradient needs dlogp and lse")
+    c, s, r = _row_vectors(device, targets.shape, dlogp, lse, rest)
     dx, ds = _gradient_of(logits, out, device, cols)
     rc = vr.lib().vrTokenLogProbsBackward(c, _ptr(gain), logits.data_ptr(), targets.data_ptr(), s,
                                           r, dx.data_ptr(), rows, cols, xs, ds, code,
@@ -729,38 +747,43 @@ def token_logprobs_backward(dlogp, logits, targets, lse, rest=None, gain=None, o
 
 def _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, clip_high, kl_coef,
             scale, gradient, out):
-    """(loss, logp, lse, dlogp, rest, dlogits or None)"""
+    """(loss, logp, lse, dlogp, rest), or (loss, logp, dlogits) of the gradient in one pass"""
     cols, code, device, rows, xs = _check_logits(logits, targets)
     if device != _current_device():
         return _on_device(device, _policy, logits, targets, old_logp, advantages, weights, ref_logp,
                           clip_low, clip_high, kl_coef, scale, gradient, out)
     if old_logp is None or advantages is None:
         raise ValueError("a policy loss needs old_logp and advantages")
-    vectors = [_row_vector(t, targets, n) for t, n in
-               ((old_logp, "old_logp"), (advantages, "advantages"), (weights, "weights"),
-                (ref_logp, "ref_logp"))]
+    vectors = _row_vectors(device, targets.shape, old_logp, advantages, weights, ref_logp)
     dx, ds = _gradient_of(logits, out, device, cols) if gradient else (None, 0)
     loss = torch.empty((), dtype=_F32, device=logits.device)
-    logp = torch.empty(targets.shape, dtype=_F32, device=logits.device)
-    lse, dlogp, rest, at = _row_buffers(targets, rows)
+    logp = torch.empty_like(old_logp)
+    kept, n, at = _row_buffers(logits, rows)
     rc = vr.lib().vrPolicyLoss(logits.data_ptr(), targets.data_ptr(), *vectors, loss.data_ptr(),
-                               logp.data_ptr(), lse.data_ptr(), rest.data_ptr(), dlogp.data_ptr(),
-                               _ptr(dx), rows, cols, xs, ds, clip_low, clip_high, kl_coef, scale,
-                               code, at, 4 * rows, _raw_stream(device))
+                               logp.data_ptr(), at, at + 8 * n, at + 4 * n, _ptr(dx), rows, cols, xs,
+                               ds, clip_low, clip_high, kl_coef, scale, code, at + 12 * n, 4 * rows,
+                               _raw_stream(device))
     if rc:
         raise vr.VrError(rc, "vrPolicyLoss")
-    if out is not None:
-        _written(out)
-    return loss, logp, lse, dlogp, rest, dx
+    if gradient:
+        if out is not None:
+            _written(out)
+        return loss, logp, dx
+    return loss, logp, *_kept_rows(kept, n, targets)
 
 
-def _row_buffers(targets, rows, extra=0):
-    """(lse, dlogp, rest, address of a workspace): one allocation for what a call keeps of
-    its rows, an aligned workspace of a float a row and `extra` bytes behind it."""
+def _row_buffers(logits, rows, extra=0):
+    """(tensor, n, address): one allocation for what a call keeps of its rows, four times n
+    floats (lse, dlogp, rest, and a workspace or the tokens' logp) and `extra` bytes."""
     n = (rows + 3) // 4 * 4
-    kept = torch.empty(4 * n + extra // 4, dtype=_F32, device=targets.device)
-    return (*(kept[i * n: i * n + rows].view(targets.shape) for i in range(3)),
-            kept.data_ptr() + 12 * n)
+    kept = torch.empty(4 * n + extra // 4, dtype=_F32, device=logits.device)
+    return kept, n, kept.data_ptr()
+
+
+def _kept_rows(kept, n, targets):
+    """(lse, dlogp, rest)"""
+    rows = targets.numel()
+    return tuple(kept[i * n: i * n + rows].view(targets.shape) for i in range(3))
 
 
 def policy_loss_forward(logits, targets, old_logp, advantages, weights=None, ref_logp=None,
@@ -791,13 +814,12 @@ def policy_loss_gradient(logits, targets, old_logp, advantages, weights=None, re
     if stream is not None:
         return _on(stream, logits.get_device(), policy_loss_gradient, logits, targets, old_logp,
                    advantages, weights, ref_logp, clip_low, clip_high, kl_coef, scale, out)
-    kept = _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, clip_high,
+    return _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, clip_high,
                    kl_coef, scale, True, out)
-    return kept[0], kept[1], kept[5]
 
 
 def _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale, gradient, out):
-    """(loss, logps, lse, dlogp, rest, dlogits or None)"""
+    """(loss, logps, lse, dlogp, rest), or (loss, logps, dlogits)"""
     cols, code, device, rows, xs = _check_logits(logits, targets)
     if device != _current_device():
         return _on_device(device, _preference, logits, targets, ref_logps, starts, beta,
@@ -812,24 +834,25 @@ def _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale
         raise ValueError("without starts, logits must be (2 pairs, tokens, vocabulary)")
     else:
         pairs = logits.shape[0] // 2
-    if ref_logps is not None and (ref_logps.dtype != _F32 or ref_logps.shape != (2, pairs) or
+    if ref_logps is not None and (ref_logps.dtype is not _F32 or ref_logps.shape != (2, pairs) or
                                   not ref_logps.is_contiguous() or ref_logps.get_device() != device):
         raise ValueError("ref_logps must be dense float32 (2, pairs), on the logits' device")
     dx, ds = _gradient_of(logits, out, device, cols) if gradient else (None, 0)
     loss = torch.empty((), dtype=_F32, device=logits.device)
     logps = torch.empty((2, pairs), dtype=_F32, device=logits.device)
-    n = (rows + 3) // 4 * 4
-    lse, dlogp, rest, at = _row_buffers(targets, rows, 16 * pairs)
+    kept, n, at = _row_buffers(logits, rows, 16 * pairs)
     rc = vr.lib().vrPreferenceLoss(logits.data_ptr(), targets.data_ptr(), _ptr(ref_logps),
-                                   _ptr(starts), loss.data_ptr(), logps.data_ptr(), at,
-                                   lse.data_ptr(), rest.data_ptr(), dlogp.data_ptr(), _ptr(dx),
-                                   pairs, rows, cols, xs, ds, beta, label_smoothing, scale, code,
-                                   at + 4 * n, 16 * pairs, _raw_stream(device))
+                                   _ptr(starts), loss.data_ptr(), logps.data_ptr(), at + 12 * n, at,
+                                   at + 8 * n, at + 4 * n, _ptr(dx), pairs, rows, cols, xs, ds, beta,
+                                   label_smoothing, scale, code, at + 16 * n, 16 * pairs,
+                                   _raw_stream(device))
     if rc:
         raise vr.VrError(rc, "vrPreferenceLoss")
-    if out is not None:
-        _written(out)
-    return loss, logps, lse, dlogp, rest, dx
+    if gradient:
+        if out is not None:
+            _written(out)
+        return loss, logps, dx
+    return loss, logps, *_kept_rows(kept, n, targets)
 
 
 def preference_loss_forward(logits, targets, ref_logps=None, starts=None, beta=0.1,
@@ -859,8 +882,7 @@ def preference_loss_gradient(logits, targets, ref_logps=None, starts=None, beta=
     if stream is not None:
         return _on(stream, logits.get_device(), preference_loss_gradient, logits, targets, ref_logps,
                    starts, beta, label_smoothing, scale, out)
-    kept = _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale, True, out)
-    return kept[0], kept[1], kept[5]
+    return _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale, True, out)
 
 
 class _TokenLogProbs(torch.autograd.Function):
@@ -883,7 +905,7 @@ class _Loss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, targets, loss, *args):
         logits, targets = _as_rows(logits), targets.contiguous()
-        value, logp, lse, dlogp, rest, _ = loss(logits, targets, *args, False, None)
+        value, logp, lse, dlogp, rest = loss(logits, targets, *args, False, None)
         ctx.save_for_backward(logits, targets, lse, dlogp, rest)
         ctx.mark_non_differentiable(logp)
         ctx.rest = len(args)
