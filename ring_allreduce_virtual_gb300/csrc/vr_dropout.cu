@@ -366,14 +366,15 @@ vrResult_t run(DropArgs& a, cudaStream_t st) {
     if (a.head > a.cols) a.head = a.cols;
     a.slots = (a.cols - a.head) / 8;
     const bool shifted = (a.offset + a.head) % 8 != 0;
-    // Four units a thread, all loaded before the first is computed, where they fill the GPU
-    // at least twice; else one, on more SMs.
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    // 64 bytes of x a thread, all loaded before the first is computed, where they fill the GPU
+    // at least twice (96 where a block of the generator more is to be spread over them; with an
+    // addition they are too many registers); else one unit, on more SMs.
+    constexpr int U = 64 / (8 * (int)sizeof(T)), SU = ADD ? U : U * 3 / 2;
     const bool many = a.slots >= (uint64_t)kSMs * 8 * kThreads * 2;
-    const uint64_t each = (many ? U : 1) * kThreads;
+    const uint64_t each = (many ? (shifted ? SU : U) : 1) * kThreads;
     blocks = (a.slots + each - 1) / each;
     if (!blocks) blocks = 1;
-    k = many ? (shifted ? (const void*)&vrDropFlat<T, U, ADD, true, DEVICE>
+    k = many ? (shifted ? (const void*)&vrDropFlat<T, SU, ADD, true, DEVICE>
                         : (const void*)&vrDropFlat<T, U, ADD, false, DEVICE>)
              : (shifted ? (const void*)&vrDropFlat<T, 1, ADD, true, DEVICE>
                         : (const void*)&vrDropFlat<T, 1, ADD, false, DEVICE>);

@@ -42,6 +42,7 @@ struct LossArgs {
   // the kernel that keeps a row on chip
   int ctas;           // blocks of a row
   uint32_t part;      // packs of a block
+  bool eager;         // rows are copied before it is known whether they count
   // preferences
   const float* refSums;
   const int64_t* starts;
@@ -224,19 +225,43 @@ struct Joined {
   }
 };
 
+// The same over the blocks of a cluster, each of which has announced itself (arrive) before.
+struct Parts {
+  float m[8], s[8];
+  __device__ __forceinline__ static void arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  }
+  __device__ __forceinline__ void operator()(Online& o, int rank, int ctas) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the others are there
+    if ((int)threadIdx.x < ctas) {
+      store_remote(&m[rank], threadIdx.x, o.m);
+      store_remote(&s[rank], threadIdx.x, o.s);
+    }
+    cluster_sync();
+    o = Online{};
+    for (int i = 0; i < ctas; ++i) o.join(m[i], s[i]);
+  }
+};
+
 constexpr int kRowThreads = 256;
 
-// A block for each row, read once, the next packs on their way while the last are summed.
-template <typename T, int KIND>
+// A block for each row, or a warp for each of a block's, read once, the next packs on their
+// way while the last are summed.
+template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constant__ LossArgs a) {
   constexpr int U = 4;
   __shared__ Joined joined;
+  __shared__ Parts parts;
   begin_kernel();
   const int tid = threadIdx.x, threads = blockDim.x;
-  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  const int ctas = CLUSTER ? a.ctas : 1, rank = CLUSTER ? (int)cluster_rank() : 0;
+  if (CLUSTER) Parts::arrive();
+  for (uint64_t row = (uint64_t)(blockIdx.x / ctas) * blockDim.y + threadIdx.y; row < a.rows;
+       row += (uint64_t)(gridDim.x / ctas) * blockDim.y) {
     const int64_t target = a.target[row];
     if (skipped<KIND>(a, row, target)) {
-      if (tid == 0) skip_row<KIND>(a, row);
+      if (tid == 0 && rank == 0) skip_row<KIND>(a, row);
+      if (CLUSTER) return;  // one row a cluster
       continue;
     }
     const T* x = static_cast<const T*>(a.x) + row * a.stride;
@@ -246,11 +271,16 @@ __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constan
     Online o;
     const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + tid;
     int64_t left = (int64_t)cut.packs - tid;  // a pack of this thread is every threads-th
+    if (CLUSTER) {
+      const int64_t first = (int64_t)rank * a.part;
+      p += first;
+      left = ((int64_t)cut.packs - first < (int64_t)a.part ? (int64_t)cut.packs - first : (int64_t)a.part) - tid;
+    }
     uint4 v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k)
       if (k * threads < left) v[k] = p[k * threads];
-    const int64_t edge = cut.edge(tid, a.cols);
+    const int64_t edge = rank == 0 ? cut.edge(tid, a.cols) : -1;
     if (edge >= 0) o.add(to_f32(x[edge]));
     while (left > 0) {
       uint4 w[U];
@@ -266,7 +296,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constan
       left -= U * threads;
     }
     joined(o);
-    if (tid == 0) finish_row<KIND>(a, row, in, o.m, o.s);
+    if (CLUSTER) parts(o, rank, ctas);
+    if (tid == 0 && rank == 0) finish_row<KIND>(a, row, in, o.m, o.s);
+    if (CLUSTER) return;
     if (threads > 32) __syncthreads();
   }
 }
@@ -301,37 +333,34 @@ __device__ __forceinline__ void store_pack(T* p, const float (&e)[kV<T>], bool a
 
 // The logarithms and the gradient of a row in one pass over it: its packs are copied to
 // shared memory, each by the thread that reads it (no barrier between), summed as they
-// come, and read again there for the gradient. A row is a block's, or a cluster's, each
-// block with its part of it.
+// come, and read again there for the gradient. A row is a warp's, a block's, or a cluster's,
+// each block with its part of it.
+constexpr int kLossThreads = 128;
 template <typename T, int KIND, bool CLUSTER>
-__global__ void __launch_bounds__(kRowThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
+__global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_constant__ LossArgs a) {
   constexpr int V = kV<T>, GROUPS = 4;
-  extern __shared__ uint4 packs[];
+  extern __shared__ uint4 shared[];
   __shared__ Joined joined;
-  __shared__ float parts[2][8];  // the cluster's blocks'
-  __shared__ float4 result;
+  __shared__ Parts parts;
+  __shared__ float3 results[kLossThreads / 32];
   begin_kernel();
   const int tid = threadIdx.x, threads = blockDim.x;
   const int ctas = CLUSTER ? a.ctas : 1, rank = CLUSTER ? (int)cluster_rank() : 0;
-  if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  for (uint64_t row = blockIdx.x / ctas; row < a.rows; row += gridDim.x / ctas) {
-    const T* x = static_cast<const T*>(a.x) + row * a.stride;
-    T* dx = static_cast<T*>(a.dx) + row * a.dStride;
-    const int64_t target = a.target[row];
-    const Cut<T> cut(x, a.cols);
-    const int first = rank * (int)a.part, all = (int)cut.packs - first;
-    const int n = all < 0 ? 0 : all < (int)a.part ? all : (int)a.part;  // this block's packs
-    const int64_t edge = rank == 0 ? cut.edge(tid, a.cols) : -1;
-    T* const dp = dx + cut.head + (int64_t)first * V;
-    if (skipped<KIND>(a, row, target)) {
-      const float zero[V] = {};
-      for (int i = tid; i < n; i += threads) store_pack<T>(dp + (int64_t)i * V, zero, a.alike);
-      if (edge >= 0) dx[edge] = from_f32<T>(0.f);
-      if (tid == 0 && rank == 0) skip_row<KIND>(a, row);
-      continue;
-    }
-    const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + first;
-    const int each = ((n + threads - 1) / threads + GROUPS - 1) / GROUPS * threads;  // packs of a group
+  if (CLUSTER) Parts::arrive();
+  const uint64_t row = (uint64_t)(blockIdx.x / ctas) * blockDim.y + threadIdx.y;
+  if (row >= a.rows) return;
+  uint4* const packs = shared + threadIdx.y * a.part;
+  const T* x = static_cast<const T*>(a.x) + row * a.stride;
+  T* dx = static_cast<T*>(a.dx) + row * a.dStride;
+  const int64_t target = a.target[row];
+  const Cut<T> cut(x, a.cols);
+  const int first = rank * (int)a.part, all = (int)cut.packs - first;
+  const int n = all < 0 ? 0 : all < (int)a.part ? all : (int)a.part;  // this block's packs
+  const int64_t edge = rank == 0 ? cut.edge(tid, a.cols) : -1;
+  T* const dp = dx + cut.head + (int64_t)first * V;
+  const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + first;
+  const int each = ((n + threads - 1) / threads + GROUPS - 1) / GROUPS * threads;  // packs of a group
+  const auto fetch = [&]() {
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads)
@@ -341,68 +370,68 @@ __global__ void __launch_bounds__(kRowThreads, 4) vrRowLossGrads(const __grid_co
                      : "memory");
       copies_commit();
     }
-    RowIn in;
-    if (tid == 0) in.load<KIND>(a, row, x, target);
-    Online o;
-    float e = 0.f;
-    if (edge >= 0) {
-      e = to_f32(x[edge]);
-      o.add(e);
-    }
-    const auto sum = [&](int g) {
-      for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads) o.add<T>(packs[i]);
-    };
-    copies_wait<3>();
-    sum(0);
-    copies_wait<2>();
-    sum(1);
-    copies_wait<1>();
-    sum(2);
+  };
+  if (a.eager) fetch();
+  if (skipped<KIND>(a, row, target)) {
     copies_wait<0>();
-    sum(3);
-    joined(o);
-    if (CLUSTER) {
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the others are there
-      if (tid < ctas) {
-        store_remote(&parts[0][rank], tid, o.m);
-        store_remote(&parts[1][rank], tid, o.s);
-      }
-      cluster_sync();
-      o = Online{};
-      for (int i = 0; i < ctas; ++i) o.join(parts[0][i], parts[1][i]);
-    }
-    if (tid == 0) {
-      const float2 r = finish_row<KIND>(a, row, in, o.m, o.s, rank == 0);
-      result = make_float4(r.x, r.y, -r.y / o.s, 0.f);
-    }
-    __syncthreads();
-    const float lp = result.x, c = result.y, f = result.z;
-    // The target's element is c (1 - p) without the difference of two numbers near 1. Of a
-    // target that is none c is NaN.
-    const bool none = c == 0.f;
-    const int64_t t = target - cut.head - (int64_t)first * V;
-    const int targetPack = t >= 0 && t < (int64_t)n * V ? (int)(t / V) : -1;
-    for (int i = tid; i < n; i += threads) {
-      float d[V];
-      scaled_exps<T>(packs[i], o.m, 0.f, f, d);
-      if (i == targetPack) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j == (int)(t % V)) d[j] = -c * expm1f(lp);
-      }
-      if (none) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) d[j] = 0.f;
-      }
-      store_pack<T>(dp + (int64_t)i * V, d, a.alike);
-    }
-    if (edge >= 0)
-      dx[edge] = from_f32<T>(none             ? 0.f
-                             : edge == target ? -c * expm1f(lp)
-                                              : f * exp2_fast((e - o.m) * kLog2e));
-    if (CLUSTER) break;  // one row a cluster
-    __syncthreads();
+    const float zero[V] = {};
+    for (int i = tid; i < n; i += threads) store_pack<T>(dp + (int64_t)i * V, zero, a.alike);
+    if (edge >= 0) dx[edge] = from_f32<T>(0.f);
+    if (tid == 0 && rank == 0) skip_row<KIND>(a, row);
+    return;
   }
+  if (!a.eager) fetch();
+  RowIn in;
+  if (tid == 0) in.load<KIND>(a, row, x, target);
+  Online o;
+  float e = 0.f;
+  if (edge >= 0) {
+    e = to_f32(x[edge]);
+    o.add(e);
+  }
+  const auto sum = [&](int g) {
+    for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads) o.add<T>(packs[i]);
+  };
+  copies_wait<3>();
+  sum(0);
+  copies_wait<2>();
+  sum(1);
+  copies_wait<1>();
+  sum(2);
+  copies_wait<0>();
+  sum(3);
+  joined(o);
+  if (CLUSTER) parts(o, rank, ctas);
+  if (tid == 0) {
+    const float2 r = finish_row<KIND>(a, row, in, o.m, o.s, rank == 0);
+    results[threadIdx.y] = make_float3(r.x, r.y, -r.y / o.s);
+  }
+  if (threads == 32) __syncwarp();
+  else __syncthreads();
+  const float lp = results[threadIdx.y].x, c = results[threadIdx.y].y, f = results[threadIdx.y].z;
+  // The target's element is c (1 - p) without the difference of two numbers near 1. Of a
+  // target that is none c is NaN.
+  const bool none = c == 0.f;
+  const int64_t t = target - cut.head - (int64_t)first * V;
+  const int targetPack = t >= 0 && t < (int64_t)n * V ? (int)(t / V) : -1;
+  for (int i = tid; i < n; i += threads) {
+    float d[V];
+    scaled_exps<T>(packs[i], o.m, 0.f, f, d);
+    if (i == targetPack) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j == (int)(t % V)) d[j] = -c * expm1f(lp);
+    }
+    if (none) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) d[j] = 0.f;
+    }
+    store_pack<T>(dp + (int64_t)i * V, d, a.alike);
+  }
+  if (edge >= 0)
+    dx[edge] = from_f32<T>(none             ? 0.f
+                           : edge == target ? -c * expm1f(lp)
+                                            : f * exp2_fast((e - o.m) * kLog2e));
 }
 
 // dx from the rows' logarithms, read by an earlier kernel: a block takes some rows' parts,
@@ -419,10 +448,11 @@ __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant
   const T* x = static_cast<const T*>(a.x) + row * a.stride;
   T* dx = static_cast<T*>(a.dx) + row * a.dStride;
   const int64_t target = a.target[row];
-  float c = target < 0 ? 0.f : a.dlogp[row];
-  if (c != 0.f && a.gain) c *= *a.gain;  // a row of 0 stays one, whatever the gain is
+  float c = a.dlogp[row];
+  const float lse = a.lse[row], rest = a.rest ? a.rest[row] : 0.f, gain = a.gain ? *a.gain : 1.f;
+  if (target < 0) c = 0.f;
+  if (c != 0.f) c *= gain;  // a row of 0 stays one, whatever the gain is
   if (target >= (int64_t)a.cols && c != 0.f) c = __int_as_float(0x7fffffff);
-  const float lse = a.lse[row], rest = a.rest ? a.rest[row] : 0.f;
   const Cut<T> cut(x, a.cols);
   const uint64_t segment = blockIdx.x - line * a.segments;
   const bool none = c == 0.f;
@@ -480,14 +510,24 @@ constexpr int kOneBlock = 1024;
 
 // The sum of a value of each thread, in an order fixed by the lanes; the same in all.
 __device__ double block_total(double v) {
-  __shared__ double buf[kOneBlock / 32];
-  return block_sum<kOneBlock / 32>(v, buf);
+  __shared__ double buf[kOneBlock / 32], all;
+  static_assert(kOneBlock == 32 * 32, "a warp adds up the warps' sums");
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    v = warp_sum(buf[threadIdx.x]);
+    if (threadIdx.x == 0) all = v;
+  }
+  __syncthreads();
+  return all;
 }
 
 // The rows' losses added up.
 __global__ void __launch_bounds__(kOneBlock) vrLossSum(const __grid_constant__ LossArgs a) {
   begin_kernel();
   double s = 0.0;
+#pragma unroll 8
   for (uint64_t i = threadIdx.x; i < a.rows; i += kOneBlock) s += (double)a.rowLoss[i];
   s = block_total(s);
   if (threadIdx.x == 0) *a.loss = (float)(s * (double)a.scale);
@@ -513,6 +553,7 @@ __global__ void __launch_bounds__(kOneBlock) vrPairLosses(const __grid_constant_
     uint64_t from, to;
     range(s, from, to);
     double sum = 0.0;
+#pragma unroll 8
     for (uint64_t i = from + lane; i < to; i += 32) sum += (double)a.logp[i];
     sum = warp_sum(sum);
     if (lane == 0) {
@@ -561,12 +602,21 @@ vrResult_t dispatch(vrDataType_t t, F f) {
 
 template <typename T, int KIND>
 vrResult_t rowLogs(LossArgs& a, cudaStream_t st) {
-  // Eight packs a thread, up to 256 threads.
-  uint64_t threads = (a.cols / kV<T> / 8 + 31) / 32 * 32;
+  // Eight packs a thread, up to 256 threads; rows of a warp eight in a block. Few rows are
+  // clusters', in parts of 32 KB at least, up to the four blocks of an SM; the fewest in
+  // parts of 8 KB (200 x 32000 bf16 in clusters 5.9 us, without 5.2).
+  const uint64_t packs = a.cols / kV<T>;
+  int ctas = 1;
+  while (ctas < 8 && a.rows * ctas * 2 <= 4 * kSMs && packs / ctas >= (a.rows * ctas * 8 <= kSMs ? 1024 : 4096)) ctas *= 2;
+  const uint64_t part = (packs + ctas - 1) / ctas;
+  a.ctas = ctas;
+  a.part = (uint32_t)part;
+  uint64_t threads = (part / 8 + 31) / 32 * 32;
   threads = threads < 32 ? 32 : threads > kRowThreads ? kRowThreads : threads;
-  const uint64_t most = 1u << 20;
-  return launch((const void*)&vrRowLogs<T, KIND>, dim3((unsigned)(a.rows < most ? a.rows : most)),
-                dim3((unsigned)threads), 0, st, a);
+  const unsigned y = threads == 32 ? kRowThreads / 32 : 1;
+  const uint64_t groups = (a.rows + y - 1) / y, most = 1u << 20;
+  const void* k = ctas > 1 ? (const void*)&vrRowLogs<T, KIND, true> : (const void*)&vrRowLogs<T, KIND, false>;
+  return launch(k, dim3((unsigned)(groups < most ? groups : most) * ctas), dim3((unsigned)threads, y), 0, st, a, ctas);
 }
 
 template <typename T>
@@ -591,32 +641,35 @@ vrResult_t rowGrads(LossArgs& a, cudaStream_t st) {
   return launch((const void*)&vrRowGrads<T, 4>, dim3((unsigned)blocks), dim3(x, y), 0, st, a);
 }
 
-// Logarithms and gradient in one pass; false if a row is too large for a cluster.
+// Logarithms and gradient in one pass; false if a row is too large for a cluster. Parts of
+// 36 KB, of which an SM holds six, each at another point of its way (131072 bf16 358 us, of
+// 72 KB and three 377; 50257 float32 238 and 246).
 constexpr size_t kMostShared = 200 * 1024;
 template <typename T, int KIND>
 bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
   alikeRows<T>(a);
   const uint64_t packs = a.cols / kV<T> ? a.cols / kV<T> : 1;
-  constexpr uint64_t kBest = 72 * 1024 / 16, kLargest = kMostShared / 16;
+  constexpr uint64_t kBest = 36 * 1024 / 16, kLargest = kMostShared / 16;
   int ctas = 1;
   while (ctas < 8 && (packs + ctas - 1) / ctas > kBest) ctas *= 2;
-  // Few rows are spread over more SMs, in parts of 8 KB at least.
-  while (ctas < 8 && a.rows * ctas < 2 * kSMs && packs / ctas >= 1024) ctas *= 2;
+  // Few rows are spread over more SMs, in parts of 8 KB at least, up to six blocks on each.
+  while (ctas < 8 && a.rows * ctas * 2 <= 6 * kSMs && packs / ctas >= 1024) ctas *= 2;
   const uint64_t part = (packs + ctas - 1) / ctas;
-  if (part > kLargest || a.rows * ctas > 0x7fffffffu) return false;
+  uint64_t threads = (part / 8 + 31) / 32 * 32;
+  threads = threads < 32 ? 32 : threads > kLossThreads ? kLossThreads : threads;
+  const unsigned y = threads == 32 ? kLossThreads / 32 : 1;
+  const uint64_t blocks = (a.rows + y - 1) / y * ctas;
+  if (part > kLargest || blocks > 0x7fffffffu) return false;
   a.ctas = ctas;
   a.part = (uint32_t)part;
-  uint64_t threads = (part / 8 + 31) / 32 * 32;
-  threads = threads < 32 ? 32 : threads > kRowThreads ? kRowThreads : threads;
-  const uint64_t rowsEach = ctas > 1 ? 1 : (1024 + part - 1) / part;  // 16 KB a block
-  const uint64_t blocks = (a.rows + rowsEach - 1) / rowsEach * ctas;
+  a.eager = blocks <= 6 * kSMs;  // a microsecond less where there is only one round
   const void* k = ctas > 1 ? (const void*)&vrRowLossGrads<T, KIND, true> : (const void*)&vrRowLossGrads<T, KIND, false>;
   if (!setOnce(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostShared) ||
       !setOnce(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared)) {
     *r = vrCudaError;
     return true;
   }
-  *r = launch(k, dim3((unsigned)blocks), dim3((unsigned)threads), part * 16, st, a, ctas);
+  *r = launch(k, dim3((unsigned)blocks), dim3((unsigned)threads, y), part * 16 * y, st, a, ctas);
   return true;
 }
 

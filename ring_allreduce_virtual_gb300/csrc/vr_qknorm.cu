@@ -136,6 +136,57 @@ struct Angles {
   }
 };
 
+// The same with a kind's weights and one factor for the whole head: three operations for two
+// elements, where weights, factor and turn one after the other are nine for four.
+template <typename T, bool INTER>
+struct WeightedAngles {
+  static constexpr int V = kV<T>, H = V / 2;
+  F2 p[H], q[H], s[H], t[H];
+  __device__ __forceinline__ void load(const Packs<T, INTER>& at, const float* cosRow, const float* sinRow, int half,
+                                       const float* w) {
+    const float one[2] = {1.f, 1.f};
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const float* wa = at.hasA ? w + at.a + 2 * i : one;
+      const float* wb = at.hasB ? w + at.b + 2 * i : one;
+      if constexpr (INTER) {
+        const int k = at.a / 2 + i, l = at.b / 2 + i;
+        const bool inA = at.hasA && k < half, inB = at.hasB && l < half;
+        const float ca = inA ? cosRow[k] : 1.f, sn = inA ? sinRow[k] : 0.f;
+        const float cb = inB ? cosRow[l] : 1.f, sm = inB ? sinRow[l] : 0.f;
+        p[i] = f2(wa[0], wa[1]) * f2(ca);
+        q[i] = f2(wa[1], wa[0]) * f2(-sn, sn);
+        s[i] = f2(wb[0], wb[1]) * f2(cb);
+        t[i] = f2(wb[1], wb[0]) * f2(-sm, sm);
+      } else {
+        const bool in = at.a < half;
+        const F2 c = in ? f2(cosRow[at.a + 2 * i], cosRow[at.a + 2 * i + 1]) : f2(1.f);
+        const F2 n = in ? f2(sinRow[at.a + 2 * i], sinRow[at.a + 2 * i + 1]) : f2(0.f);
+        p[i] = f2(wa[0], wa[1]) * c;
+        q[i] = f2(wb[0], wb[1]) * n;
+        s[i] = f2(wb[0], wb[1]) * c;
+        t[i] = f2(wa[0], wa[1]) * n;
+      }
+    }
+  }
+  __device__ __forceinline__ void turn(F2 (&x)[H], F2 (&y)[H], F2 r) const {
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      if constexpr (INTER) {
+        float a, b;
+        split(x[i], a, b);
+        x[i] = fma2(f2(b, a), q[i], x[i] * p[i]) * r;
+        split(y[i], a, b);
+        y[i] = fma2(f2(b, a), t[i], y[i] * s[i]) * r;
+      } else {
+        const F2 a = x[i];
+        x[i] = (a * p[i] - y[i] * q[i]) * r;
+        y[i] = fma2(a, t[i], y[i] * s[i]) * r;
+      }
+    }
+  }
+};
+
 // A warp's steps, token after token. First whole tokens, the warps' next to each other in
 // memory; then what is left of the tokens shared out by steps, so that all warps end at
 // the same time.
@@ -308,33 +359,40 @@ __global__ void __launch_bounds__(kThreads, kBlocks<BACK>) vrQkHeads(const __gri
     for (int i = 0; i < H; ++i) sa[0][i] = sb[0][i] = sa[1][i] = sb[1][i] = f2(0.f);
   }
   const float mean = 1.f / (float)a.dim;
-  Angles<T, INTER, BACK> angles;
+  std::conditional_t<BACK, Angles<T, INTER, true>, WeightedAngles<T, INTER>> angles;
   int stage = 0;
-  uint32_t from = 0;
-  bool first;
+  uint32_t from = 0;  // the next token's place among the tables' rows
+  bool first;         // of the token's steps here
   // Steps [now.step, end) of the present token, which are of one kind.
   const auto run = [&](auto kindOf, uint32_t end) {
     constexpr int kind = decltype(kindOf)::value;
     uint32_t head = (now.step - (kind ? keys : 0)) * U * groups + group;
     T* op = place<T>(a.out[kind], Token(a, now.token), head);
     const uint64_t oStep = groups * a.out[kind].head;
-    F2 wa[H], wb[H];
+    [[maybe_unused]] F2 wa[H], wb[H];
+    if (BACK) {
 #pragma unroll
-    for (int i = 0; i < H; ++i) {
-      const float* p = w + kind * a.dim;
-      wa[i] = at.hasA ? f2(p[at.a + 2 * i], p[at.a + 2 * i + 1]) : f2(1.f);
-      wb[i] = at.hasB ? f2(p[at.b + 2 * i], p[at.b + 2 * i + 1]) : f2(1.f);
+      for (int i = 0; i < H; ++i) {
+        const float* p = w + kind * a.dim;
+        wa[i] = at.hasA ? f2(p[at.a + 2 * i], p[at.a + 2 * i + 1]) : f2(1.f);
+        wb[i] = at.hasB ? f2(p[at.b + 2 * i], p[at.b + 2 * i + 1]) : f2(1.f);
+      }
     }
+    bool load = first || !BACK;  // the angles, forward each kind's with its weights
 #pragma unroll 1
     for (; now.step < end; ++now.step) {
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
-      if (first) {
-        first = false;
-        __syncwarp();  // the row was copied by all lanes
-        const float* r = rows + from * 2 * half;
-        angles.load(at, r, r + half, half);
-        from = from + 1 == kStages ? 0 : from + 1;
+      if (load) {
+        load = false;
+        if (first) {
+          first = false;
+          __syncwarp();  // the row was copied by all lanes
+          from = from + 1 == kStages ? 0 : from + 1;
+        }
+        const float* r = rows + (from == 0 ? kStages - 1 : from - 1) * 2 * half;
+        if constexpr (BACK) angles.load(at, r, r + half, half);
+        else angles.load(at, r, r + half, half, w + kind * a.dim);
       }
       const uint4* in = ring + stage * (U * NP * 32);
       stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -387,12 +445,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<BACK>) vrQkHeads(const __gri
             }
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < H; ++i) {
-            fa[u][i] = fa[u][i] * r2 * wa[i];
-            fb[u][i] = fb[u][i] * r2 * wb[i];
-          }
-          angles.turn(fa[u], fb[u]);
+          angles.turn(fa[u], fb[u], r2);
         }
         if (mine) {
           if (at.hasA) *reinterpret_cast<uint4*>(op + at.a) = pack<T>(fa[u]);
