@@ -673,7 +673,10 @@ bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
   return true;
 }
 
-bool sizesOk(uint64_t rows, uint64_t cols) { return cols >= 1 && cols <= kMost && rows <= kMost / cols; }
+// Rows up to 2^32: eight of them or more are a block's where they are narrow.
+bool sizesOk(uint64_t rows, uint64_t cols) {
+  return cols >= 1 && cols <= kMost && rows <= kMost / cols && rows <= 1ull << 32;
+}
 
 }  // namespace
 

@@ -742,7 +742,7 @@ bool layOut(QkArgs& a, bool backward) {
   while (a.lanes < a.pairs) a.lanes *= 2;
   a.wideTable = (((uintptr_t)a.cos | (uintptr_t)a.sin | a.rot * 2) & 15) == 0;
   // Batches whose tokens follow one another are one.
-  bool one = !a.rot || a.positionStride == a.tokens;
+  bool one = a.all != a.tokens && (!a.rot || a.positionStride == a.tokens);
   for (int k = 0; k < 2; ++k)
     for (const Side* s : {&a.x[k], &a.dy[k], &a.out[k]}) one = one && (!s->p || s->batch == a.tokens * s->token);
   if (one) a.tokens = a.all;
@@ -773,6 +773,11 @@ vrResult_t wholeHeads(QkArgs& a, cudaStream_t st) {
       !setOnce(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared))
     return vrCudaError;
   return launch(f, dim3(a.blocks), dim3(kThreads), smem, st, a);
+}
+
+// An argument for the kernels; what the stride of an axis of one element is does not matter.
+Side sideOf(const void* p, size_t heads, const size_t* st, const Shape& s) {
+  return {p, s.batch > 1 ? st[0] : 0, s.tokens > 1 ? st[1] : 0, heads > 1 ? st[2] : 0};
 }
 
 struct Call {
@@ -811,9 +816,8 @@ vrResult_t begin(Call& c, const void* q, size_t qHeads, const size_t* qStrides, 
     c.a.wide = wide;
   }
   QkArgs& a = c.a;
-  const auto side = [](const void* p, const size_t* st) { return p ? Side{p, st[0], st[1], st[2]} : Side{}; };
-  a.x[0] = side(q, qStrides);
-  if (kHeads) a.x[1] = side(k, kStrides);
+  a.x[0] = sideOf(q, qHeads, qStrides, c.s);
+  if (kHeads) a.x[1] = sideOf(k, kHeads, kStrides, c.s);
   a.w[0] = qWeight, a.w[1] = kWeight;
   a.heads[0] = (uint32_t)qHeads, a.heads[1] = (uint32_t)kHeads;
   a.cos = cosTable, a.sin = sinTable, a.tableRows = tableRows;
@@ -857,8 +861,8 @@ extern "C" VR_API vrResult_t vrQkNormRopeForward(
   if (badSide(qOut, qHeads, qOutStrides, c.s, c.es, true) ||
       (kHeads && badSide(kOut, kHeads, kOutStrides, c.s, c.es, true)))
     return vrInvalidArgument;
-  a.out[0] = {qOut, qOutStrides[0], qOutStrides[1], qOutStrides[2]};
-  if (kHeads) a.out[1] = {kOut, kOutStrides[0], kOutStrides[1], kOutStrides[2]};
+  a.out[0] = sideOf(qOut, qHeads, qOutStrides, c.s);
+  if (kHeads) a.out[1] = sideOf(kOut, kHeads, kOutStrides, c.s);
   // In place is allowed, each for itself.
   Bytes in[7];
   const int n = inputs(c, in);
@@ -903,7 +907,7 @@ extern "C" VR_API vrResult_t vrQkNormRopeBackward(
                               tableRows, positions, positionType, positionStride, batch, tokens, dim, rotaryDim,
                               interleaved, eps, dtype, weightType);
   if (rc != vrSuccess) return rc;
-  if (misaligned(dqWeight, c.ws) || misaligned(dkWeight, c.ws) || (!kHeads && dkWeight)) return vrInvalidArgument;
+  if (misaligned(dqWeight, c.ws) || misaligned(dkWeight, c.ws)) return vrInvalidArgument;
   cudaStream_t st = (cudaStream_t)stream;
   if (c.nothing) {  // sums over no tokens
     for (void* p : {dqWeight, dkWeight})
@@ -920,11 +924,11 @@ extern "C" VR_API vrResult_t vrQkNormRopeBackward(
                   badSide(dkIn, kHeads, dkInStrides, c.s, c.es, true))) ||
       (params && (!workspace || misaligned(workspace, 16) || workspaceBytes < workspaceOf(dim))))
     return vrInvalidArgument;
-  a.dy[0] = {dq, dqStrides[0], dqStrides[1], dqStrides[2]};
-  a.out[0] = {dqIn, dqInStrides[0], dqInStrides[1], dqInStrides[2]};
+  a.dy[0] = sideOf(dq, qHeads, dqStrides, c.s);
+  a.out[0] = sideOf(dqIn, qHeads, dqInStrides, c.s);
   if (kHeads) {
-    a.dy[1] = {dk, dkStrides[0], dkStrides[1], dkStrides[2]};
-    a.out[1] = {dkIn, dkInStrides[0], dkInStrides[1], dkInStrides[2]};
+    a.dy[1] = sideOf(dk, kHeads, dkStrides, c.s);
+    a.out[1] = sideOf(dkIn, kHeads, dkInStrides, c.s);
   }
   a.dw[0] = dqWeight, a.dw[1] = dkWeight;
   a.partials = params ? (float*)workspace : nullptr;

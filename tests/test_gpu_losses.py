@@ -362,6 +362,20 @@ def test_preference_of_padded_batches():
         training.preference_loss_gradient(x[:20].view(5, 4, 200), t[:20].view(5, 4), refs)
 
 
+def test_pairs_of_no_rows():
+    # both sequences empty: S = 0, the margin is the references' alone
+    x, t = torch.empty(0, 50, device="cuda"), torch.empty(0, device="cuda", dtype=torch.int64)
+    refs = torch.tensor([[3.0], [1.0]], device="cuda")
+    for args in ((x, t, refs, torch.zeros(3, device="cuda", dtype=torch.int64)), (x.view(2, 0, 50), t.view(2, 0), refs)):
+        loss, logps, dlogits = training.preference_loss_gradient(*args, beta=0.5)
+        assert abs(float(loss) - math.log1p(math.exp(1.0))) <= 1e-6 and bool((logps == 0).all()) and dlogits.shape == args[0].shape
+
+
+def test_one_row_without_axes():
+    x, t, g = make(13, 1, 77, torch.float16)
+    assert same(training.token_logprobs_forward(x[0], t[0])[0], training.token_logprobs_forward(x, t)[0][0])
+
+
 def test_starts_that_are_no_ranges_stay_inside():
     # cut at the rows that there are; a sequence whose end is not behind its start is empty
     x, t, g = make(5, 10, 64, torch.float32)

@@ -205,6 +205,24 @@ def test_no_tokens():
         assert bool((got[2] == 0).all()) and bool((got[3] == 0).all())
 
 
+def test_no_keys():
+    q = torch.randn(3, 4, 16, device="cuda")
+    k = q[:, :0]
+    yq, yk = training.qk_norm_rope_forward(q, k)
+    assert yk.shape == (3, 0, 16) and same(yq, training.qk_norm_rope_forward(q, None)[0])
+    got = training.qk_norm_rope_backward(yq, yk, q, k)
+    assert got[1].shape == (3, 0, 16) and bool((got[3] == 0).all())
+    assert same(got[0], training.qk_norm_rope_backward(yq, None, q, None)[0])
+
+
+def test_strides_of_axes_of_one_element_do_not_matter():
+    q = torch.randn(2, 1, 3, 64, device="cuda").bfloat16()
+    t = q.as_strided(q.shape, (192, 7, 64, 1))
+    assert all(same(a, b) for a, b in zip(training.qk_norm_rope_forward(q, q.clone())[:2], training.qk_norm_rope_forward(t, t.clone())))
+    one = torch.randn(1, 1, 1, 64, device="cuda").as_strided((1, 1, 1, 64), (3, 5, 7, 1))
+    check_forward(training.qk_norm_rope_forward(one, None)[0], one, None, (None, None), None, False)
+
+
 def test_gradients_against_differences():
     # the outputs' sum against dy along random directions, in steps of 2^-7: the third derivative of a head's
     # norm is below 16 / |x|^2 of its first, rounding is 2^-24 / 2^-7 of the outputs

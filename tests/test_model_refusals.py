@@ -91,7 +91,7 @@ QKB = dict(dq=8 * A, dqStrides=S, dk=9 * A, dkStrides=S, q=A, qHeads=8, qStrides
 @pytest.mark.parametrize("bad", [
     {"dq": 0}, {"dk": 0}, {"q": 0}, {"dqIn": 0}, {"dkIn": 0}, {"dqStrides": None}, {"dkInStrides": None},
     {"dqWeight": 10 * A + 1}, {"dkWeight": 11 * A + 1}, {"workspace": 0}, {"workspace": 64 * A + 8},
-    {"workspaceBytes": 64}, {"kHeads": 0}, {"dq": 8 * A + 1}, {"dqInStrides": (1024, 128, 15)},
+    {"workspaceBytes": 64}, {"dq": 8 * A + 1}, {"dqInStrides": (1024, 128, 15)},
     {"dqIn": A}, {"dkIn": 2 * A}, {"dqIn": 9 * A}, {"dkIn": 8 * A}, {"dqIn": 8 * A + 32}, {"dqWeight": 3 * A},
     {"dkWeight": 10 * A + 30}, {"workspace": 8 * A}, {"workspace": A}, {"dqIn": 5 * A}, {"dkIn": 64 * A},
     {"dqWeight": 8 * A}, {"dkWeight": 64 * A + 16},
@@ -196,3 +196,70 @@ def test_torch_layer_refuses_host_tensors():
                  lambda: training.preference_loss_forward(x, t, starts=torch.zeros(3, dtype=torch.int64))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_launches_on_the_tensors_device_and_stream(monkeypatch):
+    # tensors that say they are on a second device, a library that records where it is called
+    import contextlib
+    import types
+
+    class OnSecond(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cpu")  # where the allocations of this test go
+
+        def get_device(self):
+            return 1
+
+    state, seen = {"device": 0, "stream": None}, []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: (None if "Workspace" in name else seen.append((name, state["device"], a[-1]))) or 0
+
+    @contextlib.contextmanager
+    def device(index):
+        was, state["device"] = state["device"], index
+        yield
+        state["device"] = was
+
+    @contextlib.contextmanager
+    def stream(s):
+        was = dict(state)
+        state.update(device=s.device_index, stream=s)
+        yield
+        state.update(was)
+
+    monkeypatch.setattr(training.vr, "lib", lambda: Library())
+    monkeypatch.setattr(training, "_raw_stream", lambda i: state["stream"].handle if state["stream"] else 100 + i)
+    monkeypatch.setattr(training, "_current_device", lambda: state["device"])
+    monkeypatch.setattr(training, "_qk_workspace", lambda dim: 1024)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+
+    def on(t):
+        return t.as_subclass(OnSecond)
+    x, v, t = on(torch.zeros(4, 8)), on(torch.zeros(4)), on(torch.zeros(4, dtype=torch.int64))
+    q, starts = on(torch.zeros(3, 2, 8)), on(torch.tensor([0, 2, 4]))
+
+    def calls(**kw):
+        yield "vrDropout", lambda: training.dropout_forward(x, 0.1, 1, **kw)
+        yield "vrDropout", lambda: training.dropout_backward(x, 0.1, 1, **kw)
+        yield "vrQkNormRopeForward", lambda: training.qk_norm_rope_forward(q, q, **kw)
+        yield "vrQkNormRopeBackward", lambda: training.qk_norm_rope_backward(q, q, q, q, **kw)
+        yield "vrTokenLogProbsForward", lambda: training.token_logprobs_forward(x, t, **kw)
+        yield "vrTokenLogProbsBackward", lambda: training.token_logprobs_backward(v, x, t, v, **kw)
+        yield "vrPolicyLoss", lambda: training.policy_loss_forward(x, t, v, v, **kw)
+        yield "vrPolicyLoss", lambda: training.policy_loss_gradient(x, t, v, v, **kw)
+        yield "vrPreferenceLoss", lambda: training.preference_loss_forward(x, t, starts=starts, **kw)
+        yield "vrPreferenceLoss", lambda: training.preference_loss_gradient(x, t, starts=starts, **kw)
+    for name, call in calls():
+        call()
+        assert seen[-1] == (name, 1, 101) and state["device"] == 0
+    for name, call in calls(stream=types.SimpleNamespace(device_index=1, handle=77)):
+        call()
+        assert seen[-1] == (name, 1, 77) and state["device"] == 0
+    count = len(seen)
+    for _, call in calls(stream=types.SimpleNamespace(device_index=0, handle=77)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert len(seen) == count
