@@ -43,6 +43,7 @@ struct LossArgs {
   int ctas;           // blocks of a row
   uint32_t part;      // packs of a block
   bool eager;         // rows are copied before it is known whether they count
+  uint32_t c65536;    // 65536
   // preferences
   const float* refSums;
   const int64_t* starts;
@@ -77,26 +78,46 @@ struct Online {
     raise(x);
     s += exp2_fast((x - m) * kLog2e);
   }
-  template <typename T>
-  __device__ __forceinline__ void add(const uint4& v) {
-    constexpr int V = kV<T>;
-    F2 f[V / 2];
-    float e[V];
-    unpack<T>(v, f);
+  // U packs, whose largest element is found first, of 16-bit types two at a time.
+  template <typename T, int U>
+  __device__ __forceinline__ void add(const uint4 (&v)[U], uint32_t c65536) {
+    constexpr int V = kV<T>, H = V / 2;
+    F2 f[U][H];
+    float top;
+    if constexpr (sizeof(T) == 2) {
+      using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+      T2 most[U * 4];
+      memcpy(most, v, sizeof(most));
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) split(f[i], e[2 * i], e[2 * i + 1]);
-    float top = e[0];
+      for (int n = U * 2; n; n >>= 1)
 #pragma unroll
-    for (int i = 1; i < V; ++i) top = fmaxf(top, e[i]);
+        for (int i = 0; i < n; ++i) most[i] = __hmax2(most[i], most[i + n]);
+      top = fmaxf(to_f32(most[0].x), to_f32(most[0].y));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) unpack<T>(v[u], c65536, f[u]);
+    if constexpr (sizeof(T) == 4) {
+      top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          float p, q;
+          split(f[u][i], p, q);
+          top = fmaxf(top, fmaxf(p, q));
+        }
+    }
     raise(top);
     const F2 less = f2(-m), scale = f2(kLog2e);
     F2 sum = f2(0.f);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      float p, q;
-      split((f[i] + less) * scale, p, q);
-      sum = sum + f2(exp2_fast(p), exp2_fast(q));
-    }
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        float p, q;
+        split((f[u][i] + less) * scale, p, q);
+        sum = sum + f2(exp2_fast(p), exp2_fast(q));
+      }
     s += both(sum);
   }
   __device__ __forceinline__ void join(float m2, float s2) {
@@ -276,25 +297,35 @@ __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constan
       p += first;
       left = ((int64_t)cut.packs - first < (int64_t)a.part ? (int64_t)cut.packs - first : (int64_t)a.part) - tid;
     }
-    uint4 v[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (k * threads < left) v[k] = p[k * threads];
     const int64_t edge = rank == 0 ? cut.edge(tid, a.cols) : -1;
     if (edge >= 0) o.add(to_f32(x[edge]));
-    while (left > 0) {
-      uint4 w[U];
+    uint4 v[U];
+    if (left > (U - 1) * threads) {
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if ((k + U) * threads < left) w[k] = p[(k + U) * threads];
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (k * threads < left) o.add<T>(v[k]);
-#pragma unroll
-      for (int k = 0; k < U; ++k) v[k] = w[k];
+      for (int k = 0; k < U; ++k) v[k] = p[k * threads];
       p += U * threads;
       left -= U * threads;
+      while (left > (U - 1) * threads) {
+        uint4 w[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) w[k] = p[k * threads];
+        o.add<T>(v, a.c65536);
+#pragma unroll
+        for (int k = 0; k < U; ++k) v[k] = w[k];
+        p += U * threads;
+        left -= U * threads;
+      }
+      o.add<T>(v, a.c65536);
     }
+#pragma unroll
+    for (int k = 0; k < U - 1; ++k)
+      if (k * threads < left) v[k] = p[k * threads];
+#pragma unroll
+    for (int k = 0; k < U - 1; ++k)
+      if (k * threads < left) {
+        const uint4 one[1] = {v[k]};
+        o.add<T>(one, a.c65536);
+      }
     joined(o);
     if (CLUSTER) parts(o, rank, ctas);
     if (tid == 0 && rank == 0) finish_row<KIND>(a, row, in, o.m, o.s);
@@ -303,18 +334,34 @@ __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constan
   }
 }
 
-// f exp(x - m - rest) of a pack's elements.
+// f exp(x - m - rest) of a pack's elements. Results of 16 bits take |f| and rest in the
+// exponent, where they cost nothing (off by 2^-20 of the result), and f's sign afterwards.
+struct Factor {
+  float m, add, f;
+  uint32_t sign;
+  template <typename T>
+  __device__ __forceinline__ static Factor of(float m, float rest, float f) {
+    if constexpr (sizeof(T) == 4) return {m, -rest, f, 0};
+    return {m, fmaf(-rest, kLog2e, __log2f(fabsf(f))), f, __float_as_uint(f) & 0x80000000u};
+  }
+};
 template <typename T>
-__device__ __forceinline__ void scaled_exps(const uint4& v, float m, float rest, float f, float (&e)[kV<T>]) {
+__device__ __forceinline__ void scaled_exps(const uint4& v, const Factor& k, uint32_t c65536, float (&e)[kV<T>]) {
   constexpr int V = kV<T>;
   F2 x[V / 2];
-  unpack<T>(v, x);
-  const F2 less = f2(-m), less2 = f2(-rest), scale = f2(kLog2e);
+  unpack<T>(v, c65536, x);
+  const F2 less = f2(-k.m), add = f2(k.add), scale = f2(kLog2e);
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) {
     float p, q;
-    split((x[i] + less + less2) * scale, p, q);
-    split(f2(exp2_fast(p), exp2_fast(q)) * f2(f), e[2 * i], e[2 * i + 1]);
+    if constexpr (sizeof(T) == 4) {
+      split((x[i] + less + add) * scale, p, q);
+      split(f2(exp2_fast(p), exp2_fast(q)) * f2(k.f), e[2 * i], e[2 * i + 1]);
+    } else {
+      split(fma2(x[i] + less, scale, add), p, q);
+      e[2 * i] = __uint_as_float(__float_as_uint(exp2_fast(p)) ^ k.sign);
+      e[2 * i + 1] = __uint_as_float(__float_as_uint(exp2_fast(q)) ^ k.sign);
+    }
   }
 }
 template <typename T>
@@ -360,14 +407,14 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
   T* const dp = dx + cut.head + (int64_t)first * V;
   const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + first;
   const int each = ((n + threads - 1) / threads + GROUPS - 1) / GROUPS * threads;  // packs of a group
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(packs);
   const auto fetch = [&]() {
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
-      for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(packs + i)),
-                     "l"(p + i)
-                     : "memory");
+      const int end = min(n, (g + 1) * each);
+#pragma unroll 4
+      for (int i = g * each + tid; i < end; i += threads)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(p + i) : "memory");
       copies_commit();
     }
   };
@@ -390,7 +437,16 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
     o.add(e);
   }
   const auto sum = [&](int g) {
-    for (int i = g * each + tid; i < n && i < (g + 1) * each; i += threads) o.add<T>(packs[i]);
+    const int end = min(n, (g + 1) * each);
+    int i = g * each + tid;
+    for (; i + 3 * threads < end; i += 4 * threads) {
+      const uint4 four[4] = {packs[i], packs[i + threads], packs[i + 2 * threads], packs[i + 3 * threads]};
+      o.add<T>(four, a.c65536);
+    }
+    for (; i < end; i += threads) {
+      const uint4 one[1] = {packs[i]};
+      o.add<T>(one, a.c65536);
+    }
   };
   copies_wait<3>();
   sum(0);
@@ -412,11 +468,12 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
   // The target's element is c (1 - p) without the difference of two numbers near 1. Of a
   // target that is none c is NaN.
   const bool none = c == 0.f;
+  const Factor factor = Factor::of<T>(o.m, 0.f, f);
   const int64_t t = target - cut.head - (int64_t)first * V;
   const int targetPack = t >= 0 && t < (int64_t)n * V ? (int)(t / V) : -1;
-  for (int i = tid; i < n; i += threads) {
+  const auto gradient = [&](int i, const uint4& v) {
     float d[V];
-    scaled_exps<T>(packs[i], o.m, 0.f, f, d);
+    scaled_exps<T>(v, factor, a.c65536, d);
     if (i == targetPack) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
@@ -427,7 +484,16 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
       for (int j = 0; j < V; ++j) d[j] = 0.f;
     }
     store_pack<T>(dp + (int64_t)i * V, d, a.alike);
+  };
+  int i = tid;
+  for (; i + 3 * threads < n; i += 4 * threads) {  // four chains side by side
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = packs[i + u * threads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) gradient(i + u * threads, v[u]);
   }
+  for (; i < n; i += threads) gradient(i, packs[i]);
   if (edge >= 0)
     dx[edge] = from_f32<T>(none             ? 0.f
                            : edge == target ? -c * expm1f(lp)
@@ -473,6 +539,7 @@ __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant
     for (uint64_t i = first; i < end; i += threads) store_pack<T>(dp + i * V, zero, a.alike);
     return;
   }
+  const Factor factor = Factor::of<T>(lse, rest, -c);
   uint4 v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -487,7 +554,7 @@ __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant
       const uint64_t i = i0 + u * threads;
       if (i >= end) break;
       float d[V];
-      scaled_exps<T>(v[u], lse, rest, -c, d);
+      scaled_exps<T>(v[u], factor, a.c65536, d);
       const int64_t t = target - cut.head - (int64_t)(i * V);
       if (t >= 0 && t < V) {
         F2 f[V / 2];
@@ -695,6 +762,7 @@ extern "C" VR_API vrResult_t vrTokenLogProbsForward(const void* logits, const in
   if (anyOverlap(outs, 3, ins, 2)) return vrInvalidArgument;
   LossArgs a;
   memset(&a, 0, sizeof(a));
+  a.c65536 = 65536;
   a.x = logits, a.target = targets, a.logp = logp, a.lse = lse, a.rest = rest;
   a.rows = rows, a.cols = cols, a.stride = stride;
   return dispatch(dtype, [&](auto t) { return rowLogs<decltype(t), LOGP>(a, (cudaStream_t)stream); });
@@ -719,6 +787,7 @@ extern "C" VR_API vrResult_t vrTokenLogProbsBackward(const float* dlogp, const f
   if (anyOverlap(outs, 1, ins, 6)) return vrInvalidArgument;
   LossArgs a;
   memset(&a, 0, sizeof(a));
+  a.c65536 = 65536;
   a.x = logits, a.dx = dlogits, a.target = targets, a.lse = const_cast<float*>(lse), a.rest = const_cast<float*>(rest);
   a.dlogp = dlogp, a.gain = gain;
   a.rows = rows, a.cols = cols, a.stride = stride, a.dStride = dStride;
@@ -744,6 +813,7 @@ extern "C" VR_API vrResult_t vrPolicyLoss(const void* logits, const int64_t* tar
   cudaStream_t st = (cudaStream_t)stream;
   LossArgs a;
   memset(&a, 0, sizeof(a));
+  a.c65536 = 65536;
   a.loss = loss, a.scale = scale, a.rows = rows, a.cols = cols;
   if (rows) {
     const int es = elemSizeOf(dtype);
@@ -819,6 +889,7 @@ extern "C" VR_API vrResult_t vrPreferenceLoss(const void* logits, const int64_t*
     if (overlap(outs[i], x)) return vrInvalidArgument;
   LossArgs a;
   memset(&a, 0, sizeof(a));
+  a.c65536 = 65536;
   a.x = logits, a.dx = dlogits, a.target = targets, a.rows = rows, a.cols = cols, a.stride = stride, a.dStride = dStride;
   a.logp = logp, a.lse = lse, a.rest = rest, a.coef = dlogp, a.dlogp = dlogp;
   a.loss = loss, a.seqLogp = logps, a.refSums = refLogps, a.starts = starts, a.sums = (double*)workspace;

@@ -106,6 +106,20 @@ __device__ __forceinline__ uint4 pack(const F2* f) {
   return v;
 }
 
+// The same with bfloat16's lower elements by a product (c65536, which the compiler must not
+// know: an argument of the launch), for kernels whose time is that of the pipe that shifts,
+// compares and selects.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, uint32_t c65536, F2* f) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] * c65536), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+    unpack<T>(v, f);
+  }
+}
+
 // Copies to shared memory on their way (cp.async): a group of them, and the wait for all
 // but the last N groups.
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
