@@ -127,6 +127,13 @@ struct Online {
   }
 };
 
+// A pack of elements that add nothing.
+template <typename T>
+__device__ __forceinline__ uint4 nothing() {
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same_v<T, __half> ? 0xfc00fc00u : 0xff80ff80u;
+  return make_uint4(w, w, w, w);
+}
+
 // log(s) in 64 bits but for the logarithm of a number between 3/4 and 3/2, whose error in
 // 32 bits is 2^-25 at most.
 __device__ __forceinline__ double log_of(float s) {
@@ -317,15 +324,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constan
       }
       o.add<T>(v, a.c65536);
     }
+    if (left > 0) {
 #pragma unroll
-    for (int k = 0; k < U - 1; ++k)
-      if (k * threads < left) v[k] = p[k * threads];
-#pragma unroll
-    for (int k = 0; k < U - 1; ++k)
-      if (k * threads < left) {
-        const uint4 one[1] = {v[k]};
-        o.add<T>(one, a.c65536);
-      }
+      for (int k = 0; k < U; ++k) v[k] = k * threads < left ? p[k * threads] : nothing<T>();
+      o.add<T>(v, a.c65536);
+    }
     joined(o);
     if (CLUSTER) parts(o, rank, ctas);
     if (tid == 0 && rank == 0) finish_row<KIND>(a, row, in, o.m, o.s);
@@ -378,13 +381,20 @@ __device__ __forceinline__ void store_pack(T* p, const float (&e)[kV<T>], bool a
   }
 }
 
+template <typename T, typename I>
+__device__ __forceinline__ void zero_packs(T* p, I from, I to, I step, bool alike) {
+  const float zero[kV<T>] = {};
+#pragma unroll 4
+  for (I i = from; i < to; i += step) store_pack<T>(p + (int64_t)i * kV<T>, zero, alike);
+}
+
 // The logarithms and the gradient of a row in one pass over it: its packs are copied to
 // shared memory, each by the thread that reads it (no barrier between), summed as they
 // come, and read again there for the gradient. A row is a warp's, a block's, or a cluster's,
 // each block with its part of it.
-constexpr int kLossThreads = 128;
+constexpr int kLossThreads = 256;
 template <typename T, int KIND, bool CLUSTER>
-__global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_constant__ LossArgs a) {
+__global__ void __launch_bounds__(kLossThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
   constexpr int V = kV<T>, GROUPS = 4;
   extern __shared__ uint4 shared[];
   __shared__ Joined joined;
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
   const int64_t edge = rank == 0 ? cut.edge(tid, a.cols) : -1;
   T* const dp = dx + cut.head + (int64_t)first * V;
   const uint4* p = reinterpret_cast<const uint4*>(x + cut.head) + first;
-  const int each = ((n + threads - 1) / threads + GROUPS - 1) / GROUPS * threads;  // packs of a group
+  const int each = ((n + threads - 1) / threads + 4 * GROUPS - 1) / (4 * GROUPS) * 4 * threads;  // packs of a group
   const uint32_t to = (uint32_t)__cvta_generic_to_shared(packs);
   const auto fetch = [&]() {
 #pragma unroll
@@ -421,8 +431,7 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
   if (a.eager) fetch();
   if (skipped<KIND>(a, row, target)) {
     copies_wait<0>();
-    const float zero[V] = {};
-    for (int i = tid; i < n; i += threads) store_pack<T>(dp + (int64_t)i * V, zero, a.alike);
+    zero_packs<T>(dp, tid, n, threads, a.alike);
     if (edge >= 0) dx[edge] = from_f32<T>(0.f);
     if (tid == 0 && rank == 0) skip_row<KIND>(a, row);
     return;
@@ -438,14 +447,11 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
   }
   const auto sum = [&](int g) {
     const int end = min(n, (g + 1) * each);
-    int i = g * each + tid;
-    for (; i + 3 * threads < end; i += 4 * threads) {
-      const uint4 four[4] = {packs[i], packs[i + threads], packs[i + 2 * threads], packs[i + 3 * threads]};
-      o.add<T>(four, a.c65536);
-    }
-    for (; i < end; i += threads) {
-      const uint4 one[1] = {packs[i]};
-      o.add<T>(one, a.c65536);
+    for (int i = g * each + tid; i < end; i += 4 * threads) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = i + u * threads < end ? packs[i + u * threads] : nothing<T>();
+      o.add<T>(v, a.c65536);
     }
   };
   copies_wait<3>();
@@ -470,30 +476,20 @@ __global__ void __launch_bounds__(kLossThreads, 7) vrRowLossGrads(const __grid_c
   const bool none = c == 0.f;
   const Factor factor = Factor::of<T>(o.m, 0.f, f);
   const int64_t t = target - cut.head - (int64_t)first * V;
-  const int targetPack = t >= 0 && t < (int64_t)n * V ? (int)(t / V) : -1;
-  const auto gradient = [&](int i, const uint4& v) {
-    float d[V];
-    scaled_exps<T>(v, factor, a.c65536, d);
-    if (i == targetPack) {
+  if (none) {
+    zero_packs<T>(dp, tid, n, threads, a.alike);
+  } else {
+    for (int i = tid; i < n; i += 4 * threads) {  // four chains side by side, then the stores
+      float d[4][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (j == (int)(t % V)) d[j] = -c * expm1f(lp);
+      for (int u = 0; u < 4; ++u)
+        scaled_exps<T>(packs[i + u * threads < n ? i + u * threads : i], factor, a.c65536, d[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u * threads < n) store_pack<T>(dp + (int64_t)(i + u * threads) * V, d[u], a.alike);
     }
-    if (none) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) d[j] = 0.f;
-    }
-    store_pack<T>(dp + (int64_t)i * V, d, a.alike);
-  };
-  int i = tid;
-  for (; i + 3 * threads < n; i += 4 * threads) {  // four chains side by side
-    uint4 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = packs[i + u * threads];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) gradient(i + u * threads, v[u]);
+    if (t >= 0 && t < (int64_t)n * V && (int)(t / V) % threads == tid) dp[t] = from_f32<T>(-c * expm1f(lp));
   }
-  for (; i < n; i += threads) gradient(i, packs[i]);
   if (edge >= 0)
     dx[edge] = from_f32<T>(none             ? 0.f
                            : edge == target ? -c * expm1f(lp)
@@ -535,8 +531,7 @@ __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant
   const uint4* p = reinterpret_cast<const uint4*>(x + cut.head);
   T* const dp = dx + cut.head;
   if (none) {
-    const float zero[V] = {};
-    for (uint64_t i = first; i < end; i += threads) store_pack<T>(dp + i * V, zero, a.alike);
+    zero_packs<T>(dp, first, end, (uint64_t)threads, a.alike);
     return;
   }
   const Factor factor = Factor::of<T>(lse, rest, -c);
@@ -708,21 +703,22 @@ vrResult_t rowGrads(LossArgs& a, cudaStream_t st) {
   return launch((const void*)&vrRowGrads<T, 4>, dim3((unsigned)blocks), dim3(x, y), 0, st, a);
 }
 
-// Logarithms and gradient in one pass; false if a row is too large for a cluster. Parts of
-// 36 KB, of which an SM holds six, each at another point of its way (131072 bf16 358 us, of
-// 72 KB and three 377; 50257 float32 238 and 246).
+// Logarithms and gradient in one pass; false if a row is too large for a cluster. Parts of up to
+// 72 KB and 256 threads, four blocks an SM by their registers (50001 bf16, all rows counting, 315
+// us; parts of 36 KB and 128 threads 327, of 52 KB and 192 threads 336; 50257 float32 300, 330,
+// 314).
 constexpr size_t kMostShared = 200 * 1024;
 template <typename T, int KIND>
 bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
   alikeRows<T>(a);
   const uint64_t packs = a.cols / kV<T> ? a.cols / kV<T> : 1;
-  constexpr uint64_t kBest = 36 * 1024 / 16, kLargest = kMostShared / 16;
+  constexpr uint64_t kBest = 72 * 1024 / 16, kLargest = kMostShared / 16;
   int ctas = 1;
   while (ctas < 8 && (packs + ctas - 1) / ctas > kBest) ctas *= 2;
   // Few rows are spread over more SMs, in parts of 8 KB at least, up to six blocks on each.
   while (ctas < 8 && a.rows * ctas * 2 <= 6 * kSMs && packs / ctas >= 1024) ctas *= 2;
   const uint64_t part = (packs + ctas - 1) / ctas;
-  uint64_t threads = (part / 8 + 31) / 32 * 32;
+  uint64_t threads = (part / 4 + 31) / 32 * 32;
   threads = threads < 32 ? 32 : threads > kLossThreads ? kLossThreads : threads;
   const unsigned y = threads == 32 ? kLossThreads / 32 : 1;
   const uint64_t blocks = (a.rows + y - 1) / y * ctas;
