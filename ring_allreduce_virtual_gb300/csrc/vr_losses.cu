@@ -29,9 +29,9 @@ struct LossArgs {
   float *logp, *lse, *rest, *coef;  // coef: the derivative by logp
   // policies
   const float *old, *advantage, *weight, *ref;
-  float* rowLoss;
+  double* rowLoss;
   double low, high;  // logs of the ratio's borders
-  float least, most;  // the borders
+  double least, most;  // the borders
   float kl, scale;
   float* loss;
   // the gradient's kernel
@@ -170,19 +170,26 @@ template <int KIND>
 __device__ __forceinline__ float2 finish_row(const LossArgs& a, uint64_t row, const RowIn& in, float m, float s,
                                              bool write = true) {
   const double l = log_of(s), lp = ((double)in.at - (double)m) - l;
-  float loss = 0.f, c = 0.f;
+  float c = 0.f;
+  [[maybe_unused]] double loss = 0.0;
   if constexpr (KIND == POLICY) {
+    // Rows' losses cancel in their sum: they are of 64 bits, the ratio's distance from 1 of 32.
     const float A = in.advantage;
     const double e = lp - (double)in.old;
-    if (A > 0.f && e > a.high) loss = -(a.most * A);
-    else if (A < 0.f && e < a.low) loss = -(a.least * A);
-    else if (A != 0.f) loss = c = -(expf((float)e) * A);
+    if (A > 0.f && e > a.high) {
+      loss = -(a.most * (double)A);
+    } else if (A < 0.f && e < a.low) {
+      loss = -(a.least * (double)A);
+    } else if (A != 0.f) {
+      loss = -((e > -0.5 ? 1.0 + (double)expm1f((float)e) : (double)expf((float)e)) * (double)A);
+      c = (float)loss;
+    }
     if (a.ref) {
       const float r = (float)((double)in.ref - lp), x = expm1f(r);
-      loss = fmaf(a.kl, x - r, loss);
+      loss += (double)(a.kl * (x - r));
       c = fmaf(-a.kl, x, c);
     }
-    loss *= in.weight;
+    loss *= (double)in.weight;
     c *= a.scale * in.weight;
   }
   if (write) {
@@ -205,7 +212,10 @@ __device__ __forceinline__ void skip_row(const LossArgs& a, uint64_t row) {
   a.logp[row] = 0.f;
   if (a.lse) a.lse[row] = 0.f;
   if (a.rest) a.rest[row] = 0.f;
-  if constexpr (KIND == POLICY) a.rowLoss[row] = a.coef[row] = 0.f;
+  if constexpr (KIND == POLICY) {
+    a.rowLoss[row] = 0.0;
+    a.coef[row] = 0.f;
+  }
 }
 template <int KIND>
 __device__ __forceinline__ bool skipped(const LossArgs& a, uint64_t row, int64_t target) {
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kOneBlock) vrLossSum(const __grid_constant__ L
   begin_kernel();
   double s = 0.0;
 #pragma unroll 8
-  for (uint64_t i = threadIdx.x; i < a.rows; i += kOneBlock) s += (double)a.rowLoss[i];
+  for (uint64_t i = threadIdx.x; i < a.rows; i += kOneBlock) s += a.rowLoss[i];
   s = block_total(s);
   if (threadIdx.x == 0) *a.loss = (float)(s * (double)a.scale);
 }
@@ -792,7 +802,7 @@ extern "C" VR_API vrResult_t vrTokenLogProbsBackward(const float* dlogp, const f
 
 extern "C" VR_API vrResult_t vrPolicyLossWorkspace(size_t rows, size_t* bytes) {
   if (!bytes || rows > kMost) return vrInvalidArgument;
-  *bytes = rows * sizeof(float);
+  *bytes = rows * sizeof(double);
   return vrSuccess;
 }
 
@@ -831,9 +841,9 @@ extern "C" VR_API vrResult_t vrPolicyLoss(const void* logits, const int64_t* tar
     for (int i = 0; i < 6; ++i)
       if (overlap(outs[i], x)) return vrInvalidArgument;
     a.x = logits, a.dx = dlogits, a.target = targets, a.stride = stride, a.dStride = dStride;
-    a.logp = logp, a.lse = lse, a.rest = rest, a.coef = dlogp, a.dlogp = dlogp, a.rowLoss = (float*)workspace;
+    a.logp = logp, a.lse = lse, a.rest = rest, a.coef = dlogp, a.dlogp = dlogp, a.rowLoss = (double*)workspace;
     a.old = oldLogp, a.advantage = advantages, a.weight = weights, a.ref = klCoef != 0.f ? refLogp : nullptr;
-    a.least = (float)(1.0 - clipLow), a.most = (float)(1.0 + clipHigh);
+    a.least = 1.0 - clipLow, a.most = 1.0 + clipHigh;
     a.low = clipLow < 1.0 ? log1p(-clipLow) : -INFINITY, a.high = log1p(clipHigh);
     a.kl = klCoef;
     const vrResult_t r = dispatch(dtype, [&](auto t) {

@@ -758,10 +758,10 @@ def _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, 
     dx, ds = _gradient_of(logits, out, device, cols) if gradient else (None, 0)
     loss = torch.empty((), dtype=_F32, device=logits.device)
     logp = torch.empty_like(old_logp)
-    kept, n, at = _row_buffers(logits, rows)
+    kept, n, at = _row_buffers(logits, rows, 8 * rows)
     rc = vr.lib().vrPolicyLoss(logits.data_ptr(), targets.data_ptr(), *vectors, loss.data_ptr(),
                                logp.data_ptr(), at, at + 8 * n, at + 4 * n, _ptr(dx), rows, cols, xs,
-                               ds, clip_low, clip_high, kl_coef, scale, code, at + 12 * n, 4 * rows,
+                               ds, clip_low, clip_high, kl_coef, scale, code, at + 12 * n, 8 * rows,
                                _raw_stream(device))
     if rc:
         raise vr.VrError(rc, "vrPolicyLoss")
@@ -772,11 +772,11 @@ def _policy(logits, targets, old_logp, advantages, weights, ref_logp, clip_low, 
     return loss, logp, *_kept_rows(kept, n, targets)
 
 
-def _row_buffers(logits, rows, extra=0):
-    """(tensor, n, address): one allocation for what a call keeps of its rows, four times n
-    floats (lse, dlogp, rest, and a workspace or the tokens' logp) and `extra` bytes."""
+def _row_buffers(logits, rows, extra):
+    """(tensor, n, address): one allocation for what a call keeps of its rows, three times n
+    floats (lse, dlogp, rest), and `extra` bytes behind them."""
     n = (rows + 3) // 4 * 4
-    kept = torch.empty(4 * n + extra // 4, dtype=_F32, device=logits.device)
+    kept = torch.empty(3 * n + extra // 4, dtype=_F32, device=logits.device)
     return kept, n, kept.data_ptr()
 
 
@@ -840,7 +840,8 @@ def _preference(logits, targets, ref_logps, starts, beta, label_smoothing, scale
     dx, ds = _gradient_of(logits, out, device, cols) if gradient else (None, 0)
     loss = torch.empty((), dtype=_F32, device=logits.device)
     logps = torch.empty((2, pairs), dtype=_F32, device=logits.device)
-    kept, n, at = _row_buffers(logits, rows, 16 * pairs)
+    n = (rows + 3) // 4 * 4  # the tokens' logp and a workspace
+    kept, n, at = _row_buffers(logits, rows, 4 * n + 16 * pairs)
     rc = vr.lib().vrPreferenceLoss(logits.data_ptr(), targets.data_ptr(), _ptr(ref_logps),
                                    _ptr(starts), loss.data_ptr(), logps.data_ptr(), at + 12 * n, at,
                                    at + 8 * n, at + 4 * n, _ptr(dx), pairs, rows, cols, xs, ds, beta,
