@@ -544,38 +544,30 @@ __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant
     zero_packs<T>(dp, first, end, (uint64_t)threads, a.alike);
     return;
   }
+  // The target's element is left to the thread that writes its pack, which reads it before.
+  const int64_t t = target - cut.head, at = t >= 0 ? t / V : -1, place = at - (int64_t)(segment * a.part);
+  const bool mine = place >= 0 && at < (int64_t)end && (int)(place % threads) == (int)threadIdx.x;
+  const float atTarget = mine ? to_f32(x[target]) : 0.f;
   const Factor factor = Factor::of<T>(lse, rest, -c);
   uint4 v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (first + u * threads < end) v[u] = p[first + u * threads];
-  for (uint64_t i0 = first; i0 < end; i0 += U * threads) {
-    uint4 w[U];
+  for (uint64_t i = first; i < end; i += U * threads) {
+    uint4 w[U];  // the next, on their way
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + (U + u) * threads < end) w[u] = p[i0 + (U + u) * threads];
+      if (i + (U + u) * threads < end) w[u] = p[i + (U + u) * threads];
+    float d[U][V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint64_t i = i0 + u * threads;
-      if (i >= end) break;
-      float d[V];
-      scaled_exps<T>(v[u], factor, a.c65536, d);
-      const int64_t t = target - cut.head - (int64_t)(i * V);
-      if (t >= 0 && t < V) {
-        F2 f[V / 2];
-        float e[V];
-        unpack<T>(v[u], f);
+    for (int u = 0; u < U; ++u) scaled_exps<T>(v[u], factor, a.c65536, d[u]);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) split(f[j], e[2 * j], e[2 * j + 1]);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j == (int)t) d[j] = -c * expm1f((e[j] - lse) - rest);
-      }
-      store_pack<T>(dp + i * V, d, a.alike);
-    }
+    for (int u = 0; u < U; ++u)
+      if (i + u * threads < end) store_pack<T>(dp + (i + u * threads) * V, d[u], a.alike);
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u] = w[u];
   }
+  if (mine) dp[t] = from_f32<T>(-c * expm1f((atTarget - lse) - rest));
 }
 
 constexpr int kOneBlock = 1024;
