@@ -29,7 +29,7 @@ struct LossArgs {
   float *logp, *lse, *rest, *coef;  // coef: the derivative by logp
   // policies
   const float *old, *advantage, *weight, *ref;
-  double* rowLoss;
+  float2* rowLoss;  // a number and what its rounding lost
   double low, high;  // logs of the ratio's borders
   double least, most;  // the borders
   float kl, scale;
@@ -200,7 +200,8 @@ __device__ __forceinline__ float2 finish_row(const LossArgs& a, uint64_t row, co
       if (a.rest) a.rest[row] = (float)(((double)m - (double)lse) + l);
     }
     if constexpr (KIND == POLICY) {
-      a.rowLoss[row] = loss;
+      const float high = (float)loss;
+      a.rowLoss[row] = make_float2(high, (float)(loss - (double)high));
       a.coef[row] = c;
     }
   }
@@ -213,7 +214,7 @@ __device__ __forceinline__ void skip_row(const LossArgs& a, uint64_t row) {
   if (a.lse) a.lse[row] = 0.f;
   if (a.rest) a.rest[row] = 0.f;
   if constexpr (KIND == POLICY) {
-    a.rowLoss[row] = 0.0;
+    a.rowLoss[row] = make_float2(0.f, 0.f);
     a.coef[row] = 0.f;
   }
 }
@@ -284,7 +285,9 @@ struct Parts {
 constexpr int kRowThreads = 256;
 
 // A block for each row, or a warp for each of a block's, read once, the next packs on their
-// way while the last are summed.
+// way while the last are summed. Bound by HBM for long rows: 4096 x 131072 bf16 155 us, 1.03 of
+// the measured copy peak; 8192 x 32000 0.86, 16384 x 5000 0.60 (a row's way from its target
+// to its sum is some 4 us, of which blocks of 10 KB cannot hide all).
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constant__ LossArgs a) {
   constexpr int U = 4;
@@ -401,7 +404,11 @@ __device__ __forceinline__ void zero_packs(T* p, I from, I to, I step, bool alik
 // The logarithms and the gradient of a row in one pass over it: its packs are copied to
 // shared memory, each by the thread that reads it (no barrier between), summed as they
 // come, and read again there for the gradient. A row is a warp's, a block's, or a cluster's,
-// each block with its part of it.
+// each block with its part of it. A block's way is 8 to 10 us (its target 0.9, its copies 3.8,
+// sums and their joining 1.1, a cluster's 1.5, the loss 1.0, the gradient 1.7), four blocks are
+// on an SM: 0.8 to 0.87 of the measured copy peak for rows over 32000 bf16 (8192 x 50001, half of
+// the rows counting, 218 us; the two kernels of one pass each 281, all counting 313 and 408).
+// What took it there from 0.49 is four packs a thread side by side, in straight lines.
 constexpr int kLossThreads = 256;
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kLossThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
@@ -507,7 +514,9 @@ __global__ void __launch_bounds__(kLossThreads, 4) vrRowLossGrads(const __grid_c
 }
 
 // dx from the rows' logarithms, read by an earlier kernel: a block takes some rows' parts,
-// from the last row on, which that kernel read last.
+// from the last row on, which that kernel read last. All of a group's arithmetic comes before
+// its stores (4096 x 131072 bf16 308 us, 1.03 of the measured copy peak; with a branch for the
+// target and the end between them 468).
 constexpr int kGradThreads = 256;
 template <typename T, int U>
 __global__ void __launch_bounds__(kGradThreads) vrRowGrads(const __grid_constant__ LossArgs a) {
@@ -587,14 +596,36 @@ __device__ double block_total(double v) {
   return all;
 }
 
-// The rows' losses added up.
+// The rows' losses added up, in pairs of floats: a 64-bit addition takes 64 times as long.
+// The sum's rounding errors are added up beside it (Knuth's two-sum).
+struct Pair {
+  float s = 0.f, e = 0.f;
+  __device__ __forceinline__ void add(float v, float rest) {
+    const float t = __fadd_rn(s, v), p = __fadd_rn(t, -s);
+    e += __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -p)), __fadd_rn(v, -p)) + rest;
+    s = t;
+  }
+  __device__ __forceinline__ void warp() {
+#pragma unroll
+    for (int k = 16; k; k >>= 1) add(__shfl_xor_sync(~0u, s, k), __shfl_xor_sync(~0u, e, k));
+  }
+};
 __global__ void __launch_bounds__(kOneBlock) vrLossSum(const __grid_constant__ LossArgs a) {
+  __shared__ Pair warps[32];
   begin_kernel();
-  double s = 0.0;
+  Pair p;
 #pragma unroll 8
-  for (uint64_t i = threadIdx.x; i < a.rows; i += kOneBlock) s += a.rowLoss[i];
-  s = block_total(s);
-  if (threadIdx.x == 0) *a.loss = (float)(s * (double)a.scale);
+  for (uint64_t i = threadIdx.x; i < a.rows; i += kOneBlock) {
+    const float2 v = a.rowLoss[i];
+    p.add(v.x, v.y);
+  }
+  p.warp();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = p;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  p = warps[threadIdx.x];
+  p.warp();
+  if (threadIdx.x == 0) *a.loss = (float)(((double)p.s + (double)p.e) * (double)a.scale);
 }
 
 // The sequences' sums, the pairs' losses and the derivatives by the rows' logp.
@@ -794,7 +825,7 @@ extern "C" VR_API vrResult_t vrTokenLogProbsBackward(const float* dlogp, const f
 
 extern "C" VR_API vrResult_t vrPolicyLossWorkspace(size_t rows, size_t* bytes) {
   if (!bytes || rows > kMost) return vrInvalidArgument;
-  *bytes = rows * sizeof(double);
+  *bytes = rows * sizeof(float2);
   return vrSuccess;
 }
 
@@ -833,7 +864,7 @@ extern "C" VR_API vrResult_t vrPolicyLoss(const void* logits, const int64_t* tar
     for (int i = 0; i < 6; ++i)
       if (overlap(outs[i], x)) return vrInvalidArgument;
     a.x = logits, a.dx = dlogits, a.target = targets, a.stride = stride, a.dStride = dStride;
-    a.logp = logp, a.lse = lse, a.rest = rest, a.coef = dlogp, a.dlogp = dlogp, a.rowLoss = (double*)workspace;
+    a.logp = logp, a.lse = lse, a.rest = rest, a.coef = dlogp, a.dlogp = dlogp, a.rowLoss = (float2*)workspace;
     a.old = oldLogp, a.advantage = advantages, a.weight = weights, a.ref = klCoef != 0.f ? refLogp : nullptr;
     a.least = 1.0 - clipLow, a.most = 1.0 + clipHigh;
     a.low = clipLow < 1.0 ? log1p(-clipLow) : -INFINITY, a.high = log1p(clipHigh);
