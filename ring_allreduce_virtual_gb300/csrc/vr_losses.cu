@@ -11,9 +11,11 @@
 //
 // Rows are summed in 32 bits over their largest element; what follows for each row, where
 // an error in the last place decides on which side of the clipping's border a row is, is
-// done in 64. All of it is bound by memory traffic (two exponentials an element).
+// done in pairs of floats. All of it is bound by memory traffic (two exponentials an element).
 #include <float.h>
 #include <math.h>
+
+#include <cmath>
 
 #include "vr_packs.cuh"
 
@@ -30,8 +32,7 @@ struct LossArgs {
   // policies
   const float *old, *advantage, *weight, *ref;
   float2* rowLoss;  // a number and what its rounding lost
-  double low, high;  // logs of the ratio's borders
-  double least, most;  // the borders
+  float2 low, high, least, most;  // logs of the ratio's borders, the borders: sums of two floats
   float kl, scale;
   float* loss;
   // the gradient's kernel
@@ -134,14 +135,45 @@ __device__ __forceinline__ uint4 nothing() {
   return make_uint4(w, w, w, w);
 }
 
-// log(s) in 64 bits but for the logarithm of a number between 3/4 and 3/2, whose error in
-// 32 bits is 2^-25 at most.
-__device__ __forceinline__ double log_of(float s) {
-  if (!(s > 0.f && s < FLT_MAX)) return (double)logf(s);
+// A number as the sum of two floats, and what is done with it: 48 bits at the price of a few
+// instructions, where one of 64 bits takes the time of 16. `add` is Knuth's two-sum; of a sum
+// that is not finite the second float says nothing.
+struct Pair {
+  float s = 0.f, e = 0.f;
+  __device__ __forceinline__ void add(float v, float rest = 0.f) {
+    const float t = __fadd_rn(s, v), p = __fadd_rn(t, -s);
+    const float lost = __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -p)), __fadd_rn(v, -p)) + rest;
+    e = t - t == 0.f ? e + lost : 0.f;
+    s = t;
+  }
+  __device__ __forceinline__ void times(float f) {
+    const float p = __fmul_rn(s, f), lost = fmaf(s, f, -p);
+    e = p - p == 0.f ? fmaf(e, f, lost) : 0.f;
+    s = p;
+  }
+  __device__ __forceinline__ float value() const { return s + e; }
+  __device__ __forceinline__ void warp() {
+#pragma unroll
+    for (int k = 16; k; k >>= 1) add(__shfl_xor_sync(~0u, s, k), __shfl_xor_sync(~0u, e, k));
+  }
+};
+
+// log(s): k log(2), of which the first part is k times 16 bits and so exact, and the logarithm
+// of a number between 3/4 and 3/2, whose error is 2^-25 at most.
+__device__ __forceinline__ Pair log_of(float s) {
+  Pair l;
+  if (!(s > 0.f && s < FLT_MAX)) {
+    l.s = logf(s);
+    return l;
+  }
+  constexpr double kLog2 = 0.693147180559945309417;
+  constexpr float kUpper = (float)((double)(int)(kLog2 * 65536.0) / 65536.0), kLower = (float)(kLog2 - (double)kUpper);
   int k;
   float f = frexpf(s, &k);  // in [1/2, 1)
   if (f < 0.75f) f *= 2.f, --k;
-  return fma((double)k, 0.693147180559945309417, (double)logf(f));
+  l.s = (float)k * kUpper;
+  l.add(logf(f), (float)k * kLower);
+  return l;
 }
 
 enum { LOGP = 0, POLICY = 1 };
@@ -169,43 +201,64 @@ struct RowIn {
 template <int KIND>
 __device__ __forceinline__ float2 finish_row(const LossArgs& a, uint64_t row, const RowIn& in, float m, float s,
                                              bool write = true) {
-  const double l = log_of(s), lp = ((double)in.at - (double)m) - l;
+  const Pair l = log_of(s);
+  Pair lp;
+  lp.s = in.at;
+  lp.add(-m);
+  lp.add(-l.s, -l.e);
+  const float logp = lp.value();
   float c = 0.f;
-  [[maybe_unused]] double loss = 0.0;
+  [[maybe_unused]] Pair loss;
   if constexpr (KIND == POLICY) {
-    // Rows' losses cancel in their sum: they are of 64 bits, the ratio's distance from 1 of 32.
+    // Next to a border of the clipping, and where rows' losses cancel in their sum, 24 bits
+    // are too few.
     const float A = in.advantage;
-    const double e = lp - (double)in.old;
-    if (A > 0.f && e > a.high) {
-      loss = -(a.most * (double)A);
-    } else if (A < 0.f && e < a.low) {
-      loss = -(a.least * (double)A);
+    Pair e = lp;
+    e.add(-in.old);
+    const float above = (e.s - a.high.x) + (e.e - a.high.y), below = (e.s - a.low.x) + (e.e - a.low.y);
+    if (A > 0.f && above > 0.f) {
+      loss.s = -a.most.x, loss.e = -a.most.y;
+      loss.times(A);
+    } else if (A < 0.f && below < 0.f) {
+      loss.s = -a.least.x, loss.e = -a.least.y;
+      loss.times(A);
     } else if (A != 0.f) {
-      loss = -((e > -0.5 ? 1.0 + (double)expm1f((float)e) : (double)expf((float)e)) * (double)A);
-      c = (float)loss;
+      const float f = e.value();
+      if (f > -0.5f) {
+        loss.s = -A;
+        loss.add(-expm1f(f) * A);
+      } else {
+        loss.s = -expf(f) * A;
+      }
+      c = loss.value();
     }
     if (a.ref) {
-      const float r = (float)((double)in.ref - lp), x = expm1f(r);
-      loss += (double)(a.kl * (x - r));
+      Pair d;
+      d.s = in.ref;
+      d.add(-lp.s, -lp.e);
+      const float r = d.value(), x = expm1f(r);
+      loss.add(a.kl * (x - r));
       c = fmaf(-a.kl, x, c);
     }
-    loss *= (double)in.weight;
+    loss.times(in.weight);
     c *= a.scale * in.weight;
   }
   if (write) {
-    a.logp[row] = (float)lp;
+    a.logp[row] = logp;
     if (a.lse) {
-      const float lse = (float)((double)m + l);
-      a.lse[row] = lse;
-      if (a.rest) a.rest[row] = (float)(((double)m - (double)lse) + l);
+      Pair lse;
+      lse.s = m;
+      lse.add(l.s, l.e);
+      const float rounded = lse.value();
+      a.lse[row] = rounded;
+      if (a.rest) a.rest[row] = lse.e - (rounded - lse.s);
     }
     if constexpr (KIND == POLICY) {
-      const float high = (float)loss;
-      a.rowLoss[row] = make_float2(high, (float)(loss - (double)high));
+      a.rowLoss[row] = make_float2(loss.s, loss.e);
       a.coef[row] = c;
     }
   }
-  return make_float2((float)lp, c);
+  return make_float2(logp, c);
 }
 // A row that counts for nothing: its logits are not read.
 template <int KIND>
@@ -596,20 +649,7 @@ __device__ double block_total(double v) {
   return all;
 }
 
-// The rows' losses added up, in pairs of floats: a 64-bit addition takes 64 times as long.
-// The sum's rounding errors are added up beside it (Knuth's two-sum).
-struct Pair {
-  float s = 0.f, e = 0.f;
-  __device__ __forceinline__ void add(float v, float rest) {
-    const float t = __fadd_rn(s, v), p = __fadd_rn(t, -s);
-    e += __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -p)), __fadd_rn(v, -p)) + rest;
-    s = t;
-  }
-  __device__ __forceinline__ void warp() {
-#pragma unroll
-    for (int k = 16; k; k >>= 1) add(__shfl_xor_sync(~0u, s, k), __shfl_xor_sync(~0u, e, k));
-  }
-};
+// The rows' losses added up.
 __global__ void __launch_bounds__(kOneBlock) vrLossSum(const __grid_constant__ LossArgs a) {
   __shared__ Pair warps[32];
   begin_kernel();
@@ -682,6 +722,12 @@ __global__ void __launch_bounds__(kOneBlock) vrPairLosses(const __grid_constant_
 
 // ------------------------------------------------------------------ host
 constexpr uint64_t kMost = 1ull << 48;  // elements from the first to the last of a matrix
+
+// A number as the sum of two floats.
+float2 two(double v) {
+  const float s = (float)v;
+  return float2{s, std::isfinite(s) ? (float)(v - (double)s) : 0.f};
+}
 
 bool typeOk(vrDataType_t t) { return t == vrFloat16 || t == vrBfloat16 || t == vrFloat32; }
 
@@ -866,8 +912,8 @@ extern "C" VR_API vrResult_t vrPolicyLoss(const void* logits, const int64_t* tar
     a.x = logits, a.dx = dlogits, a.target = targets, a.stride = stride, a.dStride = dStride;
     a.logp = logp, a.lse = lse, a.rest = rest, a.coef = dlogp, a.dlogp = dlogp, a.rowLoss = (float2*)workspace;
     a.old = oldLogp, a.advantage = advantages, a.weight = weights, a.ref = klCoef != 0.f ? refLogp : nullptr;
-    a.least = 1.0 - clipLow, a.most = 1.0 + clipHigh;
-    a.low = clipLow < 1.0 ? log1p(-clipLow) : -INFINITY, a.high = log1p(clipHigh);
+    a.least = two(1.0 - clipLow), a.most = two(1.0 + clipHigh);
+    a.low = two(clipLow < 1.0 ? log1p(-clipLow) : -INFINITY), a.high = two(log1p(clipHigh));
     a.kl = klCoef;
     const vrResult_t r = dispatch(dtype, [&](auto t) {
       using T = decltype(t);
