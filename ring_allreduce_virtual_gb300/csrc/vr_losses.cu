@@ -339,7 +339,7 @@ constexpr int kRowThreads = 256;
 
 // A block for each row, or a warp for each of a block's, read once, the next packs on their
 // way while the last are summed. Bound by HBM for long rows: 4096 x 131072 bf16 155 us, 1.03 of
-// the measured copy peak; 8192 x 32000 0.86, 16384 x 5000 0.60 (a row's way from its target
+// the measured copy peak; 8192 x 32000 0.88, 16384 x 5000 0.63 (a row's way from its target
 // to its sum is some 4 us, of which blocks of 10 KB cannot hide all).
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constant__ LossArgs a) {
@@ -457,11 +457,11 @@ __device__ __forceinline__ void zero_packs(T* p, I from, I to, I step, bool alik
 // The logarithms and the gradient of a row in one pass over it: its packs are copied to
 // shared memory, each by the thread that reads it (no barrier between), summed as they
 // come, and read again there for the gradient. A row is a warp's, a block's, or a cluster's,
-// each block with its part of it. A block's way is 8 to 10 us (its target 0.9, its copies 3.8,
-// sums and their joining 1.1, a cluster's 1.5, the loss 1.0, the gradient 1.7), four blocks are
-// on an SM: 0.8 to 0.87 of the measured copy peak for rows over 32000 bf16 (8192 x 50001, half of
-// the rows counting, 218 us; the two kernels of one pass each 281, all counting 313 and 408).
-// What took it there from 0.49 is four packs a thread side by side, in straight lines.
+// each block with its part of it. A block's way is 8.5 to 10 us (its target 0.8, its copies 3.8,
+// sums and their joining 1.1, a cluster's 1.5, the loss 0.7, the gradient 2.1), three or four
+// blocks are on an SM: 0.84 to 0.90 of the measured copy peak for rows over 32000 bf16 (8192 x
+// 50001, half of the rows counting, 214 us; the two kernels of one pass each 273; all counting 306
+// and 397). What took it there from 0.49 is four packs a thread side by side, in straight lines.
 constexpr int kLossThreads = 256;
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kLossThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
