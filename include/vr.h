@@ -506,7 +506,7 @@ VR_API vrResult_t vrQkNormRopeBackwardWorkspace(size_t dim, size_t* bytes);
  *           k, of `dtype`, each with strides of its own; dqIn may be dq and dkIn dk with
  *           the same strides, other overlaps are not allowed.
  *  dqWeight, dkWeight   [device] dim elements of weightType, overwritten (zeros if there
- *           are no tokens); NULL: not wanted.
+ *           are no tokens, or no keys); NULL: not wanted.
  *  workspace    [device] 16-byte aligned, of at least vrQkNormRopeBackwardWorkspace bytes;
  *           may be NULL if dqWeight and dkWeight are.
  * Other arguments as in the forward pass. */

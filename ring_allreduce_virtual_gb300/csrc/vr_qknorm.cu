@@ -250,25 +250,27 @@ __device__ __forceinline__ T* place(const Side& s, const Token& k, uint32_t head
 // its way takes no registers. Backward, a warp's sums of g u stay in registers until its
 // last token; a block leaves one set.
 // Bound by HBM where heads fill the lanes: 4 x 4096 tokens of 32 + 8 heads of 128 bf16
-// backward 84 us, 0.90 of the measured copy peak (with one chain in twice the warps 0.65,
-// 12 warps of 168 registers 0.49: what they spill), 64 + 8 forward 107 us, 0.85 (0.74 with one
-// chain). Heads of 80 use 5 of 8 lanes: 16 + 16 float16 neighbours 0.59 and 0.47, bound by what
-// a scheduler's two warps issue (0.44 an instruction a cycle).
+// backward 84 us, 0.90 of the measured copy peak (with one chain in twice the warps 0.65, 12
+// warps of 168 registers 0.49: they spill; float32 does not, 0.93 against 0.89), 64 + 8 forward
+// 107 us, 0.85 (0.74 with one chain). Heads of 80 use 5 of 8 lanes: 16 + 16 float16 neighbours
+// 0.59 and 0.47, bound by what a scheduler's two warps issue (0.44 instructions a cycle).
 constexpr int kStages = 3, kAtOnce = 2;
 template <bool BACK>
-constexpr int kBlocks = BACK ? 1 : 2;  // on an SM: 255 registers a thread, or 128
+constexpr int kBlocks = BACK ? 1 : 2;  // on an SM: 255 (168) registers a thread, or 128
+template <typename T, bool BACK>
+constexpr int kHeadWarps = BACK && sizeof(T) == 4 ? 12 : 8;
 template <typename T, typename W, bool INTER, bool BACK>
-__global__ void __launch_bounds__(kThreads, kBlocks<BACK>) vrQkHeads(const __grid_constant__ QkArgs a) {
-  constexpr int V = kV<T>, NP = BACK ? 4 : 2, H = V / 2, U = kAtOnce;
+__global__ void __launch_bounds__(32 * kHeadWarps<T, BACK>, kBlocks<BACK>) vrQkHeads(const __grid_constant__ QkArgs a) {
+  constexpr int V = kV<T>, NP = BACK ? 4 : 2, H = V / 2, U = kAtOnce, WARPS = kHeadWarps<T, BACK>;
   extern __shared__ uint4 shared[];  // rings, then the tables' rows, then the weights
   begin_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = lane / a.lanes, groups = 32 / a.lanes, half = a.rot / 2;
   const Packs<T, INTER> at(a, lane % a.lanes);
   uint4* const ring = shared + warp * (kStages * U * NP * 32) + lane;
-  float* const rows = reinterpret_cast<float*>(shared + kWarps * kStages * U * NP * 32) + warp * (kStages * 2 * half);
-  float* const w = reinterpret_cast<float*>(shared + kWarps * kStages * U * NP * 32) + kWarps * (kStages * 2 * half);
-  for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += kThreads) {
+  float* const rows = reinterpret_cast<float*>(shared + WARPS * kStages * U * NP * 32) + warp * (kStages * 2 * half);
+  float* const w = reinterpret_cast<float*>(shared + WARPS * kStages * U * NP * 32) + WARPS * (kStages * 2 * half);
+  for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += 32 * WARPS) {
     const W* p = static_cast<const W*>(a.w[i >= a.dim]);
     w[i] = p ? to_f32(p[i < a.dim ? i : i - a.dim]) : 1.f;
   }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<BACK>) vrQkHeads(const __gri
     if (i % 2 ? !at.hasB : !at.hasA) ring[i * 32] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
-  const uint32_t me = blockIdx.x * kWarps + warp, keys = a.steps[0];
+  const uint32_t me = blockIdx.x * WARPS + warp, keys = a.steps[0];
   Walk now;
   now.start(a, me);
   Walk ahead = now, after = now;  // of the copies; of the positions, which are loaded a token before
@@ -493,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<BACK>) vrQkHeads(const __gri
       }
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < 2 * a.dim; i += 32 * WARPS) {
       float t = 0.f;
-      for (int v = 0; v < kWarps; ++v) t += sums[v * 2 * a.dim + i];
+      for (int v = 0; v < WARPS; ++v) t += sums[v * 2 * a.dim + i];
       a.partials[(uint64_t)blockIdx.x * 2 * a.dim + i] = t;
     }
   }
@@ -756,28 +758,29 @@ bool layOut(QkArgs& a, bool backward) {
 
 template <typename T, typename W, bool BACK>
 vrResult_t wholeHeads(QkArgs& a, cudaStream_t st) {
+  constexpr int WARPS = kHeadWarps<T, BACK>;
   const void* f = a.inter ? (const void*)&vrQkHeads<T, W, true, BACK> : (const void*)&vrQkHeads<T, W, false, BACK>;
   const uint32_t at = kAtOnce * (32 / a.lanes);
   a.steps[0] = (a.heads[0] + at - 1) / at;
   a.steps[1] = a.steps[0] + (a.heads[1] + at - 1) / at;
   // One round of blocks; of few steps, a warp for each.
-  const uint64_t need = ((uint64_t)a.all * a.steps[1] + kWarps - 1) / kWarps, most = (uint64_t)kSMs * kBlocks<BACK>;
+  const uint64_t need = ((uint64_t)a.all * a.steps[1] + WARPS - 1) / WARPS, most = (uint64_t)kSMs * kBlocks<BACK>;
   a.blocks = (uint32_t)(need < most ? need : most);
-  a.warps = a.blocks * kWarps;
+  a.warps = a.blocks * WARPS;
   a.rounds = a.all / a.warps;
   const uint32_t rest = a.all % a.warps * a.steps[1];  // below 2^12 tokens of below 2^17 steps
   a.quota = rest / a.warps;
   a.extra = rest % a.warps;
-  size_t smem = (size_t)kWarps * kStages * ((BACK ? 4 : 2) * 512 * kAtOnce + a.rot * sizeof(float)) +
+  size_t smem = (size_t)WARPS * kStages * ((BACK ? 4 : 2) * 512 * kAtOnce + a.rot * sizeof(float)) +
                 2 * a.dim * sizeof(float);
   if constexpr (BACK) {
-    const size_t sums = (size_t)kWarps * 2 * a.dim * sizeof(float);
+    const size_t sums = (size_t)WARPS * 2 * a.dim * sizeof(float);
     if (smem < sums) smem = sums;
   }
   if (!setOnce(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ||
       !setOnce(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared))
     return vrCudaError;
-  return launch(f, dim3(a.blocks), dim3(kThreads), smem, st, a);
+  return launch(f, dim3(a.blocks), dim3(32 * WARPS), smem, st, a);
 }
 
 // An argument for the kernels; what the stride of an axis of one element is does not matter.
