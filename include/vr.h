@@ -586,8 +586,9 @@ VR_API vrResult_t vrPreferenceLossWorkspace(size_t pairs, size_t* bytes);
  *   loss = scale sum over pairs of (1 - labelSmoothing) log(1 + exp(-h)) + labelSmoothing log(1 + exp(h))
  *  starts   [device] 2 pairs + 1 numbers of rows: sequence s is the rows from starts[s] to
  *           before starts[s + 1], cut at the rows that there are; none where the second is
- *           not larger. Rows of no sequence count for nothing. NULL: the rows in 2 pairs
- *           equal parts.
+ *           not larger. Rows of no sequence count for nothing. They do not decrease: where
+ *           they do and a row is in two sequences, its derivative is that of either.
+ *           NULL: the rows in 2 pairs equal parts.
  *  targets  negative: the row (of a prompt, or padding) counts for nothing.
  *  refLogps     [device] 2 pairs floats, or NULL: zeros.
  *  loss     [device] one float.  logps   [device] 2 pairs floats, S.

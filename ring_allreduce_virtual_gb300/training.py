@@ -865,7 +865,7 @@ def preference_loss_forward(logits, targets, ref_logps=None, starts=None, beta=0
     with logps (2, pairs) the sums of the sequences' log probabilities, row 0 of the chosen
     ones, row 1 of the rejected ones. The sequences are the rows of `logits` in that order:
     (2 pairs, tokens, vocabulary), or packed with starts, int64, of 2 pairs + 1 rows where
-    sequences begin and end. Tokens of negative targets (prompts, padding) count for nothing.
+    sequences begin and end, none smaller than the one before. Tokens of negative targets (prompts, padding) count for nothing.
     ref_logps: float32 (2, pairs), None: zeros. dlogp is the loss's gradient by the tokens'
     log probabilities: token_logprobs_backward makes the logits' of it."""
     if stream is not None:
