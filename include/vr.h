@@ -486,8 +486,9 @@ VR_API vrResult_t vrDropout(const void* x, const void* residual, void* y, size_t
  *  dim      1 .. 1024.   rotaryDim   even, 0 .. dim; with 0 neither tables nor positions
  *           are examined.   qHeads 1 .. 65535, kHeads 0 .. 65535.
  *  eps      >= 0, finite.   dtype, weightType   as for vrLayerNormForward.
- * Heads whose rows start on 16-byte boundaries and whose halves are whole 16 bytes are the
- * fastest. */
+ * The sum of a head's squares has to be a float's, as that of elements below 1e17 is (beyond it
+ * r is 0); a NaN or infinity reaches its own head alone. Heads whose rows start on 16-byte
+ * boundaries and whose halves are whole 16 bytes are the fastest. */
 VR_API vrResult_t vrQkNormRopeForward(
     const void* q, size_t qHeads, const size_t* qStrides, const void* k, size_t kHeads,
     const size_t* kStrides, const void* qWeight, const void* kWeight, void* qOut,
