@@ -339,7 +339,7 @@ constexpr int kRowThreads = 256;
 
 // A block for each row, or a warp for each of a block's, read once, the next packs on their
 // way while the last are summed. Bound by HBM for long rows: 4096 x 131072 bf16 155 us, 1.03 of
-// the measured copy peak; 8192 x 32000 0.88, 16384 x 5000 0.63 (a row's way from its target
+// the measured copy peak; 8192 x 32000 0.98, 16384 x 5000 0.69 (a row's way from its target
 // to its sum is some 4 us, of which blocks of 10 KB cannot hide all).
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constant__ LossArgs a) {
@@ -460,8 +460,8 @@ __device__ __forceinline__ void zero_packs(T* p, I from, I to, I step, bool alik
 // each block with its part of it. A block's way is 8.5 to 10 us (its target 0.8, its copies 3.8,
 // sums and their joining 1.1, a cluster's 1.5, the loss 0.7, the gradient 2.1), three or four
 // blocks are on an SM: 0.84 to 0.90 of the measured copy peak for rows over 32000 bf16 (8192 x
-// 50001, half of the rows counting, 214 us; the two kernels of one pass each 273; all counting 306
-// and 397). What took it there from 0.49 is four packs a thread side by side, in straight lines.
+// 50001, half of the rows counting, 214 us; the two kernels of one pass each 274; all counting 302
+// and 393). What took it there from 0.49 is four packs a thread side by side, in straight lines.
 constexpr int kLossThreads = 256;
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kLossThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
@@ -743,7 +743,9 @@ vrResult_t dispatch(vrDataType_t t, F f) {
 
 template <typename T, int KIND>
 vrResult_t rowLogs(LossArgs& a, cudaStream_t st) {
-  // Eight packs a thread, up to 256 threads; rows of a warp eight in a block. Few rows are
+  // Up to 256 threads, of 32 packs each, so that many rows are on their way at a time (8192 x
+  // 32000 bf16 80 us, of 8 packs 88); 8 packs where there are few rows; rows of a warp eight in a
+  // block. Few rows are
   // clusters', in parts of 32 KB at least, up to the four blocks of an SM; the fewest in
   // parts of 8 KB (200 x 32000 bf16 in clusters 5.9 us, without 5.2).
   const uint64_t packs = a.cols / kV<T>;
@@ -752,7 +754,8 @@ vrResult_t rowLogs(LossArgs& a, cudaStream_t st) {
   const uint64_t part = (packs + ctas - 1) / ctas;
   a.ctas = ctas;
   a.part = (uint32_t)part;
-  uint64_t threads = (part / 8 + 31) / 32 * 32;
+  const uint64_t each = a.rows * ctas > 8 * kSMs ? 32 : 8;
+  uint64_t threads = (part / each + 31) / 32 * 32;
   threads = threads < 32 ? 32 : threads > kRowThreads ? kRowThreads : threads;
   const unsigned y = threads == 32 ? kRowThreads / 32 : 1;
   const uint64_t groups = (a.rows + y - 1) / y, most = 1u << 20;
@@ -770,10 +773,12 @@ template <typename T>
 vrResult_t rowGrads(LossArgs& a, cudaStream_t st) {
   alikeRows<T>(a);
   const uint64_t packs = a.cols / kV<T> ? a.cols / kV<T> : 1;
-  // A row's threads, a power of two, up to a block; parts of 4096 packs, of 1024 where those
-  // are few.
+  // A row's threads, a power of two up to a block, of 32 packs each (16384 x 5000 bf16 55 us, of 4
+  // packs 105), or as many as fill the GPU three blocks an SM; parts of 4096 packs, of 1024 where
+  // those are few.
   unsigned x = 32;
-  while (x < kGradThreads && x * 4 < packs) x *= 2;
+  while (x < kGradThreads && x * 32 < packs) x *= 2;
+  while (x < kGradThreads && x * 4 < packs && a.rows * x < 3ull * kSMs * kGradThreads) x *= 2;
   const unsigned y = kGradThreads / x;
   a.part = a.rows * packs >= (uint64_t)kSMs * 16 * 4096 ? 4096 : 1024;
   a.segments = (packs + a.part - 1) / a.part;
@@ -797,7 +802,10 @@ bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
   // Few rows are spread over more SMs, in parts of 8 KB at least, up to six blocks on each.
   while (ctas < 8 && a.rows * ctas * 2 <= 6 * kSMs && packs / ctas >= 1024) ctas *= 2;
   const uint64_t part = (packs + ctas - 1) / ctas;
-  uint64_t threads = (part / 4 + 31) / 32 * 32;
+  // 16 packs a thread, so that many rows are on their way at a time (16384 x 8000 bf16 93 us, of 8
+  // packs 98, of 4 142; of 32 133); 4 where there are few.
+  const uint64_t each = a.rows * ctas > 6 * kSMs ? 16 : 4;
+  uint64_t threads = (part / each + 31) / 32 * 32;
   threads = threads < 32 ? 32 : threads > kLossThreads ? kLossThreads : threads;
   const unsigned y = threads == 32 ? kLossThreads / 32 : 1;
   const uint64_t blocks = (a.rows + y - 1) / y * ctas;
