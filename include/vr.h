@@ -585,6 +585,8 @@ VR_API vrResult_t vrPreferenceLossWorkspace(size_t pairs, size_t* bytes);
  * pair s's chosen one, pairs + s its rejected one; S is the sum of logp over a sequence's rows.
  *   h = beta ((S - ref)[chosen] - (S - ref)[rejected])
  *   loss = scale sum over pairs of (1 - labelSmoothing) log(1 + exp(-h)) + labelSmoothing log(1 + exp(h))
+ * A term whose factor is 0 is left out: an impossible token (a target's logit of -inf) in one of
+ * a pair's sequences makes h infinite and the pair's loss 0 or infinite, not NaN; in both, NaN.
  *  starts   [device] 2 pairs + 1 numbers of rows: sequence s is the rows from starts[s] to
  *           before starts[s + 1], cut at the rows that there are; none where the second is
  *           not larger. Rows of no sequence count for nothing. They do not decrease: where

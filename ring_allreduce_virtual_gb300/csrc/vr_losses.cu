@@ -705,7 +705,10 @@ __global__ void __launch_bounds__(kOneBlock) vrPairLosses(const __grid_constant_
     const float soft = log1pf(e);
     const float up = soft + fmaxf(f, 0.f), down = soft + fmaxf(-f, 0.f);  // softplus of f and -f
     const float p = (f >= 0.f ? 1.f : e) / (1.f + e), q = (f >= 0.f ? e : 1.f) / (1.f + e);
-    loss += (double)((1.f - a.smoothing) * down + a.smoothing * up);
+    // A term of factor 0 is left out: it may be infinite (of an impossible token's sum of -inf).
+    float pair = a.smoothing < 1.f ? (1.f - a.smoothing) * down : 0.f;
+    if (a.smoothing > 0.f) pair += a.smoothing * up;
+    loss += (double)pair;
     // in the place of the chosen one's sum; NaN stays one
     a.sums[i] = (double)(a.scale * a.beta * (a.smoothing * p - (1.f - a.smoothing) * (f == f ? q : f)));
   }

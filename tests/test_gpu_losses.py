@@ -403,6 +403,42 @@ def test_extreme_margins():
     assert torch.isnan(nan[0]) and torch.isnan(nan[3]).all()
 
 
+@pytest.mark.parametrize("smoothing", [0.0, 0.1, 1.0])
+@pytest.mark.parametrize("beta", [0.5, -0.5])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_infinite_margins(dtype, beta, smoothing):
+    # An impossible token makes its sequence's sum -inf and the pair's margin infinite: one term of the pair's loss is
+    # infinite and the other 0, and a term that the smoothing leaves out counts for nothing.
+    inf = float("inf")
+    x, t, g = make(21, 8, 40, dtype)
+    s = torch.arange(0, 9, 2, device="cuda")  # the rows of two chosen sequences, then of two rejected ones
+    clean = training.preference_loss_forward(x, t, None, s, beta, smoothing)
+    for row in (1, 4):  # of pair 0, the chosen and the rejected sequence
+        y = x.clone()
+        y[row, t[row]] = -inf
+        up = (row == 4) == (beta > 0)  # the margin is +inf
+        far = smoothing != 0.0 if up else smoothing != 1.0
+        value, sums, lse, dlogp = training.preference_loss_forward(y, t, None, s, beta, smoothing)
+        loss, logps, dlogits = training.preference_loss_gradient(y, t, None, s, beta, smoothing)
+        assert same(value, loss) and same(sums, logps)
+        assert sums[row // 4, 0] == -inf and same(sums[:, 1], clean[1][:, 1])
+        # what is left is the other pair's loss, of sums that were rounded once each
+        a, b = sums[:, 1].tolist()
+        h = beta * (a - b)
+        rest = (1 - smoothing) * math.log1p(math.exp(-h)) + smoothing * math.log1p(math.exp(h))
+        off = abs(beta) * U * (abs(a) + abs(b)) + 6 * U * (1 + abs(h))
+        assert float(value) == inf if far else abs(float(value) - rest) <= off
+        c = beta * (smoothing if up else smoothing - 1)
+        want = torch.tensor([c, c, -c, -c], device="cuda")
+        assert ((dlogp[[0, 1, 4, 5]] - want).abs() <= 4 * U * abs(c)).all()
+        assert same(dlogp[[2, 3, 6, 7]], clean[3][[2, 3, 6, 7]])
+        lse = torch.logsumexp(y.double(), 1)
+        check_grad(dlogits, y, t, dlogp.double(), lse, lse_far(y, lse))
+    # a margin of two infinities is none
+    y[1, t[1]] = y[4, t[4]] = -inf
+    assert torch.isnan(training.preference_loss_forward(y, t, None, s, beta, smoothing)[0])
+
+
 def test_differentiable_calls():
     x, t, g = make(6, 24, 90, torch.float32)
     args = policy_inputs(x, t, g)
