@@ -549,7 +549,7 @@ def qk_norm_rope_forward(q, k, q_weight=None, k_weight=None, cos=None, sin=None,
         code, wcode, _raw_stream(device))
     if rc:
         raise vr.VrError(rc, "vrQkNormRopeForward")
-    for t in (q_out, k_out):
+    for t in (q_out, k_out if k is not None else None):
         if t is not None:
             _written(t)
     return yq, yk
@@ -568,7 +568,8 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight=None, k_weight=None, cos=None, 
     returned) or a tensor to write to, such as a view of the flat bucket that the AllReduce
     takes; they have the weights' type (q's without). dq_in and dk_in: tensors for the
     gradients of q and k, such as views of one projection's gradient; dq and dk themselves
-    allowed."""
+    allowed. With k None, dk and dk_in are not examined, and a tensor given as dk_weight
+    is filled with zeros."""
     if stream is not None:
         return _on(stream, q.get_device(), qk_norm_rope_backward, dq, dk, q, k, q_weight, k_weight,
                    cos, sin, positions, eps, interleaved, dq_weight, dk_weight, dq_in, dk_in)
@@ -578,7 +579,8 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight=None, k_weight=None, cos=None, 
                           positions, eps, interleaved, dq_weight, dk_weight, dq_in, dk_in)
     batch, tokens, heads, dim, qs = _head_layout(q.shape, q.stride())
     dtype = q.dtype
-    given = [t for t in (dq_weight, dk_weight, dq_in, dk_in) if isinstance(t, torch.Tensor)]
+    given = [t for t in (dq_weight, dk_weight, dq_in, None if k is None else dk_in)
+             if isinstance(t, torch.Tensor)]
     wcode = _head_weights(q, dim, device, q_weight, k_weight, *[
         t for t in (dq_weight, dk_weight) if isinstance(t, torch.Tensor)])
     dqs = _heads(dq, q.shape, dtype, device, "dq")
@@ -591,7 +593,9 @@ def qk_norm_rope_backward(dq, dk, q, k, q_weight=None, k_weight=None, cos=None, 
         dk_in = torch.empty_like(k) if dk_in is None else dk_in
         dkis = _heads(dk_in, k.shape, dtype, device, "dk_in")
     else:
-        dk, dk_in, dk_weight = None, None, False
+        dk, dk_in = None, None
+        if not isinstance(dk_weight, torch.Tensor):  # a given one becomes zeros
+            dk_weight = False
     grads = [dq_weight, dk_weight]
     for i in (0, 1):
         if grads[i] is True:

@@ -215,6 +215,32 @@ def test_no_keys():
     assert same(got[0], training.qk_norm_rope_backward(yq, None, q, None)[0])
 
 
+def test_no_keys_with_tensors_given():
+    # the gradient of a weight of no keys is zeros in the tensor that is given for it
+    q, dq = torch.randn(3, 4, 16, device="cuda"), torch.randn(3, 4, 16, device="cuda")
+    want = training.qk_norm_rope_backward(dq, None, q, None)
+    for t in (torch.float32, torch.bfloat16):
+        x, d = q.to(t), dq.to(t)
+        bucket = torch.full((48,), 7.0, device="cuda", dtype=t)
+        got = training.qk_norm_rope_backward(d, None, x, None, dq_weight=bucket[:16], dk_weight=bucket[16:32])
+        assert got[3].data_ptr() == bucket[16:].data_ptr() and got[1] is None
+        assert bool((bucket[16:32] == 0).all()) and bool((bucket[32:] == 7.0).all())
+        assert t is not torch.float32 or (same(got[0], want[0]) and same(bucket[:16], want[2]))
+        bucket[16:32] = 7.0
+        got = training.qk_norm_rope_backward(d, None, x, None, dq_weight=False, dk_weight=bucket[16:32])
+        assert got[2] is None and bool((bucket[16:32] == 0).all())
+    bucket.fill_(7.0)
+    none = torch.empty(0, 4, 16, device="cuda", dtype=t)  # no tokens either
+    training.qk_norm_rope_backward(none, None, none, None, dk_weight=bucket[16:32])
+    assert bool((bucket[16:32] == 0).all()) and bool((bucket[:16] == 7.0).all())
+    # a tensor for the keys that there are none of is not written, and not said to be
+    other = torch.full_like(q, 7.0)
+    v = other._version
+    assert training.qk_norm_rope_forward(q, None, k_out=other)[1] is None
+    assert training.qk_norm_rope_backward(dq, None, q, None, dk_in=other)[1] is None
+    assert other._version == v and bool((other == 7.0).all())
+
+
 def test_strides_of_axes_of_one_element_do_not_matter():
     q = torch.randn(2, 1, 3, 64, device="cuda").bfloat16()
     t = q.as_strided(q.shape, (192, 7, 64, 1))
