@@ -558,7 +558,8 @@ VR_API vrResult_t vrPolicyLossWorkspace(size_t rows, size_t* bytes);
  *     + klCoef (exp(refLogp - logp) - (refLogp - logp) - 1)
  * and loss = scale sum(weight times the row's loss). Where the clipped ratio decides the
  * first term has no derivative.
- *  oldLogp, advantages (A)   [device] rows floats.
+ *  oldLogp, advantages (A)   [device] rows floats. The first term of a row of advantage 0 is 0,
+ *           but NaN where e is: broken logits, or a target that is none, are not hidden.
  *  weights  [device] rows floats, or NULL: ones. A row of weight 0, or of a negative
  *           target, counts for nothing, whatever its other inputs hold.
  *  refLogp  [device] rows floats, or NULL: no such term; nor is there one if klCoef is 0.

@@ -222,7 +222,7 @@ __device__ __forceinline__ float2 finish_row(const LossArgs& a, uint64_t row, co
     } else if (A < 0.f && below < 0.f) {
       loss.s = -a.least.x, loss.e = -a.least.y;
       loss.times(A);
-    } else if (A != 0.f) {
+    } else if (A != 0.f || e.s != e.s) {  // an advantage of 0 hides no NaN
       const float f = e.value();
       if (f > -0.5f) {
         loss.s = -A;

@@ -268,6 +268,46 @@ def test_impossible_tokens_infinities_and_nan(dtype, cols):
     assert torch.isnan(dx[3]).any() and bool((dx[0, 20:] == 0).all())
 
 
+@pytest.mark.parametrize("cols", [40, 3001, 450001])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_rows_of_no_number_without_advantage(dtype, cols):
+    # a row of advantage 0 has neither loss nor gradient, but a NaN in it is not hidden
+    inf, nan = float("inf"), float("nan")
+    x, t, g = make(cols + 1, 7, cols, dtype)
+    lp = training.token_logprobs_forward(x, t)[0]
+    old, zero = lp + 0.1, torch.zeros(7, device="cuda")
+    for f in (training.policy_loss_gradient, training.policy_loss_forward):
+        got = f(x, t, old, zero)
+        assert float(got[0]) == 0 and bool((got[-1] == 0).all())
+    adv = torch.where(torch.arange(7, device="cuda") == 6, 1.0, 0.0)
+    clean = training.policy_loss_gradient(x, t, old, adv)
+
+    def look(y, targets, o):
+        loss, logp, dx = training.policy_loss_gradient(y, targets, o, adv)
+        l2, _, _, dlogp = training.policy_loss_forward(y, targets, o, adv)
+        assert torch.isnan(loss) and torch.isnan(l2) and torch.isnan(dlogp[3])
+        assert torch.isnan(dx[3]).any() and bool((dlogp[[0, 1, 2, 4, 5]] == 0).all())
+        rest = [0, 1, 2, 4, 5, 6]
+        assert same(dx[rest], clean[2][rest]) and same(logp[rest], clean[1][rest])
+    for column, value in ((0, nan), (cols - 1, nan), (cols // 2, inf), (slice(None), -inf)):
+        y = x.clone()
+        y[3, column] = value
+        look(y, t, old)
+    none, o = t.clone(), old.clone()
+    none[3], o[3] = cols, nan
+    look(x, none, old)
+    look(x, t, o)
+    # of weight 0 it counts for nothing all the same
+    w = torch.ones(7, device="cuda")
+    w[3] = 0
+    assert float(training.policy_loss_gradient(x, none, o, zero, w)[0]) == 0
+    # an impossible token is a number: ratio 0
+    y = x.clone()
+    y[3, t[3]] = -inf
+    got = training.policy_loss_gradient(y, t, old, zero)
+    assert float(got[0]) == 0 and got[1][3] == -inf and bool((got[2] == 0).all())
+
+
 def test_rows_of_large_logits():
     # an offset that is the same for all of a row's logits changes nothing, but for the logits' own rounding
     x, t, g = make(12, 40, 500, torch.float32)
