@@ -562,7 +562,8 @@ VR_API vrResult_t vrPolicyLossWorkspace(size_t rows, size_t* bytes);
  *           but NaN where e is: broken logits, or a target that is none, are not hidden.
  *  weights  [device] rows floats, or NULL: ones. A row of weight 0, or of a negative
  *           target, counts for nothing, whatever its other inputs hold.
- *  refLogp  [device] rows floats, or NULL: no such term; nor is there one if klCoef is 0.
+ *  refLogp  [device] rows floats, or NULL: no such term; nor is there one if klCoef is 0. Where
+ *           refLogp - logp is infinite, either way, so is the term.
  *  loss     [device] one float. 0 without rows.
  *  logp, lse, rest, dlogp   [device] rows floats: the last is the loss's derivative by logp, for
  *           vrTokenLogProbsBackward. Rows that count for nothing get zeros in all of them.

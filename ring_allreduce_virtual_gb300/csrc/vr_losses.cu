@@ -237,7 +237,7 @@ __device__ __forceinline__ float2 finish_row(const LossArgs& a, uint64_t row, co
       d.s = in.ref;
       d.add(-lp.s, -lp.e);
       const float r = d.value(), x = expm1f(r);
-      loss.add(a.kl * (x - r));
+      loss.add(a.kl * (x < INFINITY ? x - r : x));  // of an impossible token r is infinite too
       c = fmaf(-a.kl, x, c);
     }
     loss.times(in.weight);

@@ -308,6 +308,24 @@ def test_rows_of_no_number_without_advantage(dtype, cols):
     assert float(got[0]) == 0 and got[1][3] == -inf and bool((got[2] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_impossible_tokens_far_from_the_reference(dtype):
+    # exp(d) - d - 1 grows without bound on both sides
+    inf = float("inf")
+    x, t, g = make(31, 4, 100, dtype)
+    lp = training.token_logprobs_forward(x, t)[0]
+    adv, w = torch.ones(4, device="cuda"), torch.ones(4, device="cuda")
+    y = x.clone()
+    y[2, t[2]] = -inf  # d = inf
+    ref = lp.clone()
+    ref[2] = -inf  # d = -inf
+    for logits, r in ((y, lp), (x, ref)):
+        for f in (training.policy_loss_gradient, training.policy_loss_forward):
+            got = f(logits, t, lp, adv, w, r, kl_coef=0.1)
+            assert float(got[0]) == inf
+        assert float(got[3][2]) == (-inf if r is lp else got[3][2]) and torch.isfinite(got[3][[0, 1, 3]]).all()
+
+
 def test_rows_of_large_logits():
     # an offset that is the same for all of a row's logits changes nothing, but for the logits' own rounding
     x, t, g = make(12, 40, 500, torch.float32)
