@@ -388,6 +388,9 @@ __global__ void __launch_bounds__(32 * kHeadWarps<T, BACK>, kBlocks<BACK>) vrQkH
     bool load = first || !BACK;  // the angles, forward each kind's with its weights
 #pragma unroll 1
     for (; now.step < end; ++now.step) {
+      // All lanes have read the angles of the token before, whose place a copy may fill again now (of
+      // tokens of one step); where a head is one lane's, no shuffle holds the lanes together.
+      if (first) __syncwarp();
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
       if (load) {

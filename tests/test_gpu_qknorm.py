@@ -313,6 +313,21 @@ def test_graphs_and_streams():
     assert out._version > v and same(out, eager[0])
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype,dim", [(torch.bfloat16, 16), (torch.float16, 16), (torch.float32, 8), (torch.bfloat16, 8),
+                                       (torch.float32, 4)], ids=str)
+@pytest.mark.parametrize("heads", [1, 30, 64])
+def test_heads_of_one_lane_without_keys(heads, dtype, dim, inter):
+    # tokens of one step each, of which a warp takes many one after the other with angles of their own
+    q, _, dq, _, w, tables, pos = inputs(dim + heads, 2, 20000, heads, 1, dim, dim, dtype, torch.float32, "dense")
+    args = (w[0], None, *tables, pos, EPS, inter)
+    y, none = training.qk_norm_rope_forward(q, None, *args)
+    assert none is None
+    check_forward(y, q, w[0], tables, pos, inter)
+    got = training.qk_norm_rope_backward(dq, None, q, None, *args)
+    check_backward(got[0], got[2], dq, q, w[0], tables, pos, inter)
+
+
 def test_far_elements():
     # a token more than 2^32 elements behind the first
     n = (1 << 32) // 128 + 3
