@@ -10,6 +10,7 @@
 // is bound by memory traffic: a head is read once and written once (dy and x are read
 // in the backward pass), and a token's angles once for all of its heads.
 #include "vr_packs.cuh"
+#include "vr_places.h"
 
 namespace {
 
@@ -700,30 +701,13 @@ bool badSide(const void* p, size_t heads, const size_t* st, const Shape& s, int 
   return false;
 }
 
-// The bytes of an argument as rows: its outermost axis, or the two outermost where they
-// step alike; what lies inside counts as taken in full.
-Bytes bytesOfSide(const void* p, size_t heads, const size_t* st, const Shape& s, int es) {
-  if (!p) return {0, 0, 0, 0};
-  struct Axis {
-    uint64_t n, stride;
-  } ax[3] = {{s.batch, st[0]}, {s.tokens, st[1]}, {heads, st[2]}};
-  for (int i = 0; i < 3; ++i)  // outermost first, axes of one element last
-    for (int j = i + 1; j < 3; ++j)
-      if (ax[j].n > 1 && (ax[i].n <= 1 || ax[j].stride > ax[i].stride)) {
-        const Axis t = ax[i];
-        ax[i] = ax[j], ax[j] = t;
-      }
-  uint64_t rows = ax[0].n, stride = ax[0].stride, width = s.dim;
-  int inside = 1;
-  if (ax[1].n > 1 && stride == ax[1].n * ax[1].stride) {
-    rows *= ax[1].n;
-    stride = ax[1].stride;
-    inside = 2;
-  }
-  for (int i = inside; i < 3; ++i) width += (ax[i].n - 1) * (ax[i].n > 1 ? ax[i].stride : 0);
-  if (rows <= 1) stride = width;
-  if (rows > 1 && stride < width) return bytesOf(p, ((rows - 1) * stride + width) * es);
-  return bytesOf(p, rows, width, stride, es);
+// The bytes of an argument.
+Places placesOf(const void* p, size_t heads, const size_t* st, const Shape& s, int es) {
+  Places b(p, s.dim * es);
+  b.axis(s.batch, st[0] * es);
+  b.axis(s.tokens, st[1] * es);
+  b.axis(heads, st[2] * es);
+  return b;
 }
 
 template <typename F>
@@ -839,14 +823,14 @@ vrResult_t begin(Call& c, const void* q, size_t qHeads, const size_t* qStrides, 
 }
 
 // The arguments that no output may touch.
-int inputs(const Call& c, Bytes* in) {
+int inputs(const Call& c, Places* in) {
   const QkArgs& a = c.a;
   const size_t table = a.rot ? a.tableRows * (a.rot / 2) * 4 : 0;
-  in[0] = bytesOf(a.w[0], c.s.dim * c.ws);
-  in[1] = bytesOf(a.w[1], c.s.dim * c.ws);
-  in[2] = bytesOf(a.cos, table);
-  in[3] = bytesOf(a.sin, table);
-  in[4] = bytesOf(a.positions, a.rot ? ((c.s.batch - 1) * a.positionStride + c.s.tokens) * (a.wide ? 8 : 4) : 0);
+  in[0] = Places(a.w[0], c.s.dim * c.ws);
+  in[1] = Places(a.w[1], c.s.dim * c.ws);
+  in[2] = Places(a.cos, table);
+  in[3] = Places(a.sin, table);
+  in[4] = Places(a.positions, a.rot ? ((c.s.batch - 1) * a.positionStride + c.s.tokens) * (a.wide ? 8 : 4) : 0);
   return 5;
 }
 
@@ -875,13 +859,12 @@ extern "C" VR_API vrResult_t vrQkNormRopeForward(
   a.out[0] = sideOf(qOut, qHeads, qOutStrides, c.s);
   if (kHeads) a.out[1] = sideOf(kOut, kHeads, kOutStrides, c.s);
   // In place is allowed, each for itself.
-  Bytes in[7];
+  Places in[5];
   const int n = inputs(c, in);
-  const Bytes qIn = bytesOfSide(q, qHeads, qStrides, c.s, c.es), qo = bytesOfSide(qOut, qHeads, qOutStrides, c.s, c.es);
-  const Bytes none = {0, 0, 0, 0};
-  const Bytes kIn = kHeads ? bytesOfSide(k, kHeads, kStrides, c.s, c.es) : none;
-  const Bytes ko = kHeads ? bytesOfSide(kOut, kHeads, kOutStrides, c.s, c.es) : none;
-  const Bytes outs[] = {qo, ko};
+  const Places qIn = placesOf(q, qHeads, qStrides, c.s, c.es), qo = placesOf(qOut, qHeads, qOutStrides, c.s, c.es);
+  const Places kIn = kHeads ? placesOf(k, kHeads, kStrides, c.s, c.es) : Places();
+  const Places ko = kHeads ? placesOf(kOut, kHeads, kOutStrides, c.s, c.es) : Places();
+  const Places outs[] = {qo, ko};
   if (anyOverlap(outs, 2, in, n) || overlap(qo, kIn) || overlap(ko, qIn) ||
       (!(q == qOut && same(qStrides, qOutStrides)) && overlap(qo, qIn)) ||
       (kHeads && !(k == kOut && same(kStrides, kOutStrides)) && overlap(ko, kIn)))
@@ -944,19 +927,18 @@ extern "C" VR_API vrResult_t vrQkNormRopeBackward(
   a.dw[0] = dqWeight, a.dw[1] = dkWeight;
   a.partials = params ? (float*)workspace : nullptr;
   // dq and dk may be overwritten by what is computed from them, each for itself.
-  Bytes in[9];
+  Places in[7];
   int n = inputs(c, in);
-  const Bytes none = {0, 0, 0, 0};
-  in[n++] = bytesOfSide(q, qHeads, qStrides, c.s, c.es);
-  in[n++] = kHeads ? bytesOfSide(k, kHeads, kStrides, c.s, c.es) : none;
+  in[n++] = placesOf(q, qHeads, qStrides, c.s, c.es);
+  in[n++] = kHeads ? placesOf(k, kHeads, kStrides, c.s, c.es) : Places();
   const bool overQ = dq == dqIn && same(dqStrides, dqInStrides);
   const bool overK = kHeads && dk == dkIn && same(dkStrides, dkInStrides);
-  const Bytes dqb = bytesOfSide(dq, qHeads, dqStrides, c.s, c.es);
-  const Bytes dkb = kHeads ? bytesOfSide(dk, kHeads, dkStrides, c.s, c.es) : none;
-  const Bytes outs[] = {bytesOfSide(dqIn, qHeads, dqInStrides, c.s, c.es),
-                        kHeads ? bytesOfSide(dkIn, kHeads, dkInStrides, c.s, c.es) : none,
-                        bytesOf(dqWeight, dim * c.ws), bytesOf(dkWeight, dim * c.ws),
-                        bytesOf(params ? workspace : nullptr, workspaceOf(dim))};
+  const Places dqb = placesOf(dq, qHeads, dqStrides, c.s, c.es);
+  const Places dkb = kHeads ? placesOf(dk, kHeads, dkStrides, c.s, c.es) : Places();
+  const Places outs[] = {placesOf(dqIn, qHeads, dqInStrides, c.s, c.es),
+                         kHeads ? placesOf(dkIn, kHeads, dkInStrides, c.s, c.es) : Places(),
+                         Places(dqWeight, dim * c.ws), Places(dkWeight, dim * c.ws),
+                         Places(params ? workspace : nullptr, workspaceOf(dim))};
   if (anyOverlap(outs, 5, in, n)) return vrInvalidArgument;
   for (int i = 0; i < 5; ++i)
     if ((!(i == 0 && overQ) && overlap(outs[i], dqb)) || (!(i == 1 && overK) && overlap(outs[i], dkb)))

@@ -154,6 +154,42 @@ def test_in_place_in_one_projection():
     assert bool((grad[:, :, hq + hk:] == 7.0).all())
 
 
+def test_in_place_in_one_projection_without_some_tokens():
+    # q, k and v of one buffer of which the first token of each batch, or the last, is left out; of halves of heads;
+    # of heads before tokens
+    b, t, hq, hk, d = 3, 5, 6, 2, 64
+    g = torch.Generator("cuda").manual_seed(4)
+    tables, pos = (torch.randn(9, 16, device="cuda"), torch.randn(9, 16, device="cuda")), torch.arange(t - 1, device="cuda")
+
+    def views(buf, layout):
+        if layout == "first":
+            return buf[:, 1:, :hq], buf[:, 1:, hq: hq + hk]
+        if layout == "last":
+            return buf[:, :-1, :hq], buf[:, :-1, hq: hq + hk]
+        if layout == "halves":
+            return buf[:, 1:, :, :32], buf[:, 1:, :, 32:]
+        x = buf.view(b, hq + 2 * hk, t, d)[:, :, 1:].transpose(1, 2)
+        return x[:, :, :hq], x[:, :, hq: hq + hk]
+    for layout in ("first", "last", "halves", "heads"):
+        was = torch.randn(b, t, hq + 2 * hk, d, generator=g, device="cuda").bfloat16()
+        q, k = (v.contiguous() for v in views(was, layout))
+        args = (None, None, *(c[:, :8] if layout == "halves" else c for c in tables))
+        args = tuple(a.contiguous() if a is not None else None for a in args) + (pos,)
+        yq, yk = training.qk_norm_rope_forward(q, k, *args)
+        grads = training.qk_norm_rope_backward(yq, yk, q, k, *args)
+        buf, grad = was.clone(), torch.full_like(was, 7.0)
+        vq, vk = views(buf, layout)
+        training.qk_norm_rope_forward(vq, vk, *args, q_out=vq, k_out=vk)
+        gq, gk = views(grad, layout)
+        training.qk_norm_rope_backward(vq, vk, *views(was, layout), *args, dq_in=gq, dk_in=gk)
+        assert same(vq, yq) and same(vk, yk) and same(gq, grads[0]) and same(gk, grads[1]), layout
+        for x, y in ((vq, vk), (gq, gk)):  # and nothing else
+            x.fill_(0), y.fill_(0)
+        for x in views(was, layout):
+            x.fill_(0)
+        assert same(buf, was) and int((grad != 0).sum()) == int((grad == 7.0).sum()) == grad.numel() - q.numel() - k.numel()
+
+
 def test_positions():
     size = (3, 7, 4, 2, 32, 16)
     q, k, dq, dk, w, tables, _ = inputs(5, *size, torch.float32, torch.float32, "dense")

@@ -76,6 +76,19 @@ def test_qk_forward_refuses_overlaps(vr, bad):
     refused(vr, vr.vrQkNormRopeForward, *{**QK, **bad}.values())
 
 
+S9 = (9 * 16 * 16, 16 * 16, 16)  # 8 of 9 tokens of up to 16 heads
+
+
+@pytest.mark.parametrize("k,q_out,k_out", [
+    (A + 7 * 32, A, FAR), (A + 8 * 32, A, A + 7 * 32), (A + 8 * 32, A, A + 8 * 32 + 16), (A + 512 - 30, A, FAR),
+    (A + 8 * 32, A + 512, FAR), (A + 8 * 32, A, A + 9 * 512 - 30), (A + 8 * 32, A, A + 9 * 512),
+])
+def test_qk_forward_refuses_overlaps_among_some_tokens(vr, k, q_out, k_out):
+    # in place, or shifted, in one projection that has more tokens
+    strides = {name: S9 for name in ("qStrides", "kStrides", "qOutStrides", "kOutStrides")}
+    refused(vr, vr.vrQkNormRopeForward, *{**QK, **strides, "k": k, "qOut": q_out, "kOut": k_out}.values())
+
+
 def test_qk_forward_of_nothing_launches_nothing(vr):
     vr.vrQkNormRopeForward(*{**QK, "batch": 0, "q": 0, "k": 0, "qOut": 0, "kOut": 0}.values())
     vr.vrQkNormRopeForward(*{**QK, "tokens": 0, "q": 0, "k": 0, "qOut": 0, "kOut": 0}.values())
