@@ -14,16 +14,18 @@ namespace vrop {
 
 struct Places {
   static constexpr int kAxes = 3;
-  uintptr_t at = 0;
+  uintptr_t at = 0, end = 0;
   int64_t width = 0;  // 0: nothing
   int axes = 0;
   int64_t n[kAxes], stride[kAxes];
 
   Places() = default;
-  Places(const void* p, uint64_t bytes) : at((uintptr_t)p), width(p ? (int64_t)bytes : 0) {}
+  Places(const void* p, uint64_t bytes) : at((uintptr_t)p), end(at + bytes), width(p ? (int64_t)bytes : 0) {}
   // Of one element, or without a step, it adds nothing.
   void axis(uint64_t count, uint64_t step) {
-    if (count > 1 && step) n[axes] = (int64_t)count, stride[axes++] = (int64_t)step;
+    if (count <= 1 || !step) return;
+    n[axes] = (int64_t)count, stride[axes++] = (int64_t)step;
+    end += (count - 1) * step;
   }
 };
 
@@ -48,7 +50,7 @@ struct PlaceSteps {
 };
 
 inline bool overlap(const Places& a, const Places& b) {
-  if (!a.width || !b.width) return false;
+  if (!a.width || !b.width || a.at >= b.end || b.at >= a.end) return false;
   PlaceSteps s;
   for (int side = 0; side < 2; ++side) {
     const Places& p = side ? b : a;
