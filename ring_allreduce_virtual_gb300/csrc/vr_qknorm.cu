@@ -389,9 +389,6 @@ __global__ void __launch_bounds__(32 * kHeadWarps<T, BACK>, kBlocks<BACK>) vrQkH
     bool load = first || !BACK;  // the angles, forward each kind's with its weights
 #pragma unroll 1
     for (; now.step < end; ++now.step) {
-      // All lanes have read the angles of the token before, whose place a copy may fill again now (of
-      // tokens of one step); where a head is one lane's, no shuffle holds the lanes together.
-      if (first) __syncwarp();
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       copies_wait<kStages - 1>();
       if (load) {
@@ -404,6 +401,10 @@ __global__ void __launch_bounds__(32 * kHeadWarps<T, BACK>, kBlocks<BACK>) vrQkH
         const float* r = rows + (from == 0 ? kStages - 1 : from - 1) * 2 * half;
         if constexpr (BACK) angles.load(at, r, r + half, half);
         else angles.load(at, r, r + half, half, w + kind * a.dim);
+        // Before a copy for a later token takes this one's place (of tokens of one step the next fetch's):
+        // where a head is one lane's, no shuffle holds the lanes together. In front of that fetch it
+        // costs 1 % of the backward pass, here nothing.
+        __syncwarp();
       }
       const uint4* in = ring + stage * (U * NP * 32);
       stage = stage + 1 == kStages ? 0 : stage + 1;
