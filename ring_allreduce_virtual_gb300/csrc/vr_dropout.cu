@@ -190,7 +190,10 @@ __device__ __forceinline__ float if_above(uint32_t h, uint32_t below, float x, f
 // ors. Of the measured copy peak, on 16384 x 8192: bf16 with an addition 1.06 (113 us), at
 // odd numbers 1.00; alone 0.89 (89 us), at odd numbers 0.77 (104 us; with both blocks made
 // in each lane 0.58); float32 alone 1.02. With 32 random bits an element, two blocks for 8, 107
-// us alone; keys added up in the kernel 94.
+// us alone; keys added up in the kernel 94. At odd numbers, 39892 x 2051 float16 (60 us, 0.81; at
+// even ones 53), that pipe is busy for 62 % of the cycles and an instruction issued in 66 % of them:
+// 154 a warp and unit, from 22 warps on an SM. 9973 x 2051 is 17 us (0.69), of which
+// by both sizes 3 do not grow with the elements.
 template <typename T, int U, bool ADD, bool SHIFTED, bool DEVICE>
 __global__ void __launch_bounds__(kThreads, 3) vrDropFlat(const __grid_constant__ DropArgs a) {
   constexpr int N = 8 * (int)sizeof(T) / 16;  // packs of a unit
@@ -275,7 +278,11 @@ __global__ void __launch_bounds__(kThreads, 3) vrDropFlat(const __grid_constant_
 }
 
 // Rows with other elements between them, or tensors that do not lie alike: a thread takes U
-// packs of y, cut at memory's 16-byte boundaries; a row's first and last may be parts.
+// packs of y, cut at memory's 16-byte boundaries; a row's first and last may be parts. Bound by its
+// instructions: whatever a number starts at, a pack makes its own blocks of the generator and finds
+// its row by a division. 16384 x 8192 bf16 with rows 8200 apart 150 us (0.53 of the measured copy
+// peak), at odd numbers 200, with an addition 165 (0.72); from one element off 16 bytes, read in
+// single elements, 163, 196, 227; float32 279, 332, 299 and 239, 289, 285.
 template <typename T, int U, bool ADD, bool DEVICE>
 __global__ void __launch_bounds__(kThreads) vrDropKernel(const __grid_constant__ DropArgs a) {
   constexpr int V = kV<T>;

@@ -339,7 +339,7 @@ constexpr int kRowThreads = 256;
 
 // A block for each row, or a warp for each of a block's, read once, the next packs on their
 // way while the last are summed. Bound by HBM for long rows: 4096 x 131072 bf16 155 us, 1.03 of
-// the measured copy peak; 8192 x 32000 0.98, 16384 x 5000 0.69 (a row's way from its target
+// the measured copy peak; 8192 x 32000 0.97, 16384 x 5000 0.68 (a row's way from its target
 // to its sum is some 4 us, of which blocks of 10 KB cannot hide all).
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kRowThreads, 4) vrRowLogs(const __grid_constant__ LossArgs a) {
@@ -459,9 +459,9 @@ __device__ __forceinline__ void zero_packs(T* p, I from, I to, I step, bool alik
 // come, and read again there for the gradient. A row is a warp's, a block's, or a cluster's,
 // each block with its part of it. A block's way is 8.5 to 10 us (its target 0.8, its copies 3.8,
 // sums and their joining 1.1, a cluster's 1.5, the loss 0.7, the gradient 2.1), three or four
-// blocks are on an SM: 0.84 to 0.90 of the measured copy peak for rows over 32000 bf16 (8192 x
-// 50001, half of the rows counting, 214 us; the two kernels of one pass each 274; all counting 302
-// and 393). What took it there from 0.49 is four packs a thread side by side, in straight lines.
+// blocks are on an SM. Of the measured copy peak, with half of the rows counting and with all:
+// 8192 x 32000 bf16 0.90 and 0.87 (130, 178 us), 8192 x 50001 0.84 and 0.80 (215, 302 us; the two
+// kernels of one pass each 274 and 393), 8192 x 50257 float32 0.88 and 0.87. What took it there from 0.49 is four packs a thread side by side, in straight lines.
 constexpr int kLossThreads = 256;
 template <typename T, int KIND, bool CLUSTER>
 __global__ void __launch_bounds__(kLossThreads, 4) vrRowLossGrads(const __grid_constant__ LossArgs a) {
@@ -791,9 +791,9 @@ vrResult_t rowGrads(LossArgs& a, cudaStream_t st) {
 }
 
 // Logarithms and gradient in one pass; false if a row is too large for a cluster. Parts of up to
-// 72 KB and 256 threads, four blocks an SM by their registers (50001 bf16, all rows counting, 315
-// us; parts of 36 KB and 128 threads 327, of 52 KB and 192 threads 336; 50257 float32 300, 330,
-// 314).
+// 72 KB and 256 threads, four blocks an SM by their registers (8192 x 50001 bf16, all rows counting,
+// 315 us before the pairs of floats; parts of 36 KB and 128 threads 327, of 52 KB and 192 threads
+// 336; 4096 x 50257 float32 300, 330, 314).
 constexpr size_t kMostShared = 200 * 1024;
 template <typename T, int KIND>
 bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
@@ -805,7 +805,7 @@ bool rowLossGrads(LossArgs& a, cudaStream_t st, vrResult_t* r) {
   // Few rows are spread over more SMs, in parts of 8 KB at least, up to six blocks on each.
   while (ctas < 8 && a.rows * ctas * 2 <= 6 * kSMs && packs / ctas >= 1024) ctas *= 2;
   const uint64_t part = (packs + ctas - 1) / ctas;
-  // 16 packs a thread, so that many rows are on their way at a time (16384 x 8000 bf16 93 us, of 8
+  // 16 packs a thread, so that many rows are on their way at a time (16384 x 8000 bf16, all counting, 93 us, of 8
   // packs 98, of 4 142; of 32 133); 4 where there are few.
   const uint64_t each = a.rows * ctas > 6 * kSMs ? 16 : 4;
   uint64_t threads = (part / each + 31) / 32 * 32;

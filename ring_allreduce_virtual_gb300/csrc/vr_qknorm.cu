@@ -253,8 +253,8 @@ __device__ __forceinline__ T* place(const Side& s, const Token& k, uint32_t head
 // Bound by HBM where heads fill the lanes: 4 x 4096 tokens of 32 + 8 heads of 128 bf16
 // backward 84 us, 0.90 of the measured copy peak (with one chain in twice the warps 0.65, 12
 // warps of 168 registers 0.49: they spill; float32 does not, 0.93 against 0.89), 64 + 8 forward
-// 107 us, 0.85 (0.74 with one chain). Heads of 80 use 5 of 8 lanes: 16 + 16 float16 neighbours
-// 0.59 and 0.47, bound by what a scheduler's two warps issue (0.44 instructions a cycle).
+// 107 us, 0.85 (0.74 with one chain). Heads of 80 use 5 of 8 lanes: 4 x 4096 tokens of 16 + 16
+// float16 neighbours 0.63 forward and 0.50 backward, bound by what a scheduler's two warps issue (0.44 instructions a cycle).
 constexpr int kStages = 3, kAtOnce = 2;
 template <bool BACK>
 constexpr int kBlocks = BACK ? 1 : 2;  // on an SM: 255 (168) registers a thread, or 128
@@ -508,8 +508,11 @@ __global__ void __launch_bounds__(32 * kHeadWarps<T, BACK>, kBlocks<BACK>) vrQkH
   }
 }
 
-// Heads of any width, strides and alignment: a warp for each head, walks over it in
-// single elements. Pair i is elements (2 i, 2 i + 1) or (i, i + rot / 2); the elements
+// Heads of any width, strides and alignment, and those whose rotated half is no whole packs: a warp
+// for each head walks over it in single elements, twice, and loads positions and angles for each
+// head: bound by its instructions. 4 x 4096 tokens of 16 + 16 bf16 heads of 80, of which 40 are
+// rotated, 251 us forward and 750 backward, 0.10 and 0.05 of the measured copy peak (with 32
+// rotated, whole packs, 39 and 76); of 96 with 24 rotated 246 and 735. Pair i is elements (2 i, 2 i + 1) or (i, i + rot / 2); the elements
 // past the rotated part are taken as pairs that are not turned, with their like.
 template <typename T>
 struct Pairs {
